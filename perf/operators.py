@@ -202,6 +202,16 @@ def _cache(g, pages, page, heads, D, dtype, heads_first):
     return (values.transpose(1, 2) if heads_first else values), scale
 
 
+def _caches(g, s, pages):
+    """One layer's key and value caches, and the library's handle of them."""
+    case = s["case"]
+    for name in ("k", "v"):
+        s[name + "_cache"], s[name + "_scale"] = _cache(g, pages, case["page"], case["hkv"], case["D"], case["cache"],
+                                                        case["heads_first"])
+    if own:
+        s["cache"] = _binding().KvCache(s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"])
+
+
 def _tables(g, counts, page, spare=1):
     """Block table [R, most] of requests with ``counts`` tokens: pages in random order, -1 past a request's last."""
     need = [-(-c // page) for c in counts]
@@ -253,8 +263,7 @@ def _prepare_append(case, g):
         freq = 10000.0 ** (-torch.arange(half, device="cuda", dtype=torch.float64) / half)
         ang = torch.arange(max(old) + new, device="cuda", dtype=torch.float64)[:, None] * freq
         s["cos_sin"] = torch.cat([ang.cos(), ang.sin()], dim=1).float()
-    s["k_cache"], s["k_scale"] = _cache(g, pages, case["page"], hkv, D, case["cache"], case["heads_first"])
-    s["v_cache"], s["v_scale"] = _cache(g, pages, case["page"], hkv, D, case["cache"], case["heads_first"])
+    _caches(g, s, pages)
     return s
 
 
@@ -265,8 +274,7 @@ def _prepare_attn(case, g):
     s = {"case": case, "seq_lens": seq, "block_table": table, "scale": D ** -0.5}
     s["q"] = (1.5 * g.normal(B, hq, D)).to(_DT[case["q"]])
     s["out"] = torch.empty_like(s["q"])
-    s["k_cache"], s["k_scale"] = _cache(g, pages, case["page"], hkv, D, case["cache"], case["heads_first"])
-    s["v_cache"], s["v_scale"] = _cache(g, pages, case["page"], hkv, D, case["cache"], case["heads_first"])
+    _caches(g, s, pages)
     if own:
         s["ws"] = _binding().new_attn_workspace(B, hq, hkv, D)
     return s
@@ -310,17 +318,15 @@ def _own_norm(s):
 
 
 def _own_append(s):
-    _binding().moe_kv_append(s["k"], s["v"], s["k_cache"], s["v_cache"], s["block_table"], s["positions"],
-                             req=s["req"], cos_sin=s["cos_sin"], q=s["q"], q_out=s["q_out"], k_scale=s["k_scale"],
-                             v_scale=s["v_scale"])
+    _binding().moe_kv_append(s["k"], s["v"], s["cache"], s["block_table"], s["positions"], req=s["req"],
+                             cos_sin=s["cos_sin"], q=s["q"], q_out=s["q_out"])
     return {"q": s["q_out"], "k": s["k_cache"], "v": s["v_cache"]}
 
 
 def _own_attn(s):
     c = s["case"]
-    _binding().moe_attn_decode(s["q"], s["k_cache"], s["v_cache"], s["block_table"], s["seq_lens"], s["scale"],
-                               s["out"], s["ws"], window=c["window"], softcap=c["softcap"], k_scale=s["k_scale"],
-                               v_scale=s["v_scale"])
+    _binding().moe_attn_decode(s["q"], s["cache"], s["block_table"], s["seq_lens"], s["scale"], s["out"], s["ws"],
+                               window=c["window"], softcap=c["softcap"])
     return s["out"]
 
 
