@@ -1,7 +1,7 @@
 """ctypes binding of ``libmoe_gb300.so``: argument marshalling only.
 
 Every function has the name of the C entry point it calls (see
-``include/moe_decode.h``).  Tensors are passed as device pointers, sizes are
+``include/moe_decode.h`` and ``include/moe_block.h``).  Tensors are passed as device pointers, sizes are
 read from their shapes, and the stream is torch's current CUDA stream.  No
 step of the layer runs here; a missing library raises instead of falling back.
 """
@@ -33,6 +33,15 @@ WS_FIELDS = ("total", "status", "counts", "logits", "exp_count", "exp_off", "asg
 
 class WsLayout(C.Structure):
     _fields_ = [(f, C.c_size_t) for f in WS_FIELDS]
+
+
+class KvCacheArgs(C.Structure):
+    """``moe_kv_cache`` of ``include/moe_block.h``."""
+
+    _fields_ = ([(f, C.c_void_p) for f in ("k", "v", "k_scale", "v_scale")]
+                + [(f, C.c_int64) for f in ("k_page_stride", "k_slot_stride", "k_head_stride",
+                                            "v_page_stride", "v_slot_stride", "v_head_stride")]
+                + [(f, C.c_int) for f in ("dtype", "num_pages", "page_size", "heads", "head_dim")])
 
 
 class MoeError(RuntimeError):
@@ -83,6 +92,15 @@ _SIGS = {
                                _P, _P, _P, _P, _SZ, _P, _P, _P, _P]),
     "deamoe_layer_forward": (_I, [_P, _I, _I, _I, _I, _F, _P, _P, _I, _I, _I, _I, _P, _P,
                                   _P, _P, _P, _P, _I, _P, _P, _P, _P, _SZ, _P, _P, _P, _P]),
+    "moe_rmsnorm": (_I, [_P, _I, _I64, _P, _I, _I64, _P, _I64, _P, _I, _F, _I, _I, _P, _I, _I64, _P, _I, _P]),
+    "moe_kv_append": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _I64, _I, _I, _P, _P,
+                           _P, _I, _I, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _P]),
+    "moe_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_attn_decode": (_I, [_P, _I, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _I64, _I, _P, _F, _I, _F, _P,
+                             _I, _I64, _I64, _P, _P, _SZ, _P]),
+    "moe_lora_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_lora_project": (_I, [_P, _I, _I64, _P, _I, _I, _P, _I, _I64, _P, _I, _P, _P, _P, _I, _I, _P, _P, _I, _I64,
+                              _P, _SZ, _P]),
     "moe_unique_weight_bytes_vanilla": (_I64, [_I, _I, _I, _I, _I, _I]),
     "moe_unique_weight_bytes_deamoe": (_I64, [_I, _I, _I, _I, _I, _I, _I, _I]),
 }
@@ -414,3 +432,209 @@ def moe_unique_weight_bytes_vanilla(d, n, I, I_s, dtype_code, A_e) -> int:
 
 def moe_unique_weight_bytes_deamoe(d, n, I_sh, I_pr, I_s, dtype_code, A_d, A_e) -> int:
     return int(lib().moe_unique_weight_bytes_deamoe(d, n, I_sh, I_pr, I_s, dtype_code, A_d, A_e))
+
+
+# ------------------------------------------------------- decode block
+# Sizes are read from the shapes, strides from the tensors: rows (the last
+# dimension) must be contiguous, everything else may be a view.
+
+
+_CODES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
+
+
+def _code(t, name: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _rows(t, name: str, dim: int) -> int:
+    """Device pointer of a CUDA tensor of ``dim`` dimensions whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name}: expected {dim} dimensions, got shape {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    return t.data_ptr()
+
+
+def _ld(t) -> int:
+    """Stride between the rows of a matrix (a single row's stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _want(t, name: str, shape, dtype):
+    """Device pointer of a contiguous CUDA tensor of this shape and type (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def moe_rmsnorm(x, weight, eps: float, y, residual=None, residual_out=None, y_scale=None):
+    """``y = rms_norm(x + residual) * weight`` over the rows of x [T, d].
+
+    ``residual_out`` gets x + residual (it may be ``residual`` itself);
+    ``weight`` [d] or None; ``y_scale`` goes with an E4M3 ``y``: float32 [T]
+    (a scale per row) or [T, d / 128] (per 128 columns)."""
+    T, d = x.shape
+    if y.shape != x.shape or (weight is not None and tuple(weight.shape) != (d,)):
+        raise ValueError("x and y must both be [T, d], weight [d]")
+    r_code = r_ld = ro_ld = 0
+    r_ptr = ro_ptr = None
+    if residual is not None:
+        r_code, r_ld, r_ptr = _code(residual, "residual"), _ld(residual), _rows(residual, "residual", 2)
+    if residual_out is not None:
+        code, ro_ld, ro_ptr = _code(residual_out, "residual_out"), _ld(residual_out), _rows(residual_out, "residual_out", 2)
+        if residual is not None and code != r_code:
+            raise ValueError("residual and residual_out must have one dtype")
+        r_code = code
+    for t in (residual, residual_out):
+        if t is not None and t.shape != x.shape:
+            raise ValueError("residual and residual_out must be [T, d]")
+    group = 0
+    if y_scale is not None and y_scale.dim() == 2:
+        group = 128
+        _want(y_scale, "y_scale", (T, d // 128), torch.float32)
+    else:
+        _want(y_scale, "y_scale", (T,), torch.float32)
+    rc = lib().moe_rmsnorm(
+        _rows(x, "x", 2), _code(x, "x"), _ld(x), r_ptr, r_code, r_ld, ro_ptr, ro_ld, _ptr(weight),
+        _code(weight, "weight") if weight is not None else 0, eps, T, d, _rows(y, "y", 2), _code(y, "y"), _ld(y),
+        _ptr(y_scale), group, _stream())
+    if rc:
+        _check("moe_rmsnorm", rc)
+
+
+class KvCache:
+    """One layer's paged cache as the calls take it: ``k`` and ``v`` viewed as
+    [pages, page_size, heads, D], BF16, or E4M3 with ``k_scale`` and ``v_scale``
+    float32 [heads].  Any layout with contiguous rows will do (pages of
+    [heads, page_size, D]: pass ``cache.transpose(1, 2)``).  Holds its tensors."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must have one shape and dtype")
+        pages, page, heads, D = k.shape
+        self.tensors = (k, v, k_scale, v_scale)
+        self.heads, self.head_dim, self.page_size = heads, D, page
+        self.args = KvCacheArgs(
+            _rows(k, "k", 4), _rows(v, "v", 4), _want(k_scale, "k_scale", (heads,), torch.float32),
+            _want(v_scale, "v_scale", (heads,), torch.float32), *k.stride()[:3], *v.stride()[:3], _code(k, "k"),
+            pages, page, heads, D)
+        self.ref = C.byref(self.args)
+
+
+def moe_kv_append(k, v, cache: KvCache, block_table, positions, req=None, cos_sin=None, q=None, q_out=None,
+                  status=None):
+    """Rotate q and k [T, heads, D] by their positions and write k, v into the cache.
+
+    ``block_table`` int32 [R, pages]; ``positions`` int32 [T]; ``req`` int32 [T]
+    or None (token t is request t); ``cos_sin`` float32 [positions, rot] or
+    None; ``q_out`` may be ``q``; ``status`` int32 [1] or None."""
+    T = k.shape[0]
+    code = _code(k, "k")
+    if k.shape != (T, cache.heads, cache.head_dim) or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must both be [T, heads, D] of the cache, of one dtype")
+    q_args = (None, 0, 0, None, 0, 0, 0)
+    if q is not None:
+        if q_out is None or q.shape != q_out.shape or q.dim() != 3 or q.shape[::2] != k.shape[::2] \
+                or q.dtype != k.dtype or q_out.dtype != k.dtype:
+            raise ValueError("q and q_out must both be [T, q_heads, D] of k's dtype")
+        q_args = (_rows(q, "q", 3), q.stride(0), q.stride(1), _rows(q_out, "q_out", 3), q_out.stride(0),
+                  q_out.stride(1), q.shape[1])
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    R, pages = block_table.shape
+    if block_table.dtype != torch.int32:
+        raise ValueError("block_table must be int32 [R, pages]")
+    rc = lib().moe_kv_append(
+        _rows(k, "k", 3), k.stride(0), k.stride(1), _rows(v, "v", 3), v.stride(0), v.stride(1), code, T, cache.ref,
+        _rows(block_table, "block_table", 2), _ld(block_table), R, pages,
+        _want(positions, "positions", (T,), torch.int32), _want(req, "req", (T,), torch.int32),
+        _want(cos_sin, "cos_sin", (max_pos, rot), torch.float32), rot, max_pos, *q_args,
+        _want(status, "status", (1,), torch.int32), _stream())
+    if rc:
+        _check("moe_kv_append", rc)
+
+
+def moe_attn_workspace_bytes(B: int, q_heads: int, heads: int, head_dim: int) -> int:
+    b = lib().moe_attn_workspace_bytes(B, q_heads, heads, head_dim)
+    if b == 0:
+        raise MoeError("moe_attn_workspace_bytes", -1, "invalid sizes")
+    return b
+
+
+def new_attn_workspace(B: int, q_heads: int, heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """Allocate (torch) and zero (library kernel) a workspace of moe_attn_decode."""
+    ws = torch.empty(moe_attn_workspace_bytes(B, q_heads, heads, head_dim), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws)
+    return ws
+
+
+def moe_attn_decode(q, cache: KvCache, block_table, seq_lens, scale: float, out, ws, window: int = 0,
+                    softcap: float = 0.0, lse=None):
+    """Attention of one new token per request: q, out [B, q_heads, D],
+    ``block_table`` int32 [B, pages], ``seq_lens`` int32 [B] (the new token
+    included), ``lse`` float32 [B, q_heads] or None."""
+    B, hq, D = q.shape
+    if D != cache.head_dim or out.shape != q.shape:
+        raise ValueError("q and out must both be [B, q_heads, D] of the cache's D")
+    if block_table.dtype != torch.int32 or block_table.shape[0] != B:
+        raise ValueError("block_table must be int32 [B, pages]")
+    pages = block_table.shape[1]
+    rc = lib().moe_attn_decode(
+        _rows(q, "q", 3), _code(q, "q"), q.stride(0), q.stride(1), B, hq, cache.ref,
+        _rows(block_table, "block_table", 2), _ld(block_table), pages,
+        _want(seq_lens, "seq_lens", (B,), torch.int32), scale, window, softcap, _rows(out, "out", 3),
+        _code(out, "out"), out.stride(0), out.stride(1), _want(lse, "lse", (B, hq), torch.float32), _ptr(ws),
+        ws.numel(), _stream())
+    if rc:
+        _check("moe_attn_decode", rc)
+
+
+def moe_lora_workspace_bytes(T: int, d: int, r: int) -> int:
+    b = lib().moe_lora_workspace_bytes(T, d, r)
+    if b == 0:
+        raise MoeError("moe_lora_workspace_bytes", -1, "invalid sizes")
+    return b
+
+
+def new_lora_workspace(T: int, d: int, r: int = 0, device="cuda") -> torch.Tensor:
+    """Allocate (torch) and zero (library kernel) a workspace of moe_lora_project."""
+    ws = torch.empty(moe_lora_workspace_bytes(T, d, r), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws)
+    return ws
+
+
+def moe_lora_project(x, w, y, ws, lora=None, adapter=None, x_scale=None, w_scale=None):
+    """``y[t] = w x[t]`` plus, with ``lora`` = (A [n, r, d], B [n, N, r], scale
+    [n]), ``scale[a] B[a] (A[a] x[t])`` for a = ``adapter[t]`` >= 0 (int32 [T]).
+
+    x [T, d] float32 or bfloat16 with bfloat16 w [N, d]; or both E4M3 with
+    ``x_scale`` float32 [T] and ``w_scale`` float32 [N]."""
+    T, d = x.shape
+    N = w.shape[0]
+    if w.shape[1] != d or y.shape != (T, N):
+        raise ValueError("x must be [T, d], w [N, d], y [T, N]")
+    la = lb = ls = ad = None
+    n = r = 0
+    if lora is not None:
+        n, r, _ = lora[0].shape
+        la = _want(lora[0], "lora A", (n, r, d), torch.bfloat16)
+        lb = _want(lora[1], "lora B", (n, N, r), torch.bfloat16)
+        ls = _want(lora[2], "lora scale", (n,), torch.float32)
+        ad = _want(adapter, "adapter", (T,), torch.int32)
+    elif adapter is not None:
+        raise ValueError("adapter without lora")
+    rc = lib().moe_lora_project(
+        _rows(x, "x", 2), _code(x, "x"), _ld(x), _want(x_scale, "x_scale", (T,), torch.float32),
+        T, d, _rows(w, "w", 2), _code(w, "w"), _ld(w),
+        _want(w_scale, "w_scale", (N,), torch.float32), N, la, lb, ls, n, r, ad, _rows(y, "y", 2), _code(y, "y"),
+        _ld(y), _ptr(ws), ws.numel(), _stream())
+    if rc:
+        _check("moe_lora_project", rc)

@@ -330,6 +330,16 @@ int run_ffn(moe::FfnArgs& a, int T, int n, int k, int g, int has_shared, bool tc
 }  // namespace
 
 namespace moe {
+int api_fail(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    std::vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return code;
+}
+
 int device_sm_count() {
     static int cache[64] = {};
     int dev = 0;

@@ -1,0 +1,144 @@
+// Arguments and launchers of the decode-block operators (norm, cache append,
+// paged attention, adapter projection); internal to the library.
+#pragma once
+
+#include "../../include/moe_block.h"
+#include "kernels.h"
+
+namespace moe {
+
+// Records the message of a failed call (moe_last_error) and returns `code`.
+int api_fail(int code, const char* fmt, ...);
+
+struct NormArgs {
+    const void* x;
+    const void* residual;      // null: none
+    void* residual_out;        // null: not written
+    const void* weight;        // null: ones
+    void* y;
+    float* y_scale;            // E4M3 output
+    long long x_ld, r_ld, ro_ld, y_ld;
+    int x_dt, r_dt, w_dt, y_dt;
+    int T, d, group;
+    float eps;
+};
+cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t s);
+
+struct AppendArgs {
+    const void* k;
+    const void* v;
+    const void* q;             // null: none
+    void* q_out;
+    long long k_ts, k_hs, v_ts, v_hs, q_ts, q_hs, o_ts, o_hs;
+    int in_dt, T, q_heads;
+    moe_kv_cache c;
+    const int32_t* table;
+    long long table_ld;
+    int R, max_pages;
+    const int32_t* positions;
+    const int32_t* req;        // null: token t is request t
+    const float* cos_sin;
+    int rot, max_pos;
+    int32_t* status;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
+
+struct AttnArgs {
+    const void* q;
+    void* out;
+    float* lse;
+    long long q_bs, q_hs, o_bs, o_hs;
+    int q_dt, o_dt, B, q_heads, group;   // group = q_heads / c.heads
+    moe_kv_cache c;
+    const int32_t* table;
+    long long table_ld;
+    int max_pages;
+    const int32_t* seq_lens;
+    float scale, softcap;
+    int window;
+    int32_t* status;
+    uint32_t* done;            // counters, one per unit (zero between calls)
+    float* parts;              // partial results
+};
+size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t* done_off, size_t* parts_off);
+cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
+
+struct LoraArgs {
+    const void* x;
+    const float* x_scale;
+    const void* w;
+    const float* w_scale;
+    const __nv_bfloat16* la;   // null: no adapters
+    const __nv_bfloat16* lb;
+    const float* ls;
+    const int32_t* adapter;
+    void* y;
+    long long x_ld, w_ld, y_ld;
+    int x_dt, y_dt, T, d, N, na, r;
+    int32_t* status;
+    float* v;                  // [T, r]: A_a x[t], unscaled
+    __nv_bfloat16* xs;         // [3, T, d]: bf16 terms of fp32 x
+};
+constexpr int kLoraMaxT = 128;
+constexpr int kLoraMaxRank = 128;
+size_t lora_workspace_bytes(int T, int d, int r, size_t* v_off, size_t* xs_off);
+cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s);
+
+// Launch configuration of a programmatic dependent: the kernel may start
+// before the one ahead of it on the stream has ended, and waits for it
+// (griddepcontrol.wait) before it reads anything that one may have written.
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// ---- element loads and stores of a run-time type (uniform branches) ----------
+
+// 8 consecutive elements as fp32; p + i is aligned to 8 elements (at most 16 bytes).
+__device__ __forceinline__ void load8_f32(const void* p, int dt, long long i, float (&f)[8]) {
+    if (dt == MOE_DTYPE_BF16) {
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i), f);
+    } else {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 a = q[0], b = q[1];
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store8(void* p, int dt, long long i, const float (&f)[8]) {
+    if (dt == MOE_DTYPE_BF16) {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
+    } else {
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        q[0] = make_float4(f[0], f[1], f[2], f[3]);
+        q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+// Values outside E4M3's range go to +-448.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace moe
