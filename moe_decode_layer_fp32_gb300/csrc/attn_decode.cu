@@ -1,6 +1,25 @@
-// Attention of one new token per request over the paged cache: a block per
-// (request, query head), its warps striding over the keys with a running
-// maximum and sum each, joined in shared memory at the end.
+// Attention of one new token per request over the paged cache.
+//
+// Mathematics.  For a head with scores s_j and values v_j a part of the keys is
+// summed up by (m, l, o): m = max s_j, l = sum e^(s_j - m), o = sum e^(s_j - m) v_j;
+// two parts join as m = max(m1, m2), l = l1 e^(m1 - m) + l2 e^(m2 - m), o alike, and
+// the result is o / l.  Scores are kept in base 2 (s log2 e), so that every
+// exponential is one exp2.
+//
+// Split.  The cache is read once and there are 4 to 16 multiply-adds per value
+// read: memory bounds it, so the keys of all (request, key-value head) units are
+// laid end to end in tiles, every CTA takes an equal run of them whatever the
+// requests' lengths, and the parts of a unit that several CTAs share go through
+// the workspace: the CTA that finishes last joins them in the order of the keys.
+//
+// In a CTA every warp works alone on its own keys of a tile (its own cp.async ring,
+// running maximum and sum); the warps join only where a unit ends.  All query heads
+// of a key-value head share its rows: they are the rows of the 16-row MMA tile.
+// With up to 8 heads the other 8 rows hold the second term of each value: q (when
+// fp32) and the weights p enter as sums of two or three terms of the cache's
+// 16-bit type, which keeps them to 16 bits and more at no cost in MMAs.
+#include <algorithm>
+
 #include <math_constants.h>
 
 #include "block.h"
@@ -9,96 +28,735 @@ namespace moe {
 
 namespace {
 
-constexpr int kAttnWarps = 8;
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kAttnCtasPerSm = 2;
+constexpr int kAttnMaxCtas = 320;          // bounds the workspace
+constexpr int kAttnStages = 3;
+constexpr int kMergeFloats = 4096;         // shared merge buffer, 16 KB
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float cache_elem(const void* p, int dt, long long i) {
-    if (dt == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    return unpack_e4m3x2(static_cast<const uint8_t*>(p)[i]).x;
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 bytes, or zeros where size is 0 (src is then not read).
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// bf16 parts by truncation: p = hi + rest exactly, rest of p's sign.
+__device__ __forceinline__ float bf16_trunc(float p) { return __uint_as_float(__float_as_uint(p) & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_hi(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
 
-__global__ void __launch_bounds__(kAttnWarps * 32) attn_kernel(const __grid_constant__ AttnArgs a) {
-    pdl_allow_dependents();
-    pdl_wait_primary();
-    const int b = blockIdx.x, h = blockIdx.y, g = h / a.group;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int D = a.c.head_dim, P = a.c.page_size;
-    int n = max(a.seq_lens[b], 0);
-    if ((long long)n > (long long)a.max_pages * P) {
-        n = a.max_pages * P;
-        if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE);
+// Where a CTA (or one of its warps) stands in the run of tiles.
+struct Cursor {
+    int b, unit, tile, tiles, first, n;
+    long long left;                        // tiles of this CTA from here on
+};
+
+// DP: head_dim rounded up to 64, 128 or 256.  F8: E4M3 cache.  ROWS: query heads of a
+// unit, 8 or 16.  EX: fp32 queries or output, whose terms keep 22 bits or more.
+template <int DP, bool F8, int ROWS, bool EX>
+struct Attn {
+    static constexpr int kElem = F8 ? 1 : 2;
+    static constexpr int kPitch = DP * kElem;                        // bytes of a row in shared memory
+    static constexpr int KT = kPitch <= 128 ? 32 : 16;               // keys of a warp's tile
+    static constexpr int kTileBytes = KT * kPitch;                   // K or V
+    static constexpr int kTileKeys = KT * kAttnWarps;
+    static constexpr int kChunks = kPitch / 16;                      // 16-byte chunks of a row
+    static constexpr int kRowsPerIter = 32 / kChunks;
+    static constexpr int kQTerms = EX ? (F8 ? 2 : 3) : 1;
+    static constexpr int kPTerms = EX && !F8 ? 3 : 2;
+    static constexpr int kSteps = DP / 16;                           // k16 steps of q . k
+    static constexpr int kVElems = F8 ? (DP >= 128 ? 16 : 8) : 8;    // columns a thread takes of a V row at once
+    static constexpr int kWindows = DP / (8 * kVElems);
+    static constexpr int kAccs = DP / 8;                             // n8 tiles of o
+    // p in f16 is scaled to use its range: 2^15 at the maximum
+    static constexpr float kPShift = F8 ? 15.0f : 0.0f;
+    static constexpr size_t kRing = (size_t)kAttnWarps * kAttnStages * 2 * kTileBytes;
+    static constexpr size_t kSmem = kRing + kMergeFloats * 4;
+    static constexpr int kPartFloats = ROWS * (DP + 2);
+    static_assert(ROWS == 8 || (ROWS == 16 && !EX), "16 heads only without extra terms");
+
+    // Byte offset of chunk `ch` of row `r` in a K or V tile; the chunks of a
+    // 128-byte line are permuted so that the readers below (8 rows x 4 chunks of K, 4
+    // rows of one parity x 2 chunks of V) hit distinct banks.
+    __device__ static __forceinline__ uint32_t at_k(int r, int ch) {
+        if constexpr (kPitch == 64) return (r >> 1) * 128 + ((((r & 1) * 4 + ch) ^ (2 * ((r >> 1) & 3))) << 4);
+        return r * kPitch + ((ch ^ ((r & 1) << 2)) << 4);
     }
-    const int first = a.window > 0 ? max(0, n - a.window) : 0;
-    float q[8], o[8];
-    const float ks = a.c.k_scale ? a.c.k_scale[g] : 1.0f, vs = a.c.v_scale ? a.c.v_scale[g] : 1.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int c = e * 32 + lane;
-        q[e] = o[e] = 0.0f;
-        if (c < D) {
-            const long long i = b * a.q_bs + h * a.q_hs + c;
-            q[e] = a.q_dt == MOE_DTYPE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[i])
-                                            : static_cast<const float*>(a.q)[i];
-        }
+    __device__ static __forceinline__ uint32_t at_v(int r, int ch) {
+        if constexpr (kPitch == 64) return at_k(r, ch);
+        return r * kPitch + ((ch ^ (r & 6)) << 4);
     }
-    float m = -CUDART_INF_F, l = 0.0f;
-    for (int j = first + warp; j < n; j += kAttnWarps) {
-        const int page = a.table[b * a.table_ld + j / P];
+
+    __device__ static __forceinline__ void set_request(const AttnArgs& a, Cursor& c) {
+        int n = max(a.seq_lens[c.b], 0);
+        n = (int)min((long long)n, (long long)a.max_pages * a.c.page_size);
+        c.n = n;
+        c.first = a.window > 0 ? max(0, n - a.window) : 0;
+        c.tiles = (n - c.first + kTileKeys - 1) / kTileKeys;
+    }
+    // To the next tile of the run (left > 0 says whether there is one).
+    __device__ static __forceinline__ void advance(const AttnArgs& a, int units, Cursor& c) {
+        if (--c.left <= 0) return;
+        if (++c.tile < c.tiles) return;
+        c.tile = 0;
+        if (++c.unit < units) return;
+        c.unit = 0;
+        do {
+            ++c.b;
+            set_request(a, c);
+        } while (c.tiles == 0);
+    }
+    // Page of the key that lane `lane` looks after in the warp's tile, or -1.
+    __device__ static __forceinline__ int page_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
+        const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
+        if (c.left <= 0 || lane >= KT || key >= c.n) return -1;
+        const int page = a.table[c.b * a.table_ld + key / a.c.page_size];
         if (page < 0 || page >= a.c.num_pages) {
             set_status(a.status, MOE_ERR_DEVICE);
-            continue;
+            return -1;
         }
-        const long long kb = page * a.c.k_page_stride + (j % P) * a.c.k_slot_stride + g * a.c.k_head_stride;
-        const long long vb = page * a.c.v_page_stride + (j % P) * a.c.v_slot_stride + g * a.c.v_head_stride;
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e * 32 + lane < D) s = fmaf(q[e], cache_elem(a.c.k, a.c.dtype, kb + e * 32 + lane), s);
-        s = warp_sum(s) * ks * a.scale;
-        if (a.softcap > 0.0f) s = a.softcap * tanhf(s / a.softcap);
-        if (s == -CUDART_INF_F) continue;   // weighs nothing, also before the first finite score
-        const float mn = fmaxf(m, s), corr = m == mn ? 1.0f : expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * corr + p;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e * 32 + lane < D)
-                o[e] = o[e] * corr + p * cache_elem(a.c.v, a.c.dtype, vb + e * 32 + lane);
+        return page;
     }
-    __shared__ float s_m[kAttnWarps], s_l[kAttnWarps], s_o[kAttnWarps][256];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
+    // Start the copies of the warp's K and V rows of tile c into a stage; returns the
+    // mask of the keys that count.  The rows of the others become zeros.
+    __device__ static __forceinline__ uint32_t issue(const AttnArgs& a, const Cursor& c, int page, int nsub, int warp,
+                                                     int lane, uint32_t stage) {
+        const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
+        const int g = c.unit / nsub;
+        const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+        long long ko = 0, vo = 0;
+        if (page >= 0) {
+            const int slot = key % a.c.page_size;
+            ko = (page * a.c.k_page_stride + slot * a.c.k_slot_stride + g * a.c.k_head_stride) * kElem;
+            vo = (page * a.c.v_page_stride + slot * a.c.v_slot_stride + g * a.c.v_head_stride) * kElem;
+        }
+        const int ch = lane % kChunks, r0 = lane / kChunks;
+        const bool in = ch * 16 < a.c.head_dim * kElem;
+        const char* kb = static_cast<const char*>(a.c.k) + ch * 16;
+        const char* vb = static_cast<const char*>(a.c.v) + ch * 16;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s_o[warp][e * 32 + lane] = o[e];
+        for (int i = 0; i < KT / kRowsPerIter; ++i) {
+            const int r = i * kRowsPerIter + r0;
+            const long long o = __shfl_sync(0xffffffffu, ko, r), p = __shfl_sync(0xffffffffu, vo, r);
+            const uint32_t size = in && ((mask >> r) & 1u) ? 16u : 0u;
+            cp_async16_zfill(stage + at_k(r, ch), size ? kb + o : a.c.k, size);
+            cp_async16_zfill(stage + kTileBytes + at_v(r, ch), size ? vb + p : a.c.v, size);
+        }
+        return mask;
+    }
+
+    struct State {
+        uint32_t q[kQTerms][ROWS / 8][kSteps][2];   // terms of q: A fragments of the thread's row(s)
+        float qf[ROWS / 8];                         // factor of the accumulated score (base 2)
+        float m[ROWS / 8], l[ROWS / 8];
+        float o[kAccs][4];
+    };
+
+    __device__ static __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+        if constexpr (F8) mma_f16(c, a0, a1, a2, a3, b0, b1);
+        else mma_bf16(c, a0, a1, a2, a3, b0, b1);
+    }
+
+    // The unit's query rows: the thread holds rows lane / 4 (and + 8), elements
+    // 8 (lane % 4) + {0..7} of every 32 (bf16), 16 (lane % 4) + {0..15} of every 64 (E4M3): the order
+    // in which it reads K rows; a dot product does not mind the order.
+    __device__ static void load_q(const AttnArgs& a, const Cursor& c, int nsub, int lane, State& st) {
+        const int g = c.unit / nsub, sub = c.unit % nsub;
+        const float ks = a.c.k_scale ? a.c.k_scale[g] : 1.0f;
+        constexpr int E = F8 ? 16 : 8, J = DP / (4 * E);
+#pragma unroll
+        for (int rr = 0; rr < ROWS / 8; ++rr) {
+            const int row = sub * ROWS + rr * 8 + lane / 4;
+            const bool have = row < a.group;
+            const long long base = c.b * a.q_bs + (g * a.group + (have ? row : 0)) * a.q_hs;
+            float f[J][E];
+            float mx = 0.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int h = 0; h < E / 8; ++h) {
+                    const int d0 = j * 4 * E + (lane % 4) * E + h * 8;
+                    float v[8] = {};
+                    if (have && d0 < a.c.head_dim) load8_f32(a.q, a.q_dt, base + d0, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f[j][h * 8 + e] = v[e];
+                        mx = fmaxf(mx, fabsf(v[e]));
+                    }
+                }
+            float back = 1.0f;
+            if constexpr (F8) {
+                // f16 terms: the row is scaled by a power of two to at most 2^8
+                __syncwarp();
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                int e = 0;
+                if (mx > 0.0f && mx < CUDART_INF_F) frexpf(mx, &e);
+                e = min(max(8 - e, -100), 100);
+                const float up = ldexpf(1.0f, e);
+                back = ldexpf(1.0f, -e);
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) f[j][i] *= up;
+            }
+            st.qf[rr] = a.scale * ks * back;
+#pragma unroll
+            for (int t = 0; t < kQTerms; ++t)
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const int j = s / (E / 4), i = (s % (E / 4)) * 4;
+                    uint32_t w[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float &u = f[j][i + 2 * h], &v = f[j][i + 2 * h + 1];
+                        if constexpr (F8) {
+                            w[h] = pack_f16x2(u, v);
+                            const float2 r = unpack_f16x2(w[h]);
+                            u -= r.x;
+                            v -= r.y;
+                        } else {
+                            w[h] = pack_hi(u, v);
+                            u -= bf16_trunc(u);
+                            v -= bf16_trunc(v);
+                        }
+                    }
+                    st.q[t][rr][s][0] = w[0];
+                    st.q[t][rr][s][1] = w[1];
+                }
+            st.m[rr] = -CUDART_INF_F;
+            st.l[rr] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAccs; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[i][e] = 0.0f;
+    }
+
+    // One tile: scores, running maximum, weights, o.
+    __device__ static __forceinline__ void tile(const AttnArgs& a, State& st, const char* stage, uint32_t mask, int lane) {
+        constexpr int NT = KT / 8;
+        const int col = lane % 4;
+        float s[NT][ROWS / 8][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // c: first terms (rows 0-7) and second terms or heads 8-15 (rows 8-15); c2: third terms
+            float c[4] = {}, c2[4] = {};
+            const int key = nt * 8 + lane / 4;
+#pragma unroll
+            for (int j = 0; j < kChunks / 4; ++j) {
+                const uint4 k4 = *reinterpret_cast<const uint4*>(stage + at_k(key, 4 * j + col));
+                const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+                constexpr int SJ = F8 ? 4 : 2;
+#pragma unroll
+                for (int i = 0; i < SJ; ++i) {
+                    const int step = j * SJ + i;
+                    uint32_t b0, b1;
+                    if constexpr (F8) {
+                        b0 = e4m3x2_to_f16x2(w[i]);
+                        b1 = e4m3x2_to_f16x2(w[i] >> 16);
+                    } else {
+                        b0 = w[2 * i];
+                        b1 = w[2 * i + 1];
+                    }
+                    const uint32_t* q0 = st.q[0][0][step];
+                    if constexpr (ROWS == 16) {
+                        const uint32_t* q1 = st.q[0][1][step];
+                        mma(c, q0[0], q1[0], q0[1], q1[1], b0, b1);
+                    } else if constexpr (kQTerms == 1) {
+                        mma(c, q0[0], 0u, q0[1], 0u, b0, b1);
+                    } else {
+                        const uint32_t* q1 = st.q[1][0][step];
+                        mma(c, q0[0], q1[0], q0[1], q1[1], b0, b1);
+                        if constexpr (kQTerms == 3) {
+                            const uint32_t* q2 = st.q[2][0][step];
+                            mma(c2, q2[0], 0u, q2[1], 0u, b0, b1);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                s[nt][0][e] = c[e];
+                if constexpr (ROWS == 16) s[nt][1][e] = c[2 + e];
+                // an infinite first term stands: the others' products with it may be NaN
+                else if (kQTerms > 1 && fabsf(c[e]) < CUDART_INF_F) s[nt][0][e] = c[e] + (c[2 + e] + c2[e]);
+            }
+        }
+        uint32_t pf[kPTerms][NT][ROWS / 8];   // weights as A fragments: keys 2 col, + 1 of each n8 tile
+#pragma unroll
+        for (int rr = 0; rr < ROWS / 8; ++rr) {
+            const float f = a.softcap > 0.0f ? st.qf[rr] / a.softcap : st.qf[rr] * kLog2e;
+            float mx = -CUDART_INF_F;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = s[nt][rr][e] * f;
+                    if (a.softcap > 0.0f) v = a.softcap * kLog2e * tanhf(v);
+                    if (!((mask >> (nt * 8 + 2 * col + e)) & 1u)) v = -CUDART_INF_F;
+                    s[nt][rr][e] = v;
+                    mx = fmaxf(mx, v);
+                }
+            __syncwarp();
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_new = fmaxf(st.m[rr], mx);
+            const float base = m_new == -CUDART_INF_F ? 0.0f : m_new;
+            const float corr = exp2f(st.m[rr] - base);
+            if (__any_sync(0xffffffffu, m_new != st.m[rr])) {
+                st.l[rr] *= corr;
+#pragma unroll
+                for (int i = 0; i < kAccs; ++i) {
+                    st.o[i][2 * rr] *= corr;
+                    st.o[i][2 * rr + 1] *= corr;
+                    if constexpr (ROWS == 8) {
+                        st.o[i][2] *= corr;
+                        st.o[i][3] *= corr;
+                    }
+                }
+            }
+            st.m[rr] = m_new;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p0 = exp2f(s[nt][rr][0] - base + kPShift), p1 = exp2f(s[nt][rr][1] - base + kPShift);
+                st.l[rr] += p0 + p1;
+#pragma unroll
+                for (int t = 0; t < kPTerms; ++t) {
+                    if constexpr (F8) {
+                        pf[t][nt][rr] = pack_f16x2(p0, p1);
+                        const float2 r = unpack_f16x2(pf[t][nt][rr]);
+                        p0 -= r.x;
+                        p1 -= r.y;
+                    } else if (!EX && t == 1) {
+                        pf[t][nt][rr] = pack_bf16x2(p0, p1);
+                    } else {
+                        pf[t][nt][rr] = pack_hi(p0, p1);
+                        p0 -= bf16_trunc(p0);
+                        p1 -= bf16_trunc(p1);
+                    }
+                }
+            }
+        }
+        // o += p v: the thread reads kVElems columns of its 4 keys of each 16 and pairs the
+        // keys of a column; column (8 w + n) kVElems + e is column n of MMA tile (w, e)
+        const char* vt = stage + kTileBytes;
+#pragma unroll
+        for (int w = 0; w < kWindows; ++w) {
+            float fresh[EX ? kVElems : 1][4];
+            if constexpr (EX) {
+#pragma unroll
+                for (int e = 0; e < kVElems; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) fresh[e][i] = 0.0f;
+            }
+#pragma unroll
+            for (int kg = 0; kg < KT / 16; ++kg) {
+                uint32_t v[4][4];   // keys 2 col, + 1, + 8, + 9
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kg * 16 + 2 * col + (i & 1) + (i >> 1) * 8;
+                    if constexpr (kVElems * kElem == 16) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(vt + at_v(key, 8 * w + lane / 4));
+                        v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(vt + at_v(key, lane / 8) + (lane / 4 % 2) * 8);
+                        v[i][0] = u.x; v[i][1] = u.y;
+                    }
+                }
+                const uint32_t (&p0)[ROWS / 8] = pf[0][2 * kg];
+                const uint32_t (&p0b)[ROWS / 8] = pf[0][2 * kg + 1];
+#pragma unroll
+                for (int e = 0; e < kVElems; ++e) {
+                    uint32_t b[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (F8) {
+                            const uint32_t x = __byte_perm(v[2 * h][e / 4], v[2 * h + 1][e / 4], (e & 2) ? 0x7362 : 0x5140);
+                            b[h] = e4m3x2_to_f16x2((e & 1) ? x >> 16 : x);
+                        } else {
+                            b[h] = __byte_perm(v[2 * h][e / 2], v[2 * h + 1][e / 2], (e & 1) ? 0x7632 : 0x5410);
+                        }
+                    }
+                    float (&acc)[4] = EX ? fresh[EX ? e : 0] : st.o[w * kVElems + e];
+                    if constexpr (ROWS == 16) {
+                        mma(acc, p0[0], p0[1], p0b[0], p0b[1], b[0], b[1]);
+                        if constexpr (kPTerms == 2)
+                            mma(acc, pf[1][2 * kg][0], pf[1][2 * kg][1], pf[1][2 * kg + 1][0], pf[1][2 * kg + 1][1], b[0], b[1]);
+                    } else if constexpr (kPTerms == 1) {
+                        mma(acc, p0[0], 0u, p0b[0], 0u, b[0], b[1]);
+                    } else {
+                        mma(acc, p0[0], pf[1][2 * kg][0], p0b[0], pf[1][2 * kg + 1][0], b[0], b[1]);
+                        if constexpr (kPTerms == 3)
+                            mma(acc, 0u, pf[2][2 * kg][0], 0u, pf[2][2 * kg + 1][0], b[0], b[1]);
+                    }
+                }
+            }
+            if constexpr (EX) {
+                // the tensor cores cut their sums to 24 bits instead of rounding: a tile's sum is
+                // added to o with a rounded fp32 addition, so that the cuts do not add up
+#pragma unroll
+                for (int e = 0; e < kVElems; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st.o[w * kVElems + e][i] += fresh[e][i];
+            }
+        }
+    }
+
+    struct Shared {
+        float m[kAttnWarps][ROWS], l[kAttnWarps][ROWS];
+        uint32_t mask[kAttnWarps][kAttnStages];
+        long long wsum[kAttnWarps];
+        int found_b, last;
+        long long found_pre;
+    };
+
+    // Result of a row: o / l, its value scale, and the log of the sum.
+    __device__ static __forceinline__ void finish(const AttnArgs& a, int b, int g, int sub, int row, int c4, float4 o,
+                                                  float m, float l) {
+        const int r = sub * ROWS + row;
+        if (r >= a.group || c4 * 4 >= a.c.head_dim) return;
+        const int h = g * a.group + r;
+        const float vs = a.c.v_scale ? a.c.v_scale[g] : 1.0f;
+        // l == 0: no key counted
+        const float inv = l == 0.0f ? 0.0f : vs / l;
+        const long long i = b * a.o_bs + h * a.o_hs + c4 * 4;
+        if (a.o_dt == MOE_DTYPE_BF16)
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + i) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        else
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + i) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (a.lse && c4 == 0)
+            a.lse[(long long)b * a.q_heads + h] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l) - kPShift) * kLn2;
+    }
+
+    __device__ static __forceinline__ void axpy4(float4& acc, float f, float4 v) {
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+    }
+    // 2^(m - top) for a part's maximum (0 for a part without keys)
+    __device__ static __forceinline__ float weight_of(float m, float top) {
+        return m == -CUDART_INF_F ? 0.0f : exp2f(m - top);
+    }
+
+    // Join the warps' parts of a unit: the whole unit goes to `out`, a part of one to `part`.
+    __device__ static void merge(const AttnArgs& a, const Cursor& c, int nsub, State& st, float* buf, Shared& sh, float* part) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        const int g = c.unit / nsub, sub = c.unit % nsub;
+#pragma unroll
+        for (int rr = 0; rr < ROWS / 8; ++rr) {
+            float l = st.l[rr];
+            __syncwarp();
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if (lane % 4 == 0) {
+                sh.m[warp][rr * 8 + lane / 4] = st.m[rr];
+                sh.l[warp][rr * 8 + lane / 4] = l;
+            }
+        }
+        // a round: kCols columns of all rows and warps in the buffer
+        constexpr int kCols = kMergeFloats / (kAttnWarps * ROWS) < DP ? kMergeFloats / (kAttnWarps * ROWS) : DP;
+        constexpr int kRoundWindow = 8 * kVElems;                 // columns of one window of accumulators
+        static_assert(kCols % kRoundWindow == 0 || kRoundWindow % kCols == 0, "rounds of whole windows");
+#pragma unroll
+        for (int c0 = 0; c0 < DP; c0 += kCols) {
+#pragma unroll
+            for (int w = 0; w < kWindows; ++w)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int colb = (8 * w + 2 * (lane % 4) + i) * kVElems;   // kVElems columns from here
+                    if (colb < c0 || colb >= c0 + kCols) continue;
+#pragma unroll
+                    for (int rr = 0; rr < ROWS / 8; ++rr)
+#pragma unroll
+                        for (int e = 0; e < kVElems; e += 4) {
+                            float v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float (&o)[4] = st.o[w * kVElems + e + k];
+                                v[k] = ROWS == 16 ? o[2 * rr + i] : o[i] + o[2 + i];
+                            }
+                            const int row = rr * 8 + lane / 4, f4 = (colb - c0 + e) / 4;
+                            reinterpret_cast<float4*>(buf)[(warp * ROWS + row) * (kCols / 4) + (f4 ^ (row & 7))] =
+                                make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                }
+            __syncthreads();
+            for (int it = tid; it < ROWS * (kCols / 4); it += kAttnThreads) {
+                const int row = it / (kCols / 4), f4 = it % (kCols / 4);
+                float top = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh.m[w][row]);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    const float f = weight_of(sh.m[w][row], top);
+                    // a NaN sum has no maximum: it stays NaN
+                    l = fmaf(sh.l[w][row] != sh.l[w][row] ? 1.0f : f, sh.l[w][row], l);
+                    axpy4(o, f, reinterpret_cast<const float4*>(buf)[(w * ROWS + row) * (kCols / 4) + (f4 ^ (row & 7))]);
+                }
+                const int c4 = c0 / 4 + f4;
+                if (part) {
+                    reinterpret_cast<float4*>(part)[row * (DP / 4) + c4] = o;
+                    if (c4 == 0) {
+                        part[ROWS * DP + row] = top;
+                        part[ROWS * DP + ROWS + row] = l;
+                    }
+                } else {
+                    finish(a, c.b, g, sub, row, c4, o, top, l);
+                }
+            }
+            __syncthreads();
+        }
+    }
+
+    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, long long c_first, long long c_last,
+                                bool tail_first) {
+        const int g = c.unit / nsub, sub = c.unit % nsub;
+        for (int it = threadIdx.x; it < ROWS * (DP / 4); it += kAttnThreads) {
+            const int row = it / (DP / 4), c4 = it % (DP / 4);
+            float top = -CUDART_INF_F, l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (long long k = c_first; k <= c_last; ++k) {
+                const float* p = a.parts + (2 * k + (k == c_first && tail_first ? 1 : 0)) * kPartFloats;
+                top = fmaxf(top, __ldcg(p + ROWS * DP + row));
+            }
+#pragma unroll 4
+            for (long long k = c_first; k <= c_last; ++k) {
+                const float* p = a.parts + (2 * k + (k == c_first && tail_first ? 1 : 0)) * kPartFloats;
+                const float pl = __ldcg(p + ROWS * DP + ROWS + row), f = weight_of(__ldcg(p + ROWS * DP + row), top);
+                l = fmaf(pl != pl ? 1.0f : f, pl, l);
+                axpy4(o, f, __ldcg(reinterpret_cast<const float4*>(p) + row * (DP / 4) + c4));
+            }
+            finish(a, c.b, g, sub, row, c4, o, top, l);
+        }
+    }
+};
+
+template <int DP, bool F8, int ROWS, bool EX>
+__global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) attn_kernel(const __grid_constant__ AttnArgs a) {
+    using K = Attn<DP, F8, ROWS, EX>;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ typename K::Shared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nsub = (a.group + ROWS - 1) / ROWS, units = a.c.heads * nsub;
+    pdl_allow_dependents();
+    pdl_wait_primary();
+
+    // ---- the run of this CTA: tiles [start, end) of the `total` of all requests
+    auto tiles_of = [&](int b) {
+        Cursor c;
+        c.b = b;
+        K::set_request(a, c);
+        return c.tiles;
+    };
+    long long mine = 0;
+    for (int b = tid; b < a.B; b += kAttnThreads) {
+        mine += tiles_of(b);
+        if (blockIdx.x == 0 && (long long)max(a.seq_lens[b], 0) > (long long)a.max_pages * a.c.page_size)
+            set_status(a.status, MOE_ERR_DEVICE);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sh.wsum[warp] = mine;
     __syncthreads();
-    float top = -CUDART_INF_F, sum = 0.0f, val = 0.0f;
-    for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w]);
-    const int c = threadIdx.x;
-    for (int w = 0; w < kAttnWarps; ++w) {
-        if (s_l[w] == 0.0f) continue;
-        const float f = expf(s_m[w] - top);
-        sum += f * s_l[w];
-        val += f * s_o[w][c];
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) total += sh.wsum[w];
+    total *= units;
+    // requests without keys
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (tiles_of(b) > 0) continue;
+        for (int it = tid; it < units * ROWS * (DP / 4); it += kAttnThreads) {
+            const int c4 = it % (DP / 4), row = it / (DP / 4) % ROWS, unit = it / (DP / 4) / ROWS;
+            K::finish(a, b, unit / nsub, unit % nsub, row, c4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
+        }
     }
-    if (c < D) {
-        const float r = sum == 0.0f ? 0.0f : val / sum * vs;
-        const long long i = b * a.o_bs + h * a.o_hs + c;
-        if (a.o_dt == MOE_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(r);
-        else static_cast<float*>(a.out)[i] = r;
+    const long long ctas = min((long long)gridDim.x, total);
+    if (blockIdx.x >= ctas) return;
+    const long long start = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
+    // request of tile `start`: scan the requests in blocks of the CTA's threads
+    long long before = 0;
+    for (int b0 = 0;; b0 += kAttnThreads) {
+        const int b = b0 + tid;
+        const long long t = b < a.B ? (long long)tiles_of(b) * units : 0;
+        long long incl = t;
+        __syncwarp();
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        __syncthreads();
+        if (lane == 31) sh.wsum[warp] = incl;
+        if (tid == 0) sh.found_b = -1;
+        __syncthreads();
+        long long pre = before + incl - t, all = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            if (w < warp) pre += sh.wsum[w];
+            all += sh.wsum[w];
+        }
+        if (start >= pre && start < pre + t) {
+            sh.found_b = b;
+            sh.found_pre = pre;
+        }
+        __syncthreads();
+        if (sh.found_b >= 0) break;
+        before += all;
     }
-    if (a.lse && c == 0) a.lse[(long long)b * a.q_heads + h] = sum == 0.0f ? -CUDART_INF_F : top + logf(sum);
+    Cursor c;
+    c.b = sh.found_b;
+    K::set_request(a, c);
+    c.unit = (int)((start - sh.found_pre) / c.tiles);
+    c.tile = (int)((start - sh.found_pre) % c.tiles);
+    c.left = end - start;
+
+    // ---- pipeline: `ahead` runs kAttnStages - 1 tiles in front of `c`
+    const uint32_t ring = smem_u32(smem) + warp * kAttnStages * 2 * K::kTileBytes;
+    const char* ring_p = smem + (size_t)warp * kAttnStages * 2 * K::kTileBytes;
+    float* buf = reinterpret_cast<float*>(smem + K::kRing);
+    Cursor ahead = c;
+    int page = K::page_of(a, ahead, warp, lane);
+    int stage_in = 0;
+    auto feed = [&]() {
+        if (ahead.left > 0) {
+            Cursor next = ahead;
+            K::advance(a, units, next);
+            const int page_next = K::page_of(a, next, warp, lane);
+            const uint32_t mask = K::issue(a, ahead, page, nsub, warp, lane, ring + stage_in * 2 * K::kTileBytes);
+            if (lane == 0) sh.mask[warp][stage_in] = mask;
+            stage_in = stage_in + 1 == kAttnStages ? 0 : stage_in + 1;
+            ahead = next;
+            page = page_next;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kAttnStages - 1; ++i) feed();
+
+    int stage_out = 0;
+    bool first_segment = true;
+    long long at = start;                       // linear position of c
+    while (c.left > 0) {
+        typename K::State st;
+        K::load_q(a, c, nsub, lane, st);
+        const Cursor seg = c;
+        const long long unit_begin = at - c.tile, unit_end = unit_begin + c.tiles;
+        const int count = (int)min(c.left, (long long)(c.tiles - c.tile));
+        for (int i = 0; i < count; ++i) {
+            cp_async_wait<kAttnStages - 2>();
+            __syncwarp();
+            const uint32_t mask = sh.mask[warp][stage_out];
+            feed();
+            // keys beyond the request (the tail of its last tile) count for nothing
+            if (mask) K::tile(a, st, ring_p + stage_out * 2 * K::kTileBytes, mask, lane);
+            stage_out = stage_out + 1 == kAttnStages ? 0 : stage_out + 1;
+            K::advance(a, units, c);
+        }
+        at += count;
+        const bool whole = seg.tile == 0 && count == seg.tiles;
+        float* part = whole ? nullptr : a.parts + (size_t)(2 * blockIdx.x + (first_segment ? 0 : 1)) * K::kPartFloats;
+        K::merge(a, seg, nsub, st, buf, sh, part);
+        if (!whole) {
+            // CTA of tile u: the largest k with k total / ctas <= u
+            const long long c_first = ((unit_begin + 1) * ctas - 1) / total, c_last = (unit_end * ctas - 1) / total;
+            uint32_t* done = a.done + (long long)seg.b * units + seg.unit;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const bool last = atomic_add_acq_rel_gpu(done, 1u) == (uint32_t)(c_last - c_first);
+                if (last) *done = 0u;
+                sh.last = last;
+            }
+            __syncthreads();
+            if (sh.last) {
+                __threadfence();
+                K::join(a, seg, nsub, c_first, c_last, c_first * total / ctas < unit_begin);
+            }
+        }
+        first_segment = false;
+    }
+    cp_async_wait<0>();
+}
+
+int dp_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+// Query heads of a unit: 16 where the heads of a key-value head need them and the
+// registers hold 16 rows of o and q.
+int rows_of(int group, int dp, bool exact) { return group > 8 && dp <= 128 && !exact ? 16 : 8; }
+
+template <int DP, bool F8, int ROWS, bool EX>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+    using K = Attn<DP, F8, ROWS, EX>;
+    auto kern = attn_kernel<DP, F8, ROWS, EX>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
+    if (e != cudaSuccess) return e;
+    // as many CTAs as run at once: 228 KB of shared memory per SM, 1 KB of it per CTA reserved
+    const int per_sm = K::kSmem + sizeof(typename K::Shared) + 1024 <= 114 * 1024 ? kAttnCtasPerSm : 1;
+    const int grid = std::min(per_sm * device_sm_count(), kAttnMaxCtas);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(kAttnThreads), K::kSmem, s, a);
+}
+
+template <int DP, bool F8>
+cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
+    const bool exact = a.q_dt == MOE_DTYPE_F32 || a.o_dt == MOE_DTYPE_F32;
+    if (exact) return launch<DP, F8, 8, true>(a, s);
+    if constexpr (DP <= 128) {
+        if (rows_of(a.group, DP, false) == 16) return launch<DP, F8, 16, false>(a, s);
+    }
+    return launch<DP, F8, 8, false>(a, s);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int, int, int, int, size_t* done_off, size_t* parts_off) {
-    *done_off = *parts_off = 512;
-    return 512;
+size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t* done_off, size_t* parts_off) {
+    // the parts come first: their place does not depend on B, so that the counters
+    // after them stay zero whatever the calls' batch sizes are
+    const int group = q_heads / heads, dp = dp_of(head_dim);
+    const size_t floats = (size_t)rows_of(group, dp, false) * (dp + 2);
+    *parts_off = 512;
+    *done_off = 512 + 2 * kAttnMaxCtas * floats * sizeof(float);
+    const size_t total = *done_off + (size_t)B * heads * ((group + 7) / 8) * sizeof(uint32_t);
+    return (total + 255) / 256 * 256;   // moe_workspace_init clears whole 16-byte words
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
-    return launch_pdl(attn_kernel, dim3((unsigned)a.B, (unsigned)a.q_heads), dim3(kAttnWarps * 32), 0, s, a);
+    const bool f8 = a.c.dtype == MOE_DTYPE_FP8_E4M3;
+    switch (dp_of(a.c.head_dim)) {
+        case 64: return f8 ? launch_dp<64, true>(a, s) : launch_dp<64, false>(a, s);
+        case 128: return f8 ? launch_dp<128, true>(a, s) : launch_dp<128, false>(a, s);
+        default: return f8 ? launch_dp<256, true>(a, s) : launch_dp<256, false>(a, s);
+    }
 }
 
 }  // namespace moe
