@@ -30,10 +30,8 @@ namespace {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kAttnCtasPerSm = 2;
-constexpr int kAttnMaxCtas = 320;          // bounds the workspace
-constexpr int kAttnStages = 3;
-constexpr int kMergeFloats = 4096;         // shared merge buffer, 16 KB
+constexpr int kAttnMaxCtas = 480;          // bounds the workspace
+constexpr int kMergeFloats = 2048;         // shared merge buffer, 8 KB
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -66,6 +64,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// 2^x to about 2^-22 relative; results below 2^-126 become 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// tanh(x) = 1 - 2 / (1 + e^2x), to about 2^-22 of 1 (not of small results).
+__device__ __forceinline__ float tanh_fast(float x) {
+    return 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(fminf(2.0f * kLog2e * x, 126.0f)));
+}
 // bf16 parts by truncation: p = hi + rest exactly, rest of p's sign.
 __device__ __forceinline__ float bf16_trunc(float p) { return __uint_as_float(__float_as_uint(p) & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
@@ -74,6 +82,20 @@ __device__ __forceinline__ uint32_t pack_hi(float a, float b) { return __byte_pe
 struct Cursor {
     int b, unit, tile, tiles, first, n;
     long long left;                        // tiles of this CTA from here on
+};
+
+// x / y for 0 <= x, 0 < y; 64-bit division only where it must be.
+__device__ __forceinline__ long long div_u(long long x, long long y) {
+    if (((unsigned long long)(x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+    return x / y;
+}
+// CTA k of `ctas` <= total takes the tiles from k total / ctas on.
+struct Share {
+    long long ctas, total;
+    __device__ Share(long long c, long long t) : ctas(c), total(t) {}
+    __device__ long long start(long long k) const { return div_u(k * total, ctas); }
+    // the largest k with start(k) <= u
+    __device__ int cta_of(long long u) const { return (int)div_u((u + 1) * ctas - 1, total); }
 };
 
 // DP: head_dim rounded up to 64, 128 or 256.  F8: E4M3 cache.  ROWS: query heads of a
@@ -95,7 +117,9 @@ struct Attn {
     static constexpr int kAccs = DP / 8;                             // n8 tiles of o
     // p in f16 is scaled to use its range: 2^15 at the maximum
     static constexpr float kPShift = F8 ? 15.0f : 0.0f;
-    static constexpr size_t kRing = (size_t)kAttnWarps * kAttnStages * 2 * kTileBytes;
+    static constexpr int kCtasPerSm = DP == 256 ? (F8 ? 2 : 1) : EX ? 2 : 3;
+    static constexpr int kStages = kCtasPerSm == 3 && kTileBytes == 4096 ? 2 : 3;
+    static constexpr size_t kRing = (size_t)kAttnWarps * kStages * 2 * kTileBytes;
     static constexpr size_t kSmem = kRing + kMergeFloats * 4;
     static constexpr int kPartFloats = ROWS * (DP + 2);
     static_assert(ROWS == 8 || (ROWS == 16 && !EX), "16 heads only without extra terms");
@@ -131,41 +155,47 @@ struct Attn {
             set_request(a, c);
         } while (c.tiles == 0);
     }
-    // Page of the key that lane `lane` looks after in the warp's tile, or -1.
-    __device__ static __forceinline__ int page_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
+    // Page and slot of the key that lane `lane` looks after in the warp's tile; page -1: none.
+    __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
         const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
-        if (c.left <= 0 || lane >= KT || key >= c.n) return -1;
-        const int page = a.table[c.b * a.table_ld + key / a.c.page_size];
+        if (c.left <= 0 || lane >= KT || key >= c.n) return make_int2(-1, 0);
+        const int col = key / a.c.page_size;
+        const int page = a.table[c.b * a.table_ld + col];
         if (page < 0 || page >= a.c.num_pages) {
             set_status(a.status, MOE_ERR_DEVICE);
-            return -1;
+            return make_int2(-1, 0);
         }
-        return page;
+        return make_int2(page, key - col * a.c.page_size);
     }
     // Start the copies of the warp's K and V rows of tile c into a stage; returns the
     // mask of the keys that count.  The rows of the others become zeros.
-    __device__ static __forceinline__ uint32_t issue(const AttnArgs& a, const Cursor& c, int page, int nsub, int warp,
+    __device__ static __forceinline__ uint32_t issue(const AttnArgs& a, const Cursor& c, int2 place, int nsub, int warp,
                                                      int lane, uint32_t stage) {
-        const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
-        const int g = c.unit / nsub;
-        const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+        const int g = nsub == 1 ? c.unit : c.unit / nsub;
+        const uint32_t mask = __ballot_sync(0xffffffffu, place.x >= 0);
+        if (mask == 0u) return 0u;   // nobody reads the stage
+        // offsets in 16-byte steps: 32 bits of them unless a cache tensor passes 64 GB
         long long ko = 0, vo = 0;
-        if (page >= 0) {
-            const int slot = key % a.c.page_size;
-            ko = (page * a.c.k_page_stride + slot * a.c.k_slot_stride + g * a.c.k_head_stride) * kElem;
-            vo = (page * a.c.v_page_stride + slot * a.c.v_slot_stride + g * a.c.v_head_stride) * kElem;
+        if (place.x >= 0) {
+            ko = (place.x * a.c.k_page_stride + place.y * a.c.k_slot_stride + g * a.c.k_head_stride) / (16 / kElem);
+            vo = (place.x * a.c.v_page_stride + place.y * a.c.v_slot_stride + g * a.c.v_head_stride) / (16 / kElem);
         }
         const int ch = lane % kChunks, r0 = lane / kChunks;
-        const bool in = ch * 16 < a.c.head_dim * kElem;
+        const uint32_t in = ch * 16 < a.c.head_dim * kElem ? 16u : 0u;
         const char* kb = static_cast<const char*>(a.c.k) + ch * 16;
         const char* vb = static_cast<const char*>(a.c.v) + ch * 16;
+        const bool all = mask == (KT == 32 ? 0xffffffffu : (1u << KT) - 1u);
 #pragma unroll
         for (int i = 0; i < KT / kRowsPerIter; ++i) {
             const int r = i * kRowsPerIter + r0;
-            const long long o = __shfl_sync(0xffffffffu, ko, r), p = __shfl_sync(0xffffffffu, vo, r);
-            const uint32_t size = in && ((mask >> r) & 1u) ? 16u : 0u;
-            cp_async16_zfill(stage + at_k(r, ch), size ? kb + o : a.c.k, size);
-            cp_async16_zfill(stage + kTileBytes + at_v(r, ch), size ? vb + p : a.c.v, size);
+            long long o = __shfl_sync(0xffffffffu, (uint32_t)ko, r), p = __shfl_sync(0xffffffffu, (uint32_t)vo, r);
+            if (a.far) {
+                o |= (long long)__shfl_sync(0xffffffffu, (uint32_t)(ko >> 32), r) << 32;
+                p |= (long long)__shfl_sync(0xffffffffu, (uint32_t)(vo >> 32), r) << 32;
+            }
+            const uint32_t size = all || ((mask >> r) & 1u) ? in : 0u;
+            cp_async16_zfill(stage + at_k(r, ch), kb + o * 16, size);
+            cp_async16_zfill(stage + kTileBytes + at_v(r, ch), vb + p * 16, size);
         }
         return mask;
     }
@@ -312,24 +342,36 @@ struct Attn {
         uint32_t pf[kPTerms][NT][ROWS / 8];   // weights as A fragments: keys 2 col, + 1 of each n8 tile
 #pragma unroll
         for (int rr = 0; rr < ROWS / 8; ++rr) {
-            const float f = a.softcap > 0.0f ? st.qf[rr] / a.softcap : st.qf[rr] * kLog2e;
             float mx = -CUDART_INF_F;
+            if (a.softcap > 0.0f) {
+                const float f = st.qf[rr] / a.softcap, cap = a.softcap * kLog2e;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float v = s[nt][rr][e] * f;
-                    if (a.softcap > 0.0f) v = a.softcap * kLog2e * tanhf(v);
-                    if (!((mask >> (nt * 8 + 2 * col + e)) & 1u)) v = -CUDART_INF_F;
-                    s[nt][rr][e] = v;
-                    mx = fmaxf(mx, v);
-                }
+                    for (int e = 0; e < 2; ++e)
+                        s[nt][rr][e] = cap * (EX ? tanhf(s[nt][rr][e] * f) : tanh_fast(s[nt][rr][e] * f));
+            } else {
+                const float f = st.qf[rr] * kLog2e;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[nt][rr][e] *= f;
+            }
+            if (mask != (KT == 32 ? 0xffffffffu : (1u << KT) - 1u)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (!((mask >> (nt * 8 + 2 * col + e)) & 1u)) s[nt][rr][e] = -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][rr][0], s[nt][rr][1]));
             __syncwarp();
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             const float m_new = fmaxf(st.m[rr], mx);
-            const float base = m_new == -CUDART_INF_F ? 0.0f : m_new;
-            const float corr = exp2f(st.m[rr] - base);
+            const float top = m_new == -CUDART_INF_F ? 0.0f : m_new, base = top - kPShift;
+            const float corr = exp2_fast(st.m[rr] - top);
             if (__any_sync(0xffffffffu, m_new != st.m[rr])) {
                 st.l[rr] *= corr;
 #pragma unroll
@@ -345,7 +387,7 @@ struct Attn {
             st.m[rr] = m_new;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float p0 = exp2f(s[nt][rr][0] - base + kPShift), p1 = exp2f(s[nt][rr][1] - base + kPShift);
+                float p0 = exp2_fast(s[nt][rr][0] - base), p1 = exp2_fast(s[nt][rr][1] - base);
                 st.l[rr] += p0 + p1;
 #pragma unroll
                 for (int t = 0; t < kPTerms; ++t) {
@@ -431,7 +473,7 @@ struct Attn {
 
     struct Shared {
         float m[kAttnWarps][ROWS], l[kAttnWarps][ROWS];
-        uint32_t mask[kAttnWarps][kAttnStages];
+        uint32_t mask[kAttnWarps][kStages];
         long long wsum[kAttnWarps];
         int found_b, last;
         long long found_pre;
@@ -538,32 +580,62 @@ struct Attn {
         }
     }
 
-    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, long long c_first, long long c_last,
-                                bool tail_first) {
-        const int g = c.unit / nsub, sub = c.unit % nsub;
-        for (int it = threadIdx.x; it < ROWS * (DP / 4); it += kAttnThreads) {
-            const int row = it / (DP / 4), c4 = it % (DP / 4);
-            float top = -CUDART_INF_F, l = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (long long k = c_first; k <= c_last; ++k) {
-                const float* p = a.parts + (2 * k + (k == c_first && tail_first ? 1 : 0)) * kPartFloats;
-                top = fmaxf(top, __ldcg(p + ROWS * DP + row));
-            }
-#pragma unroll 4
-            for (long long k = c_first; k <= c_last; ++k) {
-                const float* p = a.parts + (2 * k + (k == c_first && tail_first ? 1 : 0)) * kPartFloats;
-                const float pl = __ldcg(p + ROWS * DP + ROWS + row), f = weight_of(__ldcg(p + ROWS * DP + row), top);
-                l = fmaf(pl != pl ? 1.0f : f, pl, l);
-                axpy4(o, f, __ldcg(reinterpret_cast<const float4*>(p) + row * (DP / 4) + c4));
-            }
-            finish(a, c.b, g, sub, row, c4, o, top, l);
+    // Join the parts of CTAs c_first .. c_last, in that order: the weights of all
+    // parts first (in `buf`, as many at a time as it holds), then their sum.
+    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, int c_first, int c_last, bool tail_first,
+                                float* buf) {
+        const int g = c.unit / nsub, sub = c.unit % nsub, tid = threadIdx.x;
+        auto part = [&](int k) { return a.parts + (size_t)(2 * k + (k == c_first && tail_first ? 1 : 0)) * kPartFloats; };
+        constexpr int kMost = kMergeFloats / 2 / ROWS;          // parts whose maxima and sums fit
+        constexpr int kItems = ROWS * (DP / 4) / kAttnThreads;  // float4 a thread joins
+        static_assert(kItems * kAttnThreads == ROWS * (DP / 4), "whole items");
+        float top[kItems], l[kItems];
+        float4 o[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            top[i] = -CUDART_INF_F;
+            l[i] = 0.0f;
+            o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
+        for (int k0 = c_first; k0 <= c_last; k0 += kMost) {
+            const int count = min(kMost, c_last - k0 + 1);
+            __syncthreads();
+            for (int it = tid; it < count * 2 * ROWS; it += kAttnThreads)
+                buf[it] = __ldcg(part(k0 + it / (2 * ROWS)) + ROWS * DP + it % (2 * ROWS));
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int row = (tid + i * kAttnThreads) / (DP / 4);
+                float mx = top[i];
+                for (int k = 0; k < count; ++k) mx = fmaxf(mx, buf[k * 2 * ROWS + row]);
+                const float f = weight_of(top[i], mx);
+                l[i] *= f;
+                o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
+                top[i] = mx;
+            }
+#pragma unroll 8
+            for (int k = 0; k < count; ++k) {
+                const float4* p = reinterpret_cast<const float4*>(part(k0 + k));
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int row = (tid + i * kAttnThreads) / (DP / 4);
+                    const float pl = buf[k * 2 * ROWS + ROWS + row], f = weight_of(buf[k * 2 * ROWS + row], top[i]);
+                    l[i] = fmaf(pl != pl ? 1.0f : f, pl, l[i]);
+                    axpy4(o[i], f, __ldcg(p + tid + i * kAttnThreads));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int it = tid + i * kAttnThreads;
+            finish(a, c.b, g, sub, it / (DP / 4), it % (DP / 4), o[i], top[i], l[i]);
+        }
+        __syncthreads();
     }
 };
 
 template <int DP, bool F8, int ROWS, bool EX>
-__global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPerSm) attn_kernel(const __grid_constant__ AttnArgs a) {
     using K = Attn<DP, F8, ROWS, EX>;
     extern __shared__ __align__(128) char smem[];
     __shared__ typename K::Shared sh;
@@ -572,28 +644,49 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) attn_kernel(cons
     pdl_allow_dependents();
     pdl_wait_primary();
 
-    // ---- the run of this CTA: tiles [start, end) of the `total` of all requests
+    // ---- the run of this CTA: tiles [start, end) of the `total` of all requests,
+    // found with a scan of the requests in blocks of the CTA's threads
     auto tiles_of = [&](int b) {
         Cursor c;
         c.b = b;
         K::set_request(a, c);
         return c.tiles;
     };
-    long long mine = 0;
-    for (int b = tid; b < a.B; b += kAttnThreads) {
-        mine += tiles_of(b);
-        if (blockIdx.x == 0 && (long long)max(a.seq_lens[b], 0) > (long long)a.max_pages * a.c.page_size)
-            set_status(a.status, MOE_ERR_DEVICE);
+    // inclusive scan of t over the threads; `all` gets the block's sum
+    auto scan = [&](long long t, long long& all) {
+        long long incl = t;
+        __syncwarp();
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (lane == 31) sh.wsum[warp] = incl;
+        __syncthreads();
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            if (w < warp) incl += sh.wsum[w];
+            all += sh.wsum[w];
+        }
+        return incl;
+    };
+    const int t0 = tid < a.B ? tiles_of(tid) : 0;      // of the first block
+    long long sum0, total;
+    const long long incl0 = scan((long long)t0 * units, sum0);
+    total = sum0;
+    if (a.B > kAttnThreads) {
+        long long mine = 0;
+        for (int b = kAttnThreads + tid; b < a.B; b += kAttnThreads) mine += tiles_of(b);
+        long long rest;
+        __syncthreads();
+        scan(mine * units, rest);
+        total += rest;
     }
-    __syncwarp();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sh.wsum[warp] = mine;
-    __syncthreads();
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) total += sh.wsum[w];
-    total *= units;
+    if (blockIdx.x == 0) {
+        for (int b = tid; b < a.B; b += kAttnThreads)
+            if ((long long)max(a.seq_lens[b], 0) > (long long)a.max_pages * a.c.page_size) set_status(a.status, MOE_ERR_DEVICE);
+    }
     // requests without keys
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (tiles_of(b) > 0) continue;
@@ -602,68 +695,57 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) attn_kernel(cons
             K::finish(a, b, unit / nsub, unit % nsub, row, c4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
         }
     }
-    const long long ctas = min((long long)gridDim.x, total);
-    if (blockIdx.x >= ctas) return;
-    const long long start = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
-    // request of tile `start`: scan the requests in blocks of the CTA's threads
-    long long before = 0;
-    for (int b0 = 0;; b0 += kAttnThreads) {
-        const int b = b0 + tid;
-        const long long t = b < a.B ? (long long)tiles_of(b) * units : 0;
-        long long incl = t;
-        __syncwarp();
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        __syncthreads();
-        if (lane == 31) sh.wsum[warp] = incl;
-        if (tid == 0) sh.found_b = -1;
-        __syncthreads();
-        long long pre = before + incl - t, all = 0;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
-            if (w < warp) pre += sh.wsum[w];
-            all += sh.wsum[w];
-        }
-        if (start >= pre && start < pre + t) {
-            sh.found_b = b;
+    const Share share(min((long long)gridDim.x, total), total);
+    if (blockIdx.x >= share.ctas) return;
+    const long long start = share.start(blockIdx.x), end = share.start(blockIdx.x + 1);
+    long long before = 0, incl = incl0, all = sum0;
+    int t = t0, b0 = 0;
+    while (true) {
+        const long long pre = before + incl - (long long)t * units;
+        if (start >= pre && start < before + incl) {
+            sh.found_b = b0 + tid;
             sh.found_pre = pre;
         }
-        __syncthreads();
-        if (sh.found_b >= 0) break;
         before += all;
+        if (start < before) break;      // the same for all threads
+        b0 += kAttnThreads;
+        t = b0 + tid < a.B ? tiles_of(b0 + tid) : 0;
+        __syncthreads();
+        incl = scan((long long)t * units, all);
     }
+    __syncthreads();
     Cursor c;
     c.b = sh.found_b;
     K::set_request(a, c);
-    c.unit = (int)((start - sh.found_pre) / c.tiles);
-    c.tile = (int)((start - sh.found_pre) % c.tiles);
+    {
+        const long long off = start - sh.found_pre;
+        c.unit = (int)div_u(off, c.tiles);
+        c.tile = (int)(off - (long long)c.unit * c.tiles);
+    }
     c.left = end - start;
 
-    // ---- pipeline: `ahead` runs kAttnStages - 1 tiles in front of `c`
-    const uint32_t ring = smem_u32(smem) + warp * kAttnStages * 2 * K::kTileBytes;
-    const char* ring_p = smem + (size_t)warp * kAttnStages * 2 * K::kTileBytes;
+    // ---- pipeline: `ahead` runs K::kStages - 1 tiles in front of `c`
+    const uint32_t ring = smem_u32(smem) + warp * K::kStages * 2 * K::kTileBytes;
+    const char* ring_p = smem + (size_t)warp * K::kStages * 2 * K::kTileBytes;
     float* buf = reinterpret_cast<float*>(smem + K::kRing);
     Cursor ahead = c;
-    int page = K::page_of(a, ahead, warp, lane);
+    int2 place = K::place_of(a, ahead, warp, lane);
     int stage_in = 0;
     auto feed = [&]() {
         if (ahead.left > 0) {
             Cursor next = ahead;
             K::advance(a, units, next);
-            const int page_next = K::page_of(a, next, warp, lane);
-            const uint32_t mask = K::issue(a, ahead, page, nsub, warp, lane, ring + stage_in * 2 * K::kTileBytes);
+            const int2 place_next = K::place_of(a, next, warp, lane);
+            const uint32_t mask = K::issue(a, ahead, place, nsub, warp, lane, ring + stage_in * 2 * K::kTileBytes);
             if (lane == 0) sh.mask[warp][stage_in] = mask;
-            stage_in = stage_in + 1 == kAttnStages ? 0 : stage_in + 1;
+            stage_in = stage_in + 1 == K::kStages ? 0 : stage_in + 1;
             ahead = next;
-            page = page_next;
+            place = place_next;
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kAttnStages - 1; ++i) feed();
+    for (int i = 0; i < K::kStages - 1; ++i) feed();
 
     int stage_out = 0;
     bool first_segment = true;
@@ -675,13 +757,13 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) attn_kernel(cons
         const long long unit_begin = at - c.tile, unit_end = unit_begin + c.tiles;
         const int count = (int)min(c.left, (long long)(c.tiles - c.tile));
         for (int i = 0; i < count; ++i) {
-            cp_async_wait<kAttnStages - 2>();
+            cp_async_wait<K::kStages - 2>();
             __syncwarp();
             const uint32_t mask = sh.mask[warp][stage_out];
             feed();
             // keys beyond the request (the tail of its last tile) count for nothing
             if (mask) K::tile(a, st, ring_p + stage_out * 2 * K::kTileBytes, mask, lane);
-            stage_out = stage_out + 1 == kAttnStages ? 0 : stage_out + 1;
+            stage_out = stage_out + 1 == K::kStages ? 0 : stage_out + 1;
             K::advance(a, units, c);
         }
         at += count;
@@ -689,8 +771,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) attn_kernel(cons
         float* part = whole ? nullptr : a.parts + (size_t)(2 * blockIdx.x + (first_segment ? 0 : 1)) * K::kPartFloats;
         K::merge(a, seg, nsub, st, buf, sh, part);
         if (!whole) {
-            // CTA of tile u: the largest k with k total / ctas <= u
-            const long long c_first = ((unit_begin + 1) * ctas - 1) / total, c_last = (unit_end * ctas - 1) / total;
+            const int c_first = share.cta_of(unit_begin), c_last = share.cta_of(unit_end - 1);
             uint32_t* done = a.done + (long long)seg.b * units + seg.unit;
             __threadfence();
             __syncthreads();
@@ -702,7 +783,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) attn_kernel(cons
             __syncthreads();
             if (sh.last) {
                 __threadfence();
-                K::join(a, seg, nsub, c_first, c_last, c_first * total / ctas < unit_begin);
+                K::join(a, seg, nsub, c_first, c_last, share.start(c_first) < unit_begin, buf);
             }
         }
         first_segment = false;
@@ -721,9 +802,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = attn_kernel<DP, F8, ROWS, EX>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
     if (e != cudaSuccess) return e;
-    // as many CTAs as run at once: 228 KB of shared memory per SM, 1 KB of it per CTA reserved
-    const int per_sm = K::kSmem + sizeof(typename K::Shared) + 1024 <= 114 * 1024 ? kAttnCtasPerSm : 1;
-    const int grid = std::min(per_sm * device_sm_count(), kAttnMaxCtas);
+    static_assert(K::kCtasPerSm * (K::kSmem + sizeof(typename K::Shared) + 1024) <= 228 * 1024, "CTAs that run at once");
+    const int grid = std::min(K::kCtasPerSm * device_sm_count(), kAttnMaxCtas);
     return launch_pdl(kern, dim3((unsigned)grid), dim3(kAttnThreads), K::kSmem, s, a);
 }
 
@@ -750,8 +830,16 @@ size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t*
     return (total + 255) / 256 * 256;   // moe_workspace_init clears whole 16-byte words
 }
 
-cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_attn_decode(const AttnArgs& args, cudaStream_t s) {
+    AttnArgs a = args;
     const bool f8 = a.c.dtype == MOE_DTYPE_FP8_E4M3;
+    // bytes up to the last row of either tensor
+    auto reach = [&](int64_t page, int64_t slot, int64_t head) {
+        return (__int128)page * (a.c.num_pages - 1) + (__int128)slot * (a.c.page_size - 1) + (__int128)head * (a.c.heads - 1);
+    };
+    const __int128 most = std::max(reach(a.c.k_page_stride, a.c.k_slot_stride, a.c.k_head_stride),
+                                   reach(a.c.v_page_stride, a.c.v_slot_stride, a.c.v_head_stride));
+    a.far = most * (f8 ? 1 : 2) / 16 > 0xffffffffll;
     switch (dp_of(a.c.head_dim)) {
         case 64: return f8 ? launch_dp<64, true>(a, s) : launch_dp<64, false>(a, s);
         case 128: return f8 ? launch_dp<128, true>(a, s) : launch_dp<128, false>(a, s);

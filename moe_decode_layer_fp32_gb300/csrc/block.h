@@ -56,6 +56,7 @@ struct AttnArgs {
     const int32_t* seq_lens;
     float scale, softcap;
     int window;
+    int far;                   // cache offsets pass 2^32 steps of 16 bytes (set by the launcher)
     int32_t* status;
     uint32_t* done;            // counters, one per unit (zero between calls)
     float* parts;              // partial results
