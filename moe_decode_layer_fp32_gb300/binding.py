@@ -141,8 +141,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current device's current stream as a pointer.  The same value as
+# torch.cuda.current_stream().cuda_stream without building a Stream object,
+# which took longer than the launch itself (2.9 of 3.8 us on a Grace host).
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_current_device())
 
 
 def _dtype_code(t) -> int:
@@ -439,39 +445,56 @@ def moe_unique_weight_bytes_deamoe(d, n, I_sh, I_pr, I_s, dtype_code, A_d, A_e) 
 # dimension) must be contiguous, everything else may be a view.
 
 
-_CODES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
+# A small call costs its host time: these helpers ask each tensor for as little
+# as will do, and the calls reach the library through names bound once.
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_CODES = {_F32: MOE_DTYPE_F32, _BF16: MOE_DTYPE_BF16, torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
 
 
-def _code(t, name: str) -> int:
+def _bad(t, name, what):
+    raise ValueError(f"{name}: expected {what}, got {'CUDA' if t.is_cuda else 'CPU'} {t.dtype} of shape "
+                     f"{tuple(t.shape)}, strides {t.stride()}")
+
+
+def _rows(t, name, shape):
+    """(device pointer, dtype code, row stride) of a CUDA matrix of this shape whose rows are
+    contiguous (a single row's stride means nothing)."""
     code = _CODES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-    return code
+    if code is None or not t.is_cuda or t.shape != shape:
+        _bad(t, name, f"a CUDA tensor {tuple(shape)} of a supported dtype")
+    ld, step = t.stride()
+    if step != 1 and shape[1] != 1:
+        _bad(t, name, "contiguous rows")
+    return t.data_ptr(), code, ld if shape[0] > 1 else shape[1]
 
 
-def _rows(t, name: str, dim: int) -> int:
-    """Device pointer of a CUDA tensor of ``dim`` dimensions whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dim() != dim:
-        raise ValueError(f"{name}: expected {dim} dimensions, got shape {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: expected contiguous rows")
-    return t.data_ptr()
+def _heads(t, name, shape):
+    """(device pointer, dtype code, strides between tokens and heads) of a CUDA tensor [T, heads, D]."""
+    code = _CODES.get(t.dtype)
+    if code is None or not t.is_cuda or t.shape != shape:
+        _bad(t, name, f"a CUDA tensor {tuple(shape)} of a supported dtype")
+    outer, inner, step = t.stride()
+    if step != 1 and shape[2] != 1:
+        _bad(t, name, "contiguous rows")
+    return t.data_ptr(), code, outer, inner
 
 
-def _ld(t) -> int:
-    """Stride between the rows of a matrix (a single row's stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _want(t, name: str, shape, dtype):
+def _want(t, name, shape, dtype):
     """Device pointer of a contiguous CUDA tensor of this shape and type (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, name, f"a contiguous CUDA {dtype} tensor {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _table(t):
+    """(device pointer, row stride, requests, pages) of a block table."""
+    R, pages = t.shape
+    ld, step = t.stride()
+    if t.dtype is not _I32 or not t.is_cuda or (step != 1 and pages > 1):
+        _bad(t, "block_table", "a CUDA int32 tensor [requests, pages] with contiguous rows")
+    return t.data_ptr(), ld if R > 1 else pages, R, pages
 
 
 def moe_rmsnorm(x, weight, eps: float, y, residual=None, residual_out=None, y_scale=None):
@@ -480,31 +503,28 @@ def moe_rmsnorm(x, weight, eps: float, y, residual=None, residual_out=None, y_sc
     ``residual_out`` gets x + residual (it may be ``residual`` itself);
     ``weight`` [d] or None; ``y_scale`` goes with an E4M3 ``y``: float32 [T]
     (a scale per row) or [T, d / 128] (per 128 columns)."""
-    T, d = x.shape
-    if y.shape != x.shape or (weight is not None and tuple(weight.shape) != (d,)):
-        raise ValueError("x and y must both be [T, d], weight [d]")
-    r_code = r_ld = ro_ld = 0
-    r_ptr = ro_ptr = None
+    shape = x.shape
+    T, d = shape
+    x_ptr, x_code, x_ld = _rows(x, "x", shape)
+    y_ptr, y_code, y_ld = _rows(y, "y", shape)
+    r_ptr = ro_ptr = w_ptr = s_ptr = None
+    r_code = r_ld = ro_ld = w_code = group = 0
     if residual is not None:
-        r_code, r_ld, r_ptr = _code(residual, "residual"), _ld(residual), _rows(residual, "residual", 2)
+        r_ptr, r_code, r_ld = _rows(residual, "residual", shape)
     if residual_out is not None:
-        code, ro_ld, ro_ptr = _code(residual_out, "residual_out"), _ld(residual_out), _rows(residual_out, "residual_out", 2)
+        ro_ptr, code, ro_ld = _rows(residual_out, "residual_out", shape)
         if residual is not None and code != r_code:
             raise ValueError("residual and residual_out must have one dtype")
         r_code = code
-    for t in (residual, residual_out):
-        if t is not None and t.shape != x.shape:
-            raise ValueError("residual and residual_out must be [T, d]")
-    group = 0
-    if y_scale is not None and y_scale.dim() == 2:
-        group = 128
-        _want(y_scale, "y_scale", (T, d // 128), torch.float32)
-    else:
-        _want(y_scale, "y_scale", (T,), torch.float32)
-    rc = lib().moe_rmsnorm(
-        _rows(x, "x", 2), _code(x, "x"), _ld(x), r_ptr, r_code, r_ld, ro_ptr, ro_ld, _ptr(weight),
-        _code(weight, "weight") if weight is not None else 0, eps, T, d, _rows(y, "y", 2), _code(y, "y"), _ld(y),
-        _ptr(y_scale), group, _stream())
+    if weight is not None:
+        w_code = _CODES.get(weight.dtype, -1)
+        w_ptr = _want(weight, "weight", (d,), weight.dtype)
+    if y_scale is not None:
+        if y_scale.dim() == 2:
+            group = 128
+        s_ptr = _want(y_scale, "y_scale", (T, d // 128) if group else (T,), _F32)
+    rc = (_lib or lib()).moe_rmsnorm(x_ptr, x_code, x_ld, r_ptr, r_code, r_ld, ro_ptr, ro_ld, w_ptr, w_code, eps, T, d,
+                                     y_ptr, y_code, y_ld, s_ptr, group, _raw_stream(_current_device()))
     if rc:
         _check("moe_rmsnorm", rc)
 
@@ -516,14 +536,17 @@ class KvCache:
     [heads, page_size, D]: pass ``cache.transpose(1, 2)``).  Holds its tensors."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        if k.shape != v.shape or k.dtype != v.dtype:
-            raise ValueError("k and v must have one shape and dtype")
+        if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4:
+            raise ValueError("k and v must both be [pages, page_size, heads, D], of one dtype")
         pages, page, heads, D = k.shape
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype not in _CODES or not t.is_cuda or (t.stride(3) != 1 and D > 1):
+                _bad(t, name, "a CUDA tensor of a supported dtype with contiguous rows")
         self.tensors = (k, v, k_scale, v_scale)
         self.heads, self.head_dim, self.page_size = heads, D, page
         self.args = KvCacheArgs(
-            _rows(k, "k", 4), _rows(v, "v", 4), _want(k_scale, "k_scale", (heads,), torch.float32),
-            _want(v_scale, "v_scale", (heads,), torch.float32), *k.stride()[:3], *v.stride()[:3], _code(k, "k"),
+            k.data_ptr(), v.data_ptr(), _want(k_scale, "k_scale", (heads,), _F32),
+            _want(v_scale, "v_scale", (heads,), _F32), *k.stride()[:3], *v.stride()[:3], _CODES[k.dtype],
             pages, page, heads, D)
         self.ref = C.byref(self.args)
 
@@ -536,28 +559,32 @@ def moe_kv_append(k, v, cache: KvCache, block_table, positions, req=None, cos_si
     or None (token t is request t); ``cos_sin`` float32 [positions, rot] or
     None; ``q_out`` may be ``q``; ``status`` int32 [1] or None."""
     T = k.shape[0]
-    code = _code(k, "k")
-    if k.shape != (T, cache.heads, cache.head_dim) or v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must both be [T, heads, D] of the cache, of one dtype")
-    q_args = (None, 0, 0, None, 0, 0, 0)
+    shape = (T, cache.heads, cache.head_dim)
+    k_ptr, code, k_t, k_h = _heads(k, "k", shape)
+    v_ptr, v_code, v_t, v_h = _heads(v, "v", shape)
+    if v_code != code:
+        raise ValueError("k and v must have one dtype")
+    q_ptr = o_ptr = cs_ptr = None
+    q_t = q_h = o_t = o_h = q_heads = max_pos = rot = 0
     if q is not None:
-        if q_out is None or q.shape != q_out.shape or q.dim() != 3 or q.shape[::2] != k.shape[::2] \
-                or q.dtype != k.dtype or q_out.dtype != k.dtype:
-            raise ValueError("q and q_out must both be [T, q_heads, D] of k's dtype")
-        q_args = (_rows(q, "q", 3), q.stride(0), q.stride(1), _rows(q_out, "q_out", 3), q_out.stride(0),
-                  q_out.stride(1), q.shape[1])
+        if q_out is None:
+            raise ValueError("q without q_out")
+        q_heads = q.shape[1]
+        shape = (T, q_heads, cache.head_dim)
+        q_ptr, q_code, q_t, q_h = _heads(q, "q", shape)
+        o_ptr, o_code, o_t, o_h = _heads(q_out, "q_out", shape)
+        if q_code != code or o_code != code:
+            raise ValueError("q, q_out and k must have one dtype")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-    R, pages = block_table.shape
-    if block_table.dtype != torch.int32:
-        raise ValueError("block_table must be int32 [R, pages]")
-    rc = lib().moe_kv_append(
-        _rows(k, "k", 3), k.stride(0), k.stride(1), _rows(v, "v", 3), v.stride(0), v.stride(1), code, T, cache.ref,
-        _rows(block_table, "block_table", 2), _ld(block_table), R, pages,
-        _want(positions, "positions", (T,), torch.int32), _want(req, "req", (T,), torch.int32),
-        _want(cos_sin, "cos_sin", (max_pos, rot), torch.float32), rot, max_pos, *q_args,
-        _want(status, "status", (1,), torch.int32), _stream())
+    if cos_sin is not None:
+        max_pos, rot = cos_sin.shape
+        cs_ptr = _want(cos_sin, "cos_sin", (max_pos, rot), _F32)
+    table, ld, R, pages = _table(block_table)
+    rc = (_lib or lib()).moe_kv_append(
+        k_ptr, k_t, k_h, v_ptr, v_t, v_h, code, T, cache.ref, table, ld, R, pages,
+        _want(positions, "positions", (T,), _I32), _want(req, "req", (T,), _I32), cs_ptr, rot, max_pos, q_ptr, q_t, q_h,
+        o_ptr, o_t, o_h, q_heads, _want(status, "status", (1,), _I32), _raw_stream(_current_device()))
     if rc:
         _check("moe_kv_append", rc)
 
@@ -581,18 +608,19 @@ def moe_attn_decode(q, cache: KvCache, block_table, seq_lens, scale: float, out,
     """Attention of one new token per request: q, out [B, q_heads, D],
     ``block_table`` int32 [B, pages], ``seq_lens`` int32 [B] (the new token
     included), ``lse`` float32 [B, q_heads] or None."""
-    B, hq, D = q.shape
-    if D != cache.head_dim or out.shape != q.shape:
-        raise ValueError("q and out must both be [B, q_heads, D] of the cache's D")
-    if block_table.dtype != torch.int32 or block_table.shape[0] != B:
-        raise ValueError("block_table must be int32 [B, pages]")
-    pages = block_table.shape[1]
-    rc = lib().moe_attn_decode(
-        _rows(q, "q", 3), _code(q, "q"), q.stride(0), q.stride(1), B, hq, cache.ref,
-        _rows(block_table, "block_table", 2), _ld(block_table), pages,
-        _want(seq_lens, "seq_lens", (B,), torch.int32), scale, window, softcap, _rows(out, "out", 3),
-        _code(out, "out"), out.stride(0), out.stride(1), _want(lse, "lse", (B, hq), torch.float32), _ptr(ws),
-        ws.numel(), _stream())
+    shape = q.shape
+    B, hq, D = shape
+    if D != cache.head_dim:
+        raise ValueError("q must be [B, q_heads, D] of the cache's D")
+    q_ptr, q_code, q_b, q_h = _heads(q, "q", shape)
+    o_ptr, o_code, o_b, o_h = _heads(out, "out", shape)
+    table, ld, R, pages = _table(block_table)
+    if R != B:
+        raise ValueError("block_table must have a row per request")
+    rc = (_lib or lib()).moe_attn_decode(
+        q_ptr, q_code, q_b, q_h, B, hq, cache.ref, table, ld, pages, _want(seq_lens, "seq_lens", (B,), _I32), scale,
+        window, softcap, o_ptr, o_code, o_b, o_h, _want(lse, "lse", (B, hq), _F32), _ptr(ws), ws.numel(),
+        _raw_stream(_current_device()))
     if rc:
         _check("moe_attn_decode", rc)
 
@@ -617,24 +645,31 @@ def moe_lora_project(x, w, y, ws, lora=None, adapter=None, x_scale=None, w_scale
 
     x [T, d] float32 or bfloat16 with bfloat16 w [N, d]; or both E4M3 with
     ``x_scale`` float32 [T] and ``w_scale`` float32 [N]."""
-    T, d = x.shape
-    N = w.shape[0]
-    if w.shape[1] != d or y.shape != (T, N):
-        raise ValueError("x must be [T, d], w [N, d], y [T, N]")
-    la = lb = ls = ad = None
+    x_shape, w_shape = x.shape, w.shape
+    T, d = x_shape
+    N = w_shape[0]
+    if w_shape[1] != d:
+        raise ValueError("x must be [T, d] and w [N, d]")
+    x_ptr, x_code, x_ld = _rows(x, "x", x_shape)
+    w_ptr, w_code, w_ld = _rows(w, "w", w_shape)
+    y_ptr, y_code, y_ld = _rows(y, "y", (T, N))
+    la = lb = ls = ad = xs = wsc = None
     n = r = 0
     if lora is not None:
-        n, r, _ = lora[0].shape
-        la = _want(lora[0], "lora A", (n, r, d), torch.bfloat16)
-        lb = _want(lora[1], "lora B", (n, N, r), torch.bfloat16)
-        ls = _want(lora[2], "lora scale", (n,), torch.float32)
-        ad = _want(adapter, "adapter", (T,), torch.int32)
+        A, Bm, scale = lora
+        n, r, _ = A.shape
+        la = _want(A, "lora A", (n, r, d), _BF16)
+        lb = _want(Bm, "lora B", (n, N, r), _BF16)
+        ls = _want(scale, "lora scale", (n,), _F32)
+        ad = _want(adapter, "adapter", (T,), _I32)
     elif adapter is not None:
         raise ValueError("adapter without lora")
-    rc = lib().moe_lora_project(
-        _rows(x, "x", 2), _code(x, "x"), _ld(x), _want(x_scale, "x_scale", (T,), torch.float32),
-        T, d, _rows(w, "w", 2), _code(w, "w"), _ld(w),
-        _want(w_scale, "w_scale", (N,), torch.float32), N, la, lb, ls, n, r, ad, _rows(y, "y", 2), _code(y, "y"),
-        _ld(y), _ptr(ws), ws.numel(), _stream())
+    if x_scale is not None:
+        xs = _want(x_scale, "x_scale", (T,), _F32)
+    if w_scale is not None:
+        wsc = _want(w_scale, "w_scale", (N,), _F32)
+    rc = (_lib or lib()).moe_lora_project(
+        x_ptr, x_code, x_ld, xs, T, d, w_ptr, w_code, w_ld, wsc, N, la, lb, ls, n, r, ad, y_ptr, y_code, y_ld,
+        _ptr(ws), ws.numel(), _raw_stream(_current_device()))
     if rc:
         _check("moe_lora_project", rc)
