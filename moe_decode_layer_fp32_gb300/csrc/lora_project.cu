@@ -34,7 +34,8 @@ constexpr int kBlockBytes = 128;            // bytes of a row per stage (one swi
 constexpr int kWBytes = kRowsM * kBlockBytes;
 constexpr int kChunkBlocks = 4;             // stages per accumulator block
 constexpr int kMaxStages = 12;
-constexpr int kLoraStages = 2;
+constexpr int kLoraStages = 8;              // at most
+constexpr int kLoraTokens = 4;              // tokens of an adapter taken together
 constexpr int kProjThreads = 384;           // 12 warps: TMA, MMA, adapter copies, idle, 4 adapter, 4 epilogue
 constexpr int kProjSmem = 226 * 1024;
 
@@ -63,15 +64,15 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
 }
 
 constexpr int kShrinkThreads = 256;
-constexpr int kShrinkRows = 8;              // rows of A a block takes
 
-// Blocks [0, T r / 8): 8 rows of A_a against x[t], d shared out over the block's
+// Blocks [0, T r / ROWS): ROWS rows of A_a against x[t], d shared out over the block's
 // threads.  The blocks after them write the terms of x.
+template <int ROWS>
 __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ LoraArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_allow_dependents();
     pdl_wait_primary();
-    const int groups = a.r / kShrinkRows, shrink_blocks = a.T * groups;
+    const int groups = a.r / ROWS, shrink_blocks = a.T * groups;
     if ((int)blockIdx.x >= shrink_blocks) {
         const int chunks = a.d / 8;
         const long long plane = (long long)a.T * a.d;
@@ -98,21 +99,21 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
         }
         return;
     }
-    __shared__ float s_part[kShrinkThreads / 32][kShrinkRows];
-    const int t = blockIdx.x / groups, j0 = (blockIdx.x - t * groups) * kShrinkRows;
+    __shared__ float s_part[kShrinkThreads / 32][ROWS];
+    const int t = blockIdx.x / groups, j0 = (blockIdx.x - t * groups) * ROWS;
     const int ad = adapter_of(a, t);
-    float sum[kShrinkRows] = {};
+    float sum[ROWS] = {};
     if (ad >= 0) {
         const __nv_bfloat16* rows = a.la + ((long long)ad * a.r + j0) * a.d;
-#pragma unroll 2
+#pragma unroll (ROWS == 2 ? 4 : 2)
         for (int c = tid * 8; c < a.d; c += kShrinkThreads * 8) {
             float x[8];
             load8_any(a.x, a.x_dt, t * a.x_ld + c, x);
-            uint4 w[kShrinkRows];
+            uint4 w[ROWS];
 #pragma unroll
-            for (int j = 0; j < kShrinkRows; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(rows + (long long)j * a.d + c));
+            for (int j = 0; j < ROWS; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(rows + (long long)j * a.d + c));
 #pragma unroll
-            for (int j = 0; j < kShrinkRows; ++j) {
+            for (int j = 0; j < ROWS; ++j) {
                 float u[8];
                 unpack_bf16x8(w[j], u);
 #pragma unroll
@@ -121,12 +122,12 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
         }
     }
 #pragma unroll
-    for (int j = 0; j < kShrinkRows; ++j) {
+    for (int j = 0; j < ROWS; ++j) {
         const float s = warp_sum(sum[j]);
         if (lane == 0) s_part[warp][j] = s;
     }
     __syncthreads();
-    if (tid < kShrinkRows) {
+    if (tid < ROWS) {
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kShrinkThreads / 32; ++w) s += s_part[w][tid];
@@ -142,7 +143,7 @@ struct ProjArgs {
     int blocks;                 // 128-byte blocks of a row
     int split;                  // CTAs of a cluster
     int stages, lora_stages;
-    int lacc_off, lring_off, wring_off;   // byte offsets in shared memory
+    int lacc_off, v_off, lring_off, wring_off;   // byte offsets in shared memory
 };
 
 // 3-D tile load without a cache hint: what many CTAs read.
@@ -184,6 +185,40 @@ struct ProjShared {
     int order[kLoraMaxT];      // tokens by adapter (those without first), then by index
 };
 
+// out[k][128] = the thread's row of B_a times v[k], for TOK tokens.  The lanes start at different
+// 16-byte chunks of their rows (distinct banks); four pairs of sums per token keep the
+// multiply-adds independent.
+template <int TOK>
+__device__ __forceinline__ void lora_rows(const uint4* row, const float* v, int r, int C, int m, float* out) {
+    float2 acc[TOK][4];
+#pragma unroll
+    for (int k = 0; k < TOK; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[k][e] = make_float2(0.0f, 0.0f);
+    int c = m % C;
+#pragma unroll 4
+    for (int j = 0; j < C; ++j) {
+        float2 b[4];
+        unpack_bf16x8_f2(row[c], b);
+#pragma unroll
+        for (int k = 0; k < TOK; ++k) {
+            const float4* u = reinterpret_cast<const float4*>(v + k * r + c * 8);
+            const float4 x = u[0], y = u[1];
+            acc[k][0] = ffma2(b[0], make_float2(x.x, x.y), acc[k][0]);
+            acc[k][1] = ffma2(b[1], make_float2(x.z, x.w), acc[k][1]);
+            acc[k][2] = ffma2(b[2], make_float2(y.x, y.y), acc[k][2]);
+            acc[k][3] = ffma2(b[3], make_float2(y.z, y.w), acc[k][3]);
+        }
+        c = c + 1 == C ? 0 : c + 1;
+    }
+#pragma unroll
+    for (int k = 0; k < TOK; ++k) {
+        const float2 s = make_float2((acc[k][0].x + acc[k][1].x) + (acc[k][2].x + acc[k][3].x),
+                                     (acc[k][0].y + acc[k][1].y) + (acc[k][2].y + acc[k][3].y));
+        out[k * kRowsM] = s.x + s.y;
+    }
+}
+
 // TP: tokens rounded up to 16, 32, 64 or 128 (MMA columns).  F8: E4M3.  TERMS: bf16
 // terms of x (1, or 3 for fp32).
 template <int TP, bool F8, int TERMS>
@@ -198,6 +233,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     ProjShared& sm = *reinterpret_cast<ProjShared*>(base);
     float* lacc = reinterpret_cast<float*>(base + p.lacc_off);       // [own tokens][128] adapter part
+    float* vs = reinterpret_cast<float*>(base + p.v_off);            // [own tokens][r] v, times the adapter's scale
     unsigned char* lring = base + p.lring_off;
     unsigned char* ring = base + p.wring_off;
     float* red = reinterpret_cast<float*>(ring);                     // after the stream: [T][128] this CTA's sums
@@ -270,6 +306,17 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             int pos = 0;
             for (int u = 0; u < a.T; ++u) pos += sm.key[u] < k || (sm.key[u] == k && u < t);
             sm.order[pos] = t;
+        }
+        __syncthreads();
+        for (int i = tid; i < (p1 - p0) * (a.r / 4); i += kProjThreads) {
+            const int q = i / (a.r / 4), j = i - q * (a.r / 4), t = sm.order[p0 + q], ad = sm.key[t];
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (ad >= 0) {
+                const float f = a.ls[ad];
+                v = *reinterpret_cast<const float4*>(a.v + t * a.r + j * 4);
+                v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            }
+            reinterpret_cast<float4*>(vs)[i] = v;
         }
     } else {
         for (int t = tid; t < a.T; t += kProjThreads) sm.order[t] = t;
@@ -354,44 +401,30 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         if (a.r > 0) {
             const int m = (warp - 4) * 32 + lane, C = a.r / 8;
             const int lstage = kRowsM * a.r * 2;
-            int it = -1, last = -1;
-            float scale = 0.0f;
-            for (int q = p0; q < p1; ++q) {
-                const int t = sm.order[q], ad = sm.key[t];
-                float sum = 0.0f;
-                if (ad >= 0) {
-                    if (ad != last) {
-                        if (it >= 0) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm.lempty[it % p.lora_stages]);
-                        }
-                        ++it;
-                        last = ad;
-                        scale = a.ls[ad];
-                        wait(&sm.lfull[it % p.lora_stages], (it / p.lora_stages) & 1u);
-                    }
-                    const uint4* row = reinterpret_cast<const uint4*>(lring + (it % p.lora_stages) * lstage) + m * C;
-                    const float4* v = reinterpret_cast<const float4*>(a.v + t * a.r);
-                    // the lanes start at different 16-byte chunks of their rows: distinct banks
-                    int c = m % C;
-#pragma unroll 4
-                    for (int j = 0; j < C; ++j) {
-                        float b[8];
-                        unpack_bf16x8(row[c], b);
-                        const float4 u = v[2 * c], w = v[2 * c + 1];
-                        sum = fmaf(b[0], u.x, sum);
-                        sum = fmaf(b[1], u.y, sum);
-                        sum = fmaf(b[2], u.z, sum);
-                        sum = fmaf(b[3], u.w, sum);
-                        sum = fmaf(b[4], w.x, sum);
-                        sum = fmaf(b[5], w.y, sum);
-                        sum = fmaf(b[6], w.z, sum);
-                        sum = fmaf(b[7], w.w, sum);
-                        c = c + 1 == C ? 0 : c + 1;
-                    }
-                    sum *= scale;
+            int it = 0;
+            for (int q = p0; q < p1;) {
+                const int ad = sm.key[sm.order[q]];
+                if (ad < 0) {
+                    lacc[(q - p0) * kRowsM + m] = 0.0f;
+                    ++q;
+                    continue;
                 }
-                lacc[(q - p0) * kRowsM + m] = sum;
+                const int slot = it % p.lora_stages;
+                wait(&sm.lfull[slot], (it / p.lora_stages) & 1u);
+                const uint4* row = reinterpret_cast<const uint4*>(lring + slot * lstage) + m * C;
+                while (q < p1 && sm.key[sm.order[q]] == ad) {
+                    int count = 1;
+                    while (count < kLoraTokens && q + count < p1 && sm.key[sm.order[q + count]] == ad) ++count;
+                    const float* v0 = vs + (q - p0) * a.r;
+                    if (count == 1) lora_rows<1>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
+                    else if (count == 2) lora_rows<2>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
+                    else if (count == 3) lora_rows<3>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
+                    else lora_rows<4>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
+                    q += count;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.lempty[slot]);
+                ++it;
             }
         }
     } else if (warp >= 8) {
@@ -523,9 +556,13 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
         int off = round_up((int)sizeof(ProjShared), 1024);
         p.lacc_off = off;
         if (a.r > 0) off = round_up(off + (a.T + p.split - 1) / p.split * kRowsM * 4, 1024);
+        p.v_off = off;
+        off = round_up(off + (a.T + p.split - 1) / p.split * a.r * 4, 1024);
         p.lring_off = off;
         const int lstage = kRowsM * a.r * 2;
-        p.lora_stages = kProjSmem - 1024 - off - kLoraStages * lstage >= 3 * kStageBytes ? kLoraStages : 1;
+        // 64 KB of B_a in flight, one tile at least, and three stages of W beside them where they fit
+        p.lora_stages = a.r > 0 ? std::min({kLoraStages, 65536 / lstage, (a.T + p.split - 1) / p.split}) : 1;
+        while (p.lora_stages > 1 && kProjSmem - 1024 - off - p.lora_stages * lstage < 3 * kStageBytes) --p.lora_stages;
         off = round_up(off + p.lora_stages * lstage, 1024);
         p.wring_off = off;
         p.stages = std::min(kMaxStages, (kProjSmem - 1024 - off) / kStageBytes);
@@ -584,8 +621,11 @@ cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s) {
     const bool f32 = a.x_dt == MOE_DTYPE_F32;
     if (a.r > 0 || f32) {
         const int split_blocks = f32 ? std::min(4 * device_sm_count(), (a.T * a.d / 8 + kShrinkThreads - 1) / kShrinkThreads) : 0;
-        const cudaError_t e = launch_pdl(lora_shrink_kernel, dim3((unsigned)(a.T * (a.r / kShrinkRows) + split_blocks)),
-                                         dim3(kShrinkThreads), 0, s, a);
+        // few products: 2 rows of A per block, so that more SMs share the reading
+        const bool few = a.T * a.r / 8 < 4 * device_sm_count();
+        const int rows = few ? 2 : 8;
+        const cudaError_t e = launch_pdl(few ? lora_shrink_kernel<2> : lora_shrink_kernel<8>,
+                                         dim3((unsigned)(a.T * (a.r / rows) + split_blocks)), dim3(kShrinkThreads), 0, s, a);
         if (e != cudaSuccess) return e;
     }
     ProjArgs p = {};
