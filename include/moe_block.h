@@ -171,8 +171,9 @@ size_t moe_lora_workspace_bytes(int T, int d, int r);
  *   adapter    int32[T]
  *   y          [T, N] F32 or BF16, row stride y_ld
  * F32 activations enter the tensor cores as three bf16 terms (exact to 2^-24);
- * A_a x[t] stays in fp32.
- * Limits: d a multiple of 8 (16 for E4M3) up to 32768, N of 8, r of 8 up to 128;
+ * so does v = lora_scale A_a x[t] in the second product.
+ * Limits: d a multiple of 8 (16 for E4M3) up to 32768, N of 8, r of 8 up to 128,
+ * n_adapters * N < 2^31;
  * pointers 16-byte aligned, row strides of x and w multiples of 16 bytes.
  */
 int moe_lora_project(const void* x, int x_dtype, int64_t x_ld, const float* x_scale, int T, int d,

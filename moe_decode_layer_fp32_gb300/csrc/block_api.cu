@@ -1,5 +1,6 @@
 // C ABI of the decode-block operators: host-side argument checks and launches.
 // See include/moe_block.h for the contract of each call.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -196,6 +197,8 @@ int moe_lora_project(const void* x, int x_dtype, int64_t x_ld, const float* x_sc
     if (r % 8 != 0 || r > moe::kLoraMaxRank || r < 0)
         return api_fail(r < 0 || r % 8 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED, "%s: r=%d must be a multiple of 8 up to %d",
                         who, r, moe::kLoraMaxRank);
+    if (has && (long long)n_adapters * std::max(N, r) > INT_MAX)
+        return api_fail(MOE_ERR_UNSUPPORTED, "%s: %d adapters of N=%d rows exceed 2^31 rows", who, n_adapters, N);
     if (T == 0) return MOE_OK;
     int rc;
     const int xstep = x_dtype == MOE_DTYPE_F32 ? 4 : step;

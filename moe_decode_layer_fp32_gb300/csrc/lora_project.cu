@@ -35,7 +35,7 @@ constexpr int kWBytes = kRowsM * kBlockBytes;
 constexpr int kChunkBlocks = 4;             // stages per accumulator block
 constexpr int kMaxStages = 12;
 constexpr int kLoraStages = 8;              // at most
-constexpr int kLoraTokens = 4;              // tokens of an adapter taken together
+constexpr int kLoraBox = kRowsM * 128;       // 128 rows x 64 columns of B_a
 constexpr int kProjThreads = 384;           // 12 warps: TMA, MMA, adapter copies, idle, 4 adapter, 4 epilogue
 constexpr int kProjSmem = 226 * 1024;
 
@@ -64,15 +64,17 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
 }
 
 constexpr int kShrinkThreads = 256;
+constexpr int kShrinkTc = 1024;             // tokens times rank from which A x goes to the tensor cores
 
 // Blocks [0, T r / ROWS): ROWS rows of A_a against x[t], d shared out over the block's
-// threads.  The blocks after them write the terms of x.
+// threads.  The blocks after them write the terms of x: three bf16 of fp32, one of E4M3
+// (which bf16 holds exactly).
 template <int ROWS>
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ LoraArgs a, int shrink_blocks) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_allow_dependents();
     pdl_wait_primary();
-    const int groups = a.r / ROWS, shrink_blocks = a.T * groups;
+    const int groups = a.r / ROWS;
     if ((int)blockIdx.x >= shrink_blocks) {
         const int chunks = a.d / 8;
         const long long plane = (long long)a.T * a.d;
@@ -80,9 +82,9 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
              i += (gridDim.x - shrink_blocks) * kShrinkThreads) {
             const int t = i / chunks, c = (i - t * chunks) * 8;
             float f[8];
-            load8_f32(a.x, MOE_DTYPE_F32, t * a.x_ld + c, f);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
+            load8_any(a.x, a.x_dt, t * a.x_ld + c, f);
+            const int terms = a.x_dt == MOE_DTYPE_F32 ? 3 : 1;
+            for (int p = 0; p < terms; ++p) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -139,7 +141,8 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
 
 struct ProjArgs {
     LoraArgs l;
-    CUtensorMap wmap, xmap;     // W [N, d]; x [T, d], or its terms [3, T, d]
+    CUtensorMap wmap, xmap;     // W [N, d] (shrink: A [na r, d], boxes of r rows); x [T, d], or its terms [3, T, d]
+    CUtensorMap bmap;           // B [na N, r]
     int blocks;                 // 128-byte blocks of a row
     int split;                  // CTAs of a cluster
     int stages, lora_stages;
@@ -182,46 +185,38 @@ struct ProjShared {
     uint64_t mma_done;
     uint32_t tmem;
     int key[kLoraMaxT];        // adapter of each token
+    int index[kLoraMaxT];      // its place among the adapters in use, by number (-1: none)
+    int used[kLoraMaxT];       // the adapters in use
+    int count;                 // how many
     int order[kLoraMaxT];      // tokens by adapter (those without first), then by index
 };
 
-// out[k][128] = the thread's row of B_a times v[k], for TOK tokens.  The lanes start at different
-// 16-byte chunks of their rows (distinct banks); four pairs of sums per token keep the
-// multiply-adds independent.
-template <int TOK>
-__device__ __forceinline__ void lora_rows(const uint4* row, const float* v, int r, int C, int m, float* out) {
-    float2 acc[TOK][4];
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// f as three bf16 terms (an infinite or NaN first term stands alone).
+__device__ __forceinline__ void split3(float f, __nv_bfloat16 (&t)[3]) {
 #pragma unroll
-    for (int k = 0; k < TOK; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[k][e] = make_float2(0.0f, 0.0f);
-    int c = m % C;
-#pragma unroll 4
-    for (int j = 0; j < C; ++j) {
-        float2 b[4];
-        unpack_bf16x8_f2(row[c], b);
-#pragma unroll
-        for (int k = 0; k < TOK; ++k) {
-            const float4* u = reinterpret_cast<const float4*>(v + k * r + c * 8);
-            const float4 x = u[0], y = u[1];
-            acc[k][0] = ffma2(b[0], make_float2(x.x, x.y), acc[k][0]);
-            acc[k][1] = ffma2(b[1], make_float2(x.z, x.w), acc[k][1]);
-            acc[k][2] = ffma2(b[2], make_float2(y.x, y.y), acc[k][2]);
-            acc[k][3] = ffma2(b[3], make_float2(y.z, y.w), acc[k][3]);
-        }
-        c = c + 1 == C ? 0 : c + 1;
-    }
-#pragma unroll
-    for (int k = 0; k < TOK; ++k) {
-        const float2 s = make_float2((acc[k][0].x + acc[k][1].x) + (acc[k][2].x + acc[k][3].x),
-                                     (acc[k][0].y + acc[k][1].y) + (acc[k][2].y + acc[k][3].y));
-        out[k * kRowsM] = s.x + s.y;
+    for (int p = 0; p < 3; ++p) {
+        t[p] = __float2bfloat16_rn(f);
+        const float b = __bfloat162float(t[p]);
+        f = fabsf(b) <= 3.4028234e38f ? f - b : 0.0f;
     }
 }
 
+// Stride of a token's v terms in shared memory: whole k16 steps, and 16 bytes more so that
+// tokens fall on different banks.
+__host__ __device__ inline int v_stride(int r) { return (r + 15) / 16 * 16 + 8; }
+
 // TP: tokens rounded up to 16, 32, 64 or 128 (MMA columns).  F8: E4M3.  TERMS: bf16
-// terms of x (1, or 3 for fp32).
-template <int TP, bool F8, int TERMS>
+// terms of x (1, or 3 for fp32).  SHRINK: the same stream over the rows of A in the place
+// of W, as many whole adapters in use per tile as 128 rows hold; each token keeps the
+// rows of its own, v[t] = A_a x[t].
+template <int TP, bool F8, int TERMS, bool SHRINK>
 __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __grid_constant__ ProjArgs p) {
     constexpr int kAccs = TERMS > 1 ? 2 : 1;                  // the first term's sum, and the others'
     constexpr uint32_t kBufCols = kAccs * TP;
@@ -233,14 +228,15 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     ProjShared& sm = *reinterpret_cast<ProjShared*>(base);
     float* lacc = reinterpret_cast<float*>(base + p.lacc_off);       // [own tokens][128] adapter part
-    float* vs = reinterpret_cast<float*>(base + p.v_off);            // [own tokens][r] v, times the adapter's scale
+    // [3][own tokens][v_stride]: bf16 terms of v times the adapter's scale
+    __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(base + p.v_off);
     unsigned char* lring = base + p.lring_off;
     unsigned char* ring = base + p.wring_off;
     float* red = reinterpret_cast<float*>(ring);                     // after the stream: [T][128] this CTA's sums
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = p.split > 1 ? (int)cluster_rank() : 0;
-    const int n0 = (int)(blockIdx.x / p.split) * kRowsM;
+    const int tile = (int)(blockIdx.x / p.split), n0 = SHRINK ? 0 : tile * kRowsM;
     const int kb0 = p.blocks * rank / p.split, kb1 = p.blocks * (rank + 1) / p.split;
     const int nkb = kb1 - kb0, chunks = (nkb + kChunkBlocks - 1) / kChunkBlocks;
     // positions of the sorted tokens that this CTA adds up and writes
@@ -263,6 +259,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         mbar_init_fence();
         tma_prefetch_map(&p.wmap);
         tma_prefetch_map(&p.xmap);
+        if (!SHRINK && a.r > 0) tma_prefetch_map(&p.bmap);
     }
     if (warp == 1) {
         tmem_alloc(&sm.tmem, kTmemCols);
@@ -286,13 +283,24 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     // ---- TMA producer, first part: W of the first stages, before x is there
     const uint64_t pol = l2_policy_evict_first();
     constexpr int kColsPerBlock = F8 ? 128 : 64;
+    const int early = min(nkb, p.stages);
+    // shrink: the tile's adapters are used[first_ad .. + ads)
+    const int per_tile = SHRINK ? kRowsM / a.r : 0, first_ad = tile * per_tile;
+    int ads = 0;
     auto load_w = [&](int i) {
         const int slot = i % p.stages;
-        mbar_arrive_expect_tx(&sm.full[slot], kStageBytes);
-        tma_load_2d(ring + slot * kStageBytes, &p.wmap, (kb0 + i) * kColsPerBlock, n0, &sm.full[slot], pol);
+        unsigned char* dst = ring + slot * kStageBytes;
+        if constexpr (SHRINK) {
+            mbar_arrive_expect_tx(&sm.full[slot], kStageBytes - kWBytes + ads * a.r * kBlockBytes);
+            for (int k = 0; k < ads; ++k)
+                tma_load_2d(dst + k * a.r * kBlockBytes, &p.wmap, (kb0 + i) * kColsPerBlock, sm.used[first_ad + k] * a.r,
+                            &sm.full[slot], pol);
+        } else {
+            mbar_arrive_expect_tx(&sm.full[slot], kStageBytes);
+            tma_load_2d(dst, &p.wmap, (kb0 + i) * kColsPerBlock, n0, &sm.full[slot], pol);
+        }
     };
-    const int early = min(nkb, p.stages);
-    if (warp == 0 && lane == 0)
+    if (!SHRINK && warp == 0 && lane == 0)
         for (int i = 0; i < early; ++i) load_w(i);
 
     pdl_wait_primary();
@@ -308,24 +316,47 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             sm.order[pos] = t;
         }
         __syncthreads();
-        for (int i = tid; i < (p1 - p0) * (a.r / 4); i += kProjThreads) {
-            const int q = i / (a.r / 4), j = i - q * (a.r / 4), t = sm.order[p0 + q], ad = sm.key[t];
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (ad >= 0) {
-                const float f = a.ls[ad];
-                v = *reinterpret_cast<const float4*>(a.v + t * a.r + j * 4);
-                v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+        if constexpr (SHRINK) {
+            // a sorted token whose adapter differs from the one before starts an adapter in use
+            for (int q = tid; q < a.T; q += kProjThreads) {
+                const int k = sm.key[sm.order[q]];
+                int index = -1, last = -1;
+                for (int u = 0; u <= q; ++u) {
+                    const int ku = sm.key[sm.order[u]];
+                    index += ku >= 0 && ku != last;
+                    last = ku;
+                }
+                sm.index[sm.order[q]] = k >= 0 ? index : -1;
+                if (k >= 0) sm.used[index] = k;
+                if (q == a.T - 1) sm.count = index + 1;
             }
-            reinterpret_cast<float4*>(vs)[i] = v;
+            __syncthreads();
+            ads = max(0, min(per_tile, sm.count - first_ad));
+        } else {
+            const int vstr = v_stride(a.r), own = p1 - p0;
+            for (int i = tid; i < own * (vstr / 2); i += kProjThreads) {
+                const int q = i / (vstr / 2), j = (i - q * (vstr / 2)) * 2, t = sm.order[p0 + q], ad = sm.key[t];
+                __nv_bfloat16 t0[3] = {}, t1[3] = {};
+                if (ad >= 0 && j < a.r) {
+                    const float f = a.ls[ad];
+                    const float2 v = *reinterpret_cast<const float2*>(a.v + t * a.r + j);
+                    split3(v.x * f, t0);
+                    split3(v.y * f, t1);
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<__nv_bfloat162*>(vs + (k * own + q) * vstr + j) = __halves2bfloat162(t0[k], t1[k]);
+            }
         }
     } else {
         for (int t = tid; t < a.T; t += kProjThreads) sm.order[t] = t;
     }
     __syncthreads();
+    const bool idle = SHRINK && ads == 0;          // a tile beyond the adapters in use
 
     if (warp == 0) {
         // ===================== TMA producer =====================
-        if (lane == 0) {
+        if (lane == 0 && !idle) {
             auto load_x = [&](int i) {
                 const int slot = i % p.stages;
                 unsigned char* dst = ring + slot * kStageBytes + kWBytes;
@@ -333,7 +364,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                 for (int t = 0; t < TERMS; ++t)
                     tma_load_3d_plain(dst + t * kXBytes, &p.xmap, (kb0 + i) * kColsPerBlock, 0, t, &sm.full[slot]);
             };
-            for (int i = 0; i < early; ++i) load_x(i);
+            for (int i = 0; i < early; ++i) {
+                if (SHRINK) load_w(i);
+                load_x(i);
+            }
             int i = early;
             for (; i < nkb; ++i) {
                 if (!wait(&sm.empty[i % p.stages], ((i / p.stages) & 1u) ^ 1u)) break;
@@ -349,7 +383,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             const uint64_t a0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
             const uint64_t b0 = smem_desc_sw128(smem_u32(ring + kWBytes), 16, 1024);
             const uint32_t idesc = F8 ? idesc_e4m3_f32(128, TP) : idesc_bf16_f32(128, TP, false, false);
-            for (int c = 0; ok && c < chunks; ++c) {
+            for (int c = 0; ok && !idle && c < chunks; ++c) {
                 const uint32_t buf = c & 1;
                 if (!wait(&sm.acc_empty[buf], ((c >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after_sync();
@@ -379,9 +413,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         }
     } else if (warp == 2) {
         // ===================== adapter copies =====================
-        if (lane == 0 && a.r > 0) {
-            const uint32_t bytes = (uint32_t)min(kRowsM, a.N - n0) * a.r * 2;
-            const int lstage = kRowsM * a.r * 2;
+        if (!SHRINK && lane == 0 && a.r > 0) {
+            const int boxes = (a.r + 63) / 64;
             int it = 0, last = -1;
             for (int q = p0; q < p1; ++q) {
                 const int ad = sm.key[sm.order[q]];
@@ -389,37 +422,65 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                 last = ad;
                 const int slot = it % p.lora_stages;
                 if (!wait(&sm.lempty[slot], ((it / p.lora_stages) & 1u) ^ 1u)) break;
-                mbar_arrive_expect_tx(&sm.lfull[slot], bytes);
-                bulk_load(lring + slot * lstage, a.lb + ((long long)ad * a.N + n0) * a.r, bytes, &sm.lfull[slot], pol);
+                mbar_arrive_expect_tx(&sm.lfull[slot], boxes * kLoraBox);
+                for (int b = 0; b < boxes; ++b)
+                    tma_load_2d(lring + (slot * boxes + b) * kLoraBox, &p.bmap, b * 64, ad * a.N + n0, &sm.lfull[slot], pol);
                 ++it;
             }
             for (int j = max(0, it - p.lora_stages); j < it; ++j)
                 mbar_wait_bounded(&sm.lfull[j % p.lora_stages], (j / p.lora_stages) & 1u);
         }
     } else if (warp >= 4 && warp < 8) {
-        // ===================== adapters: s B_a v on the CUDA cores =====================
-        if (a.r > 0) {
-            const int m = (warp - 4) * 32 + lane, C = a.r / 8;
-            const int lstage = kRowsM * a.r * 2;
+        // ===================== adapters: B_a v, 32 rows a warp, up to 8 tokens of an adapter =====================
+        if (!SHRINK && a.r > 0) {
+            const int m0 = (warp - 4) * 32, boxes = (a.r + 63) / 64, steps = (a.r + 15) / 16;
+            const int vstr = v_stride(a.r), own = p1 - p0;
+            // ldmatrix: lane's row and 16-byte chunk within a 16 x 16 block
+            const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
             int it = 0;
             for (int q = p0; q < p1;) {
                 const int ad = sm.key[sm.order[q]];
                 if (ad < 0) {
-                    lacc[(q - p0) * kRowsM + m] = 0.0f;
+                    lacc[(q - p0) * kRowsM + m0 + lane] = 0.0f;
                     ++q;
                     continue;
                 }
                 const int slot = it % p.lora_stages;
                 wait(&sm.lfull[slot], (it / p.lora_stages) & 1u);
-                const uint4* row = reinterpret_cast<const uint4*>(lring + slot * lstage) + m * C;
+                __syncwarp();
+                const uint32_t tile_b = smem_u32(lring + slot * boxes * kLoraBox);
                 while (q < p1 && sm.key[sm.order[q]] == ad) {
                     int count = 1;
-                    while (count < kLoraTokens && q + count < p1 && sm.key[sm.order[q + count]] == ad) ++count;
-                    const float* v0 = vs + (q - p0) * a.r;
-                    if (count == 1) lora_rows<1>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
-                    else if (count == 2) lora_rows<2>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
-                    else if (count == 3) lora_rows<3>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
-                    else lora_rows<4>(row, v0, a.r, C, m, lacc + (q - p0) * kRowsM + m);
+                    while (count < 8 && q + count < p1 && sm.key[sm.order[q + count]] == ad) ++count;
+                    float c[2][4] = {};
+                    const __nv_bfloat16* v = vs + (q - p0 + lane / 4) * vstr + (lane & 3) * 2;
+                    const bool mine = lane / 4 < count;
+                    for (int ks = 0; ks < steps; ++ks) {
+                        uint32_t b[3][2] = {};
+                        if (mine) {
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) {
+                                b[k][0] = *reinterpret_cast<const uint32_t*>(v + k * own * vstr + ks * 16);
+                                b[k][1] = *reinterpret_cast<const uint32_t*>(v + k * own * vstr + ks * 16 + 8);
+                            }
+                        }
+                        const int ch = (ks & 3) * 2 + lch;
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            const int row = m0 + mt * 16 + lrow;
+                            uint32_t f[4];
+                            ldmatrix_x4(tile_b + (ks >> 2) * kLoraBox + row * 128 + ((ch ^ (row & 7)) << 4), f);
+#pragma unroll
+                            for (int k = 2; k >= 0; --k) mma_bf16(c[mt], f[0], f[1], f[2], f[3], b[k][0], b[k][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int tok = (lane & 3) * 2 + (e & 1), row = m0 + mt * 16 + lane / 4 + (e >> 1) * 8;
+                            if (tok < count) lacc[(q - p0 + tok) * kRowsM + row] = c[mt][e];
+                        }
                     q += count;
                 }
                 __syncwarp();
@@ -433,7 +494,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 #pragma unroll
         for (int t = 0; t < TP; ++t) acc[t] = 0.0f;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = 0; c < chunks && !idle; ++c) {
             const uint32_t buf = c & 1;
             if (!__all_sync(0xffffffffu, wait(&sm.acc_full[buf], (c >> 1) & 1u))) break;
             tc_fence_after_sync();
@@ -462,11 +523,18 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     tc_fence_after_sync();
 
     // ---- the cluster's sum of this CTA's tokens, scales, adapter part, output
-    const int warps = kProjThreads / 32, n = n0 + lane * 4;
+    const int warps = kProjThreads / 32;
     for (int q = p0 + warp; q < p1; q += warps) {
         const int t = sm.order[q];
+        int col = lane * 4;                      // of the tile's 128 rows
+        if constexpr (SHRINK) {
+            const int k = sm.index[t] - first_ad;
+            if (sm.index[t] < 0 || k < 0 || k >= ads || col >= a.r) continue;
+            col += k * a.r;
+        }
+        const int n = n0 + col;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float* at = red + t * kRowsM + lane * 4;
+        const float* at = red + t * kRowsM + col;
         if (p.split > 1) {
 #pragma unroll 8
             for (int k = 0; k < p.split; ++k) {
@@ -476,7 +544,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         } else {
             s = *reinterpret_cast<const float4*>(at);
         }
-        if (n < a.N) {
+        if constexpr (SHRINK) {
+            const float f = a.x_scale ? a.x_scale[t] : 1.0f;
+            *reinterpret_cast<float4*>(a.v + t * a.r + lane * 4) = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+        } else if (n < a.N) {
             if constexpr (F8) {
                 const float xs = a.x_scale[t];
                 s.x *= xs * a.w_scale[n];
@@ -520,7 +591,7 @@ EncodeTiledFn encode_tiled() {
 
 // [planes, rows, d] row-major with row stride ld: boxes of 128 bytes x box_rows, 128 B swizzle.
 // What lies beyond d or the rows reads as zero.
-bool encode_rows(CUtensorMap* m, const void* ptr, int planes, int rows, int d, long long ld, int box_rows, bool f8) {
+bool encode_rows(CUtensorMap* m, const void* ptr, int planes, long long rows, int d, long long ld, int box_rows, bool f8) {
     const EncodeTiledFn fn = encode_tiled();
     if (!fn) return false;
     const cuuint64_t es = f8 ? 1 : 2;
@@ -536,40 +607,45 @@ bool encode_rows(CUtensorMap* m, const void* ptr, int planes, int rows, int d, l
 
 inline int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
-template <int TP, bool F8, int TERMS>
+template <int TP, bool F8, int TERMS, bool SHRINK>
 cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     const LoraArgs& a = p.l;
     constexpr int kStageBytes = kWBytes + TERMS * TP * kBlockBytes;
-    auto kern = lora_project_kernel<TP, F8, TERMS>;
+    auto kern = lora_project_kernel<TP, F8, TERMS, SHRINK>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kProjSmem);
     if (e != cudaSuccess) return e;
-    const int tiles = (a.N + kRowsM - 1) / kRowsM, sms = device_sm_count();
+    const int sms = device_sm_count();
+    // shrink: at most min(T, na) adapters are in use
+    const int per_tile = SHRINK ? kRowsM / a.r : 1;
+    const int tiles = SHRINK ? (std::min(a.T, a.na) + per_tile - 1) / per_tile : (a.N + kRowsM - 1) / kRowsM;
+    const bool low = !SHRINK && a.r > 0;
     p.blocks = (a.d * (F8 ? 1 : 2) + kBlockBytes - 1) / kBlockBytes;
     // Split d while the clusters still run at once (a cluster of 8 does not fill a
     // GPC: about 7/8 of the SMs) and a CTA keeps two blocks or more.
     p.split = 1;
     for (int k = 2; k <= 8; k *= 2)
         if (tiles * k <= (k == 8 ? sms * 13 / 16 : sms) && p.blocks / k >= 2) p.split = k;
-    // Shared memory: control words, adapter part of the own tokens, B_a ring, W ring (whose
-    // place the CTA's sums take at the end).
+    // Shared memory: control words, adapter part of the own tokens, their v, B_a ring, W ring
+    // (whose place the CTA's sums take at the end).
+    const int lstage = low ? (a.r + 63) / 64 * kLoraBox : 0;
     auto plan = [&] {
+        const int own = (a.T + p.split - 1) / p.split;
         int off = round_up((int)sizeof(ProjShared), 1024);
         p.lacc_off = off;
-        if (a.r > 0) off = round_up(off + (a.T + p.split - 1) / p.split * kRowsM * 4, 1024);
+        if (low) off = round_up(off + own * kRowsM * 4, 1024);
         p.v_off = off;
-        off = round_up(off + (a.T + p.split - 1) / p.split * a.r * 4, 1024);
+        if (low) off = round_up(off + 3 * own * v_stride(a.r) * 2, 1024);
         p.lring_off = off;
-        const int lstage = kRowsM * a.r * 2;
         // 64 KB of B_a in flight, one tile at least, and three stages of W beside them where they fit
-        p.lora_stages = a.r > 0 ? std::min({kLoraStages, 65536 / lstage, (a.T + p.split - 1) / p.split}) : 1;
+        p.lora_stages = low ? std::min({kLoraStages, 65536 / lstage, own}) : 1;
         while (p.lora_stages > 1 && kProjSmem - 1024 - off - p.lora_stages * lstage < 3 * kStageBytes) --p.lora_stages;
-        off = round_up(off + p.lora_stages * lstage, 1024);
+        off += p.lora_stages * lstage;
         p.wring_off = off;
         p.stages = std::min(kMaxStages, (kProjSmem - 1024 - off) / kStageBytes);
     };
     plan();
-    if (p.stages < 2 && p.split == 1 && p.blocks >= 2) {
-        p.split = 2;     // half the own tokens: room for the ring
+    while (p.stages < 2 && p.split < 8) {
+        p.split *= 2;     // fewer own tokens: room for the ring
         plan();
     }
     p.stages = std::min(p.stages, (p.blocks + p.split - 1) / p.split);
@@ -578,10 +654,14 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     const size_t smem = std::max((size_t)(1024 + p.wring_off + std::max(p.stages * kStageBytes, a.T * kRowsM * 4)),
                                  (size_t)116 * 1024);
     if (p.stages < 1 || smem > (size_t)kProjSmem) return cudaErrorInvalidConfiguration;
-    const bool three = TERMS == 3;
-    if (!encode_rows(&p.wmap, a.w, 0, a.N, a.d, a.w_ld, kRowsM, F8) ||
-        !encode_rows(&p.xmap, three ? (const void*)a.xs : a.x, three ? 3 : 1, a.T, a.d, three ? a.d : a.x_ld, TP, F8))
-        return cudaErrorInvalidValue;
+    // fp32 x comes as its terms, and so does E4M3 x for the bf16 rows of A
+    const bool terms = TERMS == 3 || (SHRINK && a.x_dt == MOE_DTYPE_FP8_E4M3);
+    const bool maps =
+        (SHRINK ? encode_rows(&p.wmap, a.la, 0, (long long)a.na * a.r, a.d, a.d, a.r, false)
+                : encode_rows(&p.wmap, a.w, 0, a.N, a.d, a.w_ld, kRowsM, F8)) &&
+        encode_rows(&p.xmap, terms ? (const void*)a.xs : a.x, TERMS, a.T, a.d, terms ? a.d : a.x_ld, TP, F8) &&
+        (!low || encode_rows(&p.bmap, a.lb, 0, (long long)a.na * a.N, a.r, a.r, kRowsM, false));
+    if (!maps) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * p.split));
     cfg.blockDim = dim3(kProjThreads);
@@ -598,13 +678,14 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <bool F8, int TERMS>
-cudaError_t launch_tp(ProjArgs& p, cudaStream_t s) {
-    const int T = p.l.T;
-    if (T <= 16) return launch_project<16, F8, TERMS>(p, s);
-    if (T <= 32) return launch_project<32, F8, TERMS>(p, s);
-    if (T <= 64) return launch_project<64, F8, TERMS>(p, s);
-    return launch_project<128, F8, TERMS>(p, s);
+template <bool F8, int TERMS, bool SHRINK>
+cudaError_t launch_tp(const LoraArgs& a, cudaStream_t s) {
+    ProjArgs p = {};
+    p.l = a;
+    if (a.T <= 16) return launch_project<16, F8, TERMS, SHRINK>(p, s);
+    if (a.T <= 32) return launch_project<32, F8, TERMS, SHRINK>(p, s);
+    if (a.T <= 64) return launch_project<64, F8, TERMS, SHRINK>(p, s);
+    return launch_project<128, F8, TERMS, SHRINK>(p, s);
 }
 
 }  // namespace
@@ -618,20 +699,22 @@ size_t lora_workspace_bytes(int T, int d, int r, size_t* v_off, size_t* xs_off) 
 }
 
 cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s) {
-    const bool f32 = a.x_dt == MOE_DTYPE_F32;
-    if (a.r > 0 || f32) {
-        const int split_blocks = f32 ? std::min(4 * device_sm_count(), (a.T * a.d / 8 + kShrinkThreads - 1) / kShrinkThreads) : 0;
-        // few products: 2 rows of A per block, so that more SMs share the reading
-        const bool few = a.T * a.r / 8 < 4 * device_sm_count();
-        const int rows = few ? 2 : 8;
-        const cudaError_t e = launch_pdl(few ? lora_shrink_kernel<2> : lora_shrink_kernel<8>,
-                                         dim3((unsigned)(a.T * (a.r / rows) + split_blocks)), dim3(kShrinkThreads), 0, s, a);
-        if (e != cudaSuccess) return e;
-    }
-    ProjArgs p = {};
-    p.l = a;
-    if (a.x_dt == MOE_DTYPE_FP8_E4M3) return launch_tp<true, 1>(p, s);
-    return f32 ? launch_tp<false, 3>(p, s) : launch_tp<false, 1>(p, s);
+    const bool f32 = a.x_dt == MOE_DTYPE_F32, f8 = a.x_dt == MOE_DTYPE_FP8_E4M3;
+    // v = A_a x: many rows on the tensor cores, which read each adapter once for all its
+    // tokens; a few are done sooner by one small kernel, together with the terms of x.
+    const bool tc = a.T * a.r >= kShrinkTc;
+    const int split_blocks = f32 || (f8 && tc)
+                                 ? std::min(4 * device_sm_count(), (a.T * (a.d / 8) + kShrinkThreads - 1) / kShrinkThreads) : 0;
+    const bool few = a.T * a.r / 8 < 4 * device_sm_count();    // 2 rows of A per block: more SMs share the reading
+    const int shrink_blocks = tc ? 0 : a.T * (a.r / (few ? 2 : 8));
+    cudaError_t e = cudaSuccess;
+    if (shrink_blocks + split_blocks > 0)
+        e = launch_pdl(few ? lora_shrink_kernel<2> : lora_shrink_kernel<8>, dim3((unsigned)(shrink_blocks + split_blocks)),
+                       dim3(kShrinkThreads), 0, s, a, shrink_blocks);
+    if (e == cudaSuccess && tc) e = f32 ? launch_tp<false, 3, true>(a, s) : launch_tp<false, 1, true>(a, s);
+    if (e != cudaSuccess) return e;
+    if (f8) return launch_tp<true, 1, false>(a, s);
+    return f32 ? launch_tp<false, 3, false>(a, s) : launch_tp<false, 1, false>(a, s);
 }
 
 }  // namespace moe

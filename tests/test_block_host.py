@@ -171,6 +171,7 @@ LORA = dict(x=P, x_dt=BF16, x_ld=64, xs=None, T=2, d=64, w=P, w_dt=BF16, w_ld=64
     (dict(la=None), INVALID, "adapters"),
     (dict(ad=None), INVALID, "adapters"),
     (dict(na=0), INVALID, "adapters"),
+    (dict(na=1 << 27), UNSUPPORTED, "2^31"),
     (dict(la=P + 2), INVALID, "lora_a"),
     (dict(x=None), INVALID, "x null"),
     (dict(w=P + 8), INVALID, "w null or unaligned"),

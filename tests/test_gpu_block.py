@@ -592,6 +592,38 @@ def test_lora_adapter_mixes(B, kind, x):
     lora_case(B, T, 256, 264, x=x, na=na, adapter=ad, seed=1)
 
 
+@pytest.mark.parametrize("x", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("r", [8, 24, 64, 72, 128])
+def test_lora_many_tokens_and_ranks(B, x, r):
+    """Tokens times rank large enough for the tensor-core form of A x; adapters shared by many tokens or by
+    none, small and large d, ranks that do not divide 128."""
+    lora_case(B, 128, 16, 136, x=x, r=r, na=40, seed=r)
+    lora_case(B, 128, 1040, 264, x=x, r=r, na=3, y="bf16", seed=r)
+    lora_case(B, 77, 512, 128, x=x, r=r, na=100, adapter=[(t * 13) % 101 - 1 for t in range(77)], seed=r)
+    lora_case(B, 128, 256, 136, x=x, r=r, na=2, adapter=[1] * 128, seed=r)
+
+
+def test_lora_keeps_adapters_apart(B):
+    """An adapter of NaN and infinite weights spoils its own tokens alone, whichever kernel forms A x."""
+    for T, r in ((6, 8), (96, 64)):
+        g = gen(T)
+        na, d, N = 8, 256, 256
+        x, w = normal(g, T, d, dtype=torch.bfloat16), normal(g, N, d, dtype=torch.bfloat16)
+        lora = [normal(g, na, r, d, dtype=torch.bfloat16), normal(g, na, N, r, dtype=torch.bfloat16), torch.ones(na, device="cuda")]
+        lora[0][2], lora[1][2] = math.nan, math.nan
+        lora[0][5], lora[1][5] = math.inf, -math.inf
+        ad = torch.tensor([t % na for t in range(T)], dtype=torch.int32, device="cuda")
+        y = torch.empty(T, N, device="cuda")
+        B.moe_lora_project(x, w, y, B.new_lora_workspace(T, d, r), lora=tuple(lora), adapter=ad)
+        good = [t for t in range(T) if t % na not in (2, 5)]
+        clean = [lora[0].clone(), lora[1].clone(), lora[2]]
+        for i in (2, 5):
+            clean[0][i], clean[1][i] = 0, 0
+        want, size = O.lora_project(x, w, clean, ad)
+        assert_within(y[good], want[good], 64 * U * size[good], "the other tokens")
+        assert not torch.isfinite(y[[t for t in range(T) if t % na in (2, 5)]]).any()
+
+
 def test_lora_large(B):
     lora_case(B, 1, 7168, 9216, x="f32", seed=1)
     lora_case(B, 128, 7168, 7168, x="f32", y="bf16", r=64, na=20, seed=2)
