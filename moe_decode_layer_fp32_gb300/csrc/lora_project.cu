@@ -21,6 +21,7 @@
 // the adapter, and four warps multiply them with v in fp32 beside the MMAs.  A token
 // meets no weights but its own adapter's, whatever the others hold.
 #include <algorithm>
+#include <climits>
 
 #include "block.h"
 #include "tc_ptx.cuh"
@@ -184,11 +185,12 @@ struct ProjShared {
     uint64_t lfull[kLoraStages], lempty[kLoraStages];
     uint64_t mma_done;
     uint32_t tmem;
-    int key[kLoraMaxT];        // adapter of each token
-    int index[kLoraMaxT];      // its place among the adapters in use, by number (-1: none)
-    int used[kLoraMaxT];       // the adapters in use
-    int count;                 // how many
+    alignas(16) int key[kLoraMaxT];   // adapter of each token (beyond the tokens: INT_MAX)
     int order[kLoraMaxT];      // tokens by adapter (those without first), then by index
+    int skey[kLoraMaxT];       // their adapters in that order
+    int index[kLoraMaxT];      // ... and the adapters' places among those in use (-1: none)
+    int used[kLoraMaxT];       // the adapters in use
+    int starts[kLoraMaxT / 32];
 };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -208,6 +210,13 @@ __device__ __forceinline__ void split3(float f, __nv_bfloat16 (&t)[3]) {
     }
 }
 
+// Tiles of B_a (128 rows): ranks of whole k16 steps up to 48 come as one bulk copy of rows as they
+// lie; the others as boxes of 64 columns in 128-byte rows, zeros beyond the rank, whose
+// permuted chunks spare ldmatrix the bank conflicts.
+__host__ __device__ inline bool lora_bulk(int r) { return r <= 48 && r % 16 == 0; }
+__host__ __device__ inline int lora_stage_bytes(int r) {
+    return lora_bulk(r) ? kRowsM * r * 2 : (r + 63) / 64 * kLoraBox;
+}
 // Stride of a token's v terms in shared memory: whole k16 steps, and 16 bytes more so that
 // tokens fall on different banks.
 __host__ __device__ inline int v_stride(int r) { return (r + 15) / 16 * 16 + 8; }
@@ -307,35 +316,48 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 
     // ---- order of the tokens
     if (a.r > 0) {
-        for (int t = tid; t < a.T; t += kProjThreads) sm.key[t] = adapter_of(a, t);
+        if (tid < kLoraMaxT) sm.key[tid] = tid < a.T ? adapter_of(a, tid) : INT_MAX;
         __syncthreads();
-        for (int t = tid; t < a.T; t += kProjThreads) {
-            const int k = sm.key[t];
+        if (tid < a.T) {
+            const int k = sm.key[tid];
             int pos = 0;
-            for (int u = 0; u < a.T; ++u) pos += sm.key[u] < k || (sm.key[u] == k && u < t);
-            sm.order[pos] = t;
+#pragma unroll 8
+            for (int u = 0; u < kLoraMaxT; u += 4) {
+                const int4 w = *reinterpret_cast<const int4*>(sm.key + u);
+                pos += (w.x < k || (w.x == k && u < tid)) + (w.y < k || (w.y == k && u + 1 < tid)) +
+                       (w.z < k || (w.z == k && u + 2 < tid)) + (w.w < k || (w.w == k && u + 3 < tid));
+            }
+            sm.order[pos] = tid;
+            sm.skey[pos] = k;
         }
         __syncthreads();
         if constexpr (SHRINK) {
             // a sorted token whose adapter differs from the one before starts an adapter in use
-            for (int q = tid; q < a.T; q += kProjThreads) {
-                const int k = sm.key[sm.order[q]];
-                int index = -1, last = -1;
-                for (int u = 0; u <= q; ++u) {
-                    const int ku = sm.key[sm.order[u]];
-                    index += ku >= 0 && ku != last;
-                    last = ku;
-                }
-                sm.index[sm.order[q]] = k >= 0 ? index : -1;
-                if (k >= 0) sm.used[index] = k;
-                if (q == a.T - 1) sm.count = index + 1;
+            bool start = false;
+            uint32_t bits = 0u;
+            if (tid < kLoraMaxT) {
+                start = tid < a.T && sm.skey[tid] >= 0 && (tid == 0 || sm.skey[tid - 1] != sm.skey[tid]);
+                bits = __ballot_sync(0xffffffffu, start);
+                if (lane == 0) sm.starts[warp] = __popc(bits);
             }
             __syncthreads();
-            ads = max(0, min(per_tile, sm.count - first_ad));
+            int before = 0, count = 0;
+#pragma unroll
+            for (int w = 0; w < kLoraMaxT / 32; ++w) {
+                if (w < warp) before += sm.starts[w];
+                count += sm.starts[w];
+            }
+            if (tid < a.T) {
+                const int index = before + __popc(bits & (0xffffffffu >> (31 - lane))) - 1;
+                sm.index[tid] = sm.skey[tid] >= 0 ? index : -1;
+                if (start) sm.used[index] = sm.skey[tid];
+            }
+            __syncthreads();
+            ads = max(0, min(per_tile, count - first_ad));
         } else {
             const int vstr = v_stride(a.r), own = p1 - p0;
             for (int i = tid; i < own * (vstr / 2); i += kProjThreads) {
-                const int q = i / (vstr / 2), j = (i - q * (vstr / 2)) * 2, t = sm.order[p0 + q], ad = sm.key[t];
+                const int q = i / (vstr / 2), j = (i - q * (vstr / 2)) * 2, t = sm.order[p0 + q], ad = sm.skey[p0 + q];
                 __nv_bfloat16 t0[3] = {}, t1[3] = {};
                 if (ad >= 0 && j < a.r) {
                     const float f = a.ls[ad];
@@ -414,17 +436,23 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     } else if (warp == 2) {
         // ===================== adapter copies =====================
         if (!SHRINK && lane == 0 && a.r > 0) {
-            const int boxes = (a.r + 63) / 64;
+            const int boxes = (a.r + 63) / 64, lstage = lora_stage_bytes(a.r);
+            const uint32_t bulk = (uint32_t)min(kRowsM, a.N - n0) * a.r * 2;
             int it = 0, last = -1;
             for (int q = p0; q < p1; ++q) {
-                const int ad = sm.key[sm.order[q]];
+                const int ad = sm.skey[q];
                 if (ad < 0 || ad == last) continue;
                 last = ad;
                 const int slot = it % p.lora_stages;
                 if (!wait(&sm.lempty[slot], ((it / p.lora_stages) & 1u) ^ 1u)) break;
-                mbar_arrive_expect_tx(&sm.lfull[slot], boxes * kLoraBox);
-                for (int b = 0; b < boxes; ++b)
-                    tma_load_2d(lring + (slot * boxes + b) * kLoraBox, &p.bmap, b * 64, ad * a.N + n0, &sm.lfull[slot], pol);
+                if (lora_bulk(a.r)) {
+                    mbar_arrive_expect_tx(&sm.lfull[slot], bulk);
+                    bulk_load(lring + slot * lstage, a.lb + ((long long)ad * a.N + n0) * a.r, bulk, &sm.lfull[slot], pol);
+                } else {
+                    mbar_arrive_expect_tx(&sm.lfull[slot], boxes * kLoraBox);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(lring + slot * lstage + b * kLoraBox, &p.bmap, b * 64, ad * a.N + n0, &sm.lfull[slot], pol);
+                }
                 ++it;
             }
             for (int j = max(0, it - p.lora_stages); j < it; ++j)
@@ -433,13 +461,15 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     } else if (warp >= 4 && warp < 8) {
         // ===================== adapters: B_a v, 32 rows a warp, up to 8 tokens of an adapter =====================
         if (!SHRINK && a.r > 0) {
-            const int m0 = (warp - 4) * 32, boxes = (a.r + 63) / 64, steps = (a.r + 15) / 16;
+            const int m0 = (warp - 4) * 32, steps = (a.r + 15) / 16, lstage = lora_stage_bytes(a.r);
+            // rows of 128 bytes with permuted chunks, or of 2 r bytes as they are
+            const int pitch = lora_bulk(a.r) ? a.r * 2 : 128, swizzle = lora_bulk(a.r) ? 0 : 7;
             const int vstr = v_stride(a.r), own = p1 - p0;
             // ldmatrix: lane's row and 16-byte chunk within a 16 x 16 block
             const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
             int it = 0;
             for (int q = p0; q < p1;) {
-                const int ad = sm.key[sm.order[q]];
+                const int ad = sm.skey[q];
                 if (ad < 0) {
                     lacc[(q - p0) * kRowsM + m0 + lane] = 0.0f;
                     ++q;
@@ -448,13 +478,14 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                 const int slot = it % p.lora_stages;
                 wait(&sm.lfull[slot], (it / p.lora_stages) & 1u);
                 __syncwarp();
-                const uint32_t tile_b = smem_u32(lring + slot * boxes * kLoraBox);
-                while (q < p1 && sm.key[sm.order[q]] == ad) {
+                const uint32_t tile_b = smem_u32(lring + slot * lstage);
+                while (q < p1 && sm.skey[q] == ad) {
                     int count = 1;
-                    while (count < 8 && q + count < p1 && sm.key[sm.order[q + count]] == ad) ++count;
-                    float c[2][4] = {};
+                    while (count < 8 && q + count < p1 && sm.skey[q + count] == ad) ++count;
+                    float c[3][2][4] = {};          // a sum per term: short chains of MMAs
                     const __nv_bfloat16* v = vs + (q - p0 + lane / 4) * vstr + (lane & 3) * 2;
                     const bool mine = lane / 4 < count;
+#pragma unroll 4
                     for (int ks = 0; ks < steps; ++ks) {
                         uint32_t b[3][2] = {};
                         if (mine) {
@@ -469,9 +500,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                         for (int mt = 0; mt < 2; ++mt) {
                             const int row = m0 + mt * 16 + lrow;
                             uint32_t f[4];
-                            ldmatrix_x4(tile_b + (ks >> 2) * kLoraBox + row * 128 + ((ch ^ (row & 7)) << 4), f);
+                            ldmatrix_x4(tile_b + (ks >> 2) * kLoraBox + row * pitch + ((ch ^ (row & swizzle)) << 4), f);
 #pragma unroll
-                            for (int k = 2; k >= 0; --k) mma_bf16(c[mt], f[0], f[1], f[2], f[3], b[k][0], b[k][1]);
+                            for (int k = 0; k < 3; ++k) mma_bf16(c[k][mt], f[0], f[1], f[2], f[3], b[k][0], b[k][1]);
                         }
                     }
 #pragma unroll
@@ -479,7 +510,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int tok = (lane & 3) * 2 + (e & 1), row = m0 + mt * 16 + lane / 4 + (e >> 1) * 8;
-                            if (tok < count) lacc[(q - p0 + tok) * kRowsM + row] = c[mt][e];
+                            if (tok < count)
+                                lacc[(q - p0 + tok) * kRowsM + row] = c[0][mt][e] + (c[1][mt][e] + c[2][mt][e]);
                         }
                     q += count;
                 }
@@ -528,8 +560,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         const int t = sm.order[q];
         int col = lane * 4;                      // of the tile's 128 rows
         if constexpr (SHRINK) {
-            const int k = sm.index[t] - first_ad;
-            if (sm.index[t] < 0 || k < 0 || k >= ads || col >= a.r) continue;
+            const int k = sm.index[q] - first_ad;
+            if (sm.index[q] < 0 || k < 0 || k >= ads || col >= a.r) continue;
             col += k * a.r;
         }
         const int n = n0 + col;
@@ -627,7 +659,7 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
         if (tiles * k <= (k == 8 ? sms * 13 / 16 : sms) && p.blocks / k >= 2) p.split = k;
     // Shared memory: control words, adapter part of the own tokens, their v, B_a ring, W ring
     // (whose place the CTA's sums take at the end).
-    const int lstage = low ? (a.r + 63) / 64 * kLoraBox : 0;
+    const int lstage = low ? lora_stage_bytes(a.r) : 0;
     auto plan = [&] {
         const int own = (a.T + p.split - 1) / p.split;
         int off = round_up((int)sizeof(ProjShared), 1024);
@@ -639,7 +671,7 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
         // 64 KB of B_a in flight, one tile at least, and three stages of W beside them where they fit
         p.lora_stages = low ? std::min({kLoraStages, 65536 / lstage, own}) : 1;
         while (p.lora_stages > 1 && kProjSmem - 1024 - off - p.lora_stages * lstage < 3 * kStageBytes) --p.lora_stages;
-        off += p.lora_stages * lstage;
+        off = round_up(off + p.lora_stages * lstage, 1024);
         p.wring_off = off;
         p.stages = std::min(kMaxStages, (kProjSmem - 1024 - off) / kStageBytes);
     };
