@@ -35,7 +35,7 @@ constexpr int kBlockBytes = 128;            // bytes of a row per stage (one swi
 constexpr int kWBytes = kRowsM * kBlockBytes;
 constexpr int kChunkBlocks = 4;             // stages per accumulator block
 constexpr int kMaxStages = 12;
-constexpr int kLoraStages = 8;              // at most
+constexpr int kLoraStages = 16;             // at most
 constexpr int kLoraBox = kRowsM * 128;       // 128 rows x 64 columns of B_a
 constexpr int kProjThreads = 384;           // 12 warps: TMA, MMA, adapter copies, idle, 4 adapter, 4 epilogue
 constexpr int kProjSmem = 226 * 1024;
@@ -191,6 +191,7 @@ struct ProjShared {
     int index[kLoraMaxT];      // ... and the adapters' places among those in use (-1: none)
     int used[kLoraMaxT];       // the adapters in use
     int starts[kLoraMaxT / 32];
+    float scale[kLoraMaxT];    // adapters' scales, by sorted token
 };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -314,23 +315,34 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 
     pdl_wait_primary();
 
-    // ---- order of the tokens
-    if (a.r > 0) {
-        if (tid < kLoraMaxT) sm.key[tid] = tid < a.T ? adapter_of(a, tid) : INT_MAX;
-        __syncthreads();
-        if (tid < a.T) {
-            const int k = sm.key[tid];
+    // ---- order of the tokens: by the warps that need it first (the adapters' copies and
+    // products; in the shrink form the W copies too, so all of them), the others go ahead
+    const bool sorter = SHRINK || warp == 2 || (warp >= 4 && warp < 8);
+    constexpr int kSorters = SHRINK ? kProjThreads : 160;
+    const int sid = SHRINK ? tid : warp == 2 ? 128 + lane : tid - 128;
+    auto sort_sync = [&] { named_bar_sync(1, kSorters); };
+    if (a.r > 0 && sorter) {
+        float scale = 0.0f;
+        if (sid < kLoraMaxT) {
+            const int k = sid < a.T ? adapter_of(a, sid) : INT_MAX;
+            sm.key[sid] = k;
+            if (!SHRINK && sid < a.T && k >= 0) scale = a.ls[k];
+        }
+        sort_sync();
+        if (sid < a.T) {
+            const int k = sm.key[sid];
             int pos = 0;
 #pragma unroll 8
             for (int u = 0; u < kLoraMaxT; u += 4) {
                 const int4 w = *reinterpret_cast<const int4*>(sm.key + u);
-                pos += (w.x < k || (w.x == k && u < tid)) + (w.y < k || (w.y == k && u + 1 < tid)) +
-                       (w.z < k || (w.z == k && u + 2 < tid)) + (w.w < k || (w.w == k && u + 3 < tid));
+                pos += (w.x < k || (w.x == k && u < sid)) + (w.y < k || (w.y == k && u + 1 < sid)) +
+                       (w.z < k || (w.z == k && u + 2 < sid)) + (w.w < k || (w.w == k && u + 3 < sid));
             }
-            sm.order[pos] = tid;
+            sm.order[pos] = sid;
             sm.skey[pos] = k;
+            sm.scale[pos] = scale;
         }
-        __syncthreads();
+        sort_sync();
         if constexpr (SHRINK) {
             // a sorted token whose adapter differs from the one before starts an adapter in use
             bool start = false;
@@ -354,26 +366,39 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             }
             __syncthreads();
             ads = max(0, min(per_tile, count - first_ad));
-        } else {
+        } else if (warp != 2) {
             const int vstr = v_stride(a.r), own = p1 - p0;
-            for (int i = tid; i < own * (vstr / 2); i += kProjThreads) {
-                const int q = i / (vstr / 2), j = (i - q * (vstr / 2)) * 2, t = sm.order[p0 + q], ad = sm.skey[p0 + q];
-                __nv_bfloat16 t0[3] = {}, t1[3] = {};
-                if (ad >= 0 && j < a.r) {
-                    const float f = a.ls[ad];
-                    const float2 v = *reinterpret_cast<const float2*>(a.v + t * a.r + j);
-                    split3(v.x * f, t0);
-                    split3(v.y * f, t1);
+            // two elements of a token's v at a time, the loads of kAhead of them together
+            constexpr int kAhead = 6;
+            const int pairs = vstr / 2, n = own * pairs;
+            for (int i0 = sid; i0 < n; i0 += kAhead * 128) {
+                float2 v[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * 128, q = i / pairs, j = (i - q * pairs) * 2;
+                    v[u] = make_float2(0.0f, 0.0f);
+                    if (i < n && j < a.r && sm.skey[p0 + q] >= 0)
+                        v[u] = *reinterpret_cast<const float2*>(a.v + sm.order[p0 + q] * a.r + j);
                 }
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<__nv_bfloat162*>(vs + (k * own + q) * vstr + j) = __halves2bfloat162(t0[k], t1[k]);
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * 128, q = i / pairs, j = (i - q * pairs) * 2;
+                    if (i >= n) break;
+                    const float f = sm.scale[p0 + q];
+                    __nv_bfloat16 t0[3], t1[3];
+                    split3(v[u].x * f, t0);
+                    split3(v[u].y * f, t1);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        *reinterpret_cast<__nv_bfloat162*>(vs + (k * own + q) * vstr + j) = __halves2bfloat162(t0[k], t1[k]);
+                }
             }
+            named_bar_sync(2, 128);
         }
-    } else {
+    } else if (a.r == 0) {
         for (int t = tid; t < a.T; t += kProjThreads) sm.order[t] = t;
     }
-    __syncthreads();
+    if (SHRINK) __syncthreads();
     const bool idle = SHRINK && ads == 0;          // a tile beyond the adapters in use
 
     if (warp == 0) {
