@@ -190,6 +190,8 @@ struct ProjShared {
     int skey[kLoraMaxT];       // their adapters in that order
     int index[kLoraMaxT];      // ... and the adapters' places among those in use (-1: none)
     int used[kLoraMaxT];       // the adapters in use
+    int seg[kLoraMaxT + 1];    // projection: first sorted token of each adapter among the own tokens
+    int segs;
     int starts[kLoraMaxT / 32];
     float scale[kLoraMaxT];    // adapters' scales, by sorted token
 };
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         }
         for (int i = 0; i < kLoraStages; ++i) {
             mbar_init(&sm.lfull[i], 1);
-            mbar_init(&sm.lempty[i], 4);
+            mbar_init(&sm.lempty[i], 1);
         }
         mbar_init(&sm.mma_done, 1);
         mbar_init_fence();
@@ -343,30 +345,35 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             sm.scale[pos] = scale;
         }
         sort_sync();
-        if constexpr (SHRINK) {
-            // a sorted token whose adapter differs from the one before starts an adapter in use
-            bool start = false;
-            uint32_t bits = 0u;
-            if (tid < kLoraMaxT) {
-                start = tid < a.T && sm.skey[tid] >= 0 && (tid == 0 || sm.skey[tid - 1] != sm.skey[tid]);
-                bits = __ballot_sync(0xffffffffu, start);
-                if (lane == 0) sm.starts[warp] = __popc(bits);
-            }
-            __syncthreads();
+        // A sorted token whose adapter differs from the one before starts an adapter in use: of all
+        // tokens (shrink) or of the own ones.
+        {
+            const int q0 = SHRINK ? 0 : p0, q1 = SHRINK ? a.T : p1;
+            const bool start = sid < a.T && sid >= q0 && sid < q1 && sm.skey[sid] >= 0 &&
+                               (sid == q0 || sm.skey[sid - 1] != sm.skey[sid]);
+            const uint32_t bits = __ballot_sync(0xffffffffu, start);
+            if (sid < kLoraMaxT && lane == 0) sm.starts[sid / 32] = __popc(bits);
+            sort_sync();
             int before = 0, count = 0;
 #pragma unroll
             for (int w = 0; w < kLoraMaxT / 32; ++w) {
-                if (w < warp) before += sm.starts[w];
+                if (w < sid / 32) before += sm.starts[w];
                 count += sm.starts[w];
             }
-            if (tid < a.T) {
+            if (sid < a.T) {
                 const int index = before + __popc(bits & (0xffffffffu >> (31 - lane))) - 1;
-                sm.index[tid] = sm.skey[tid] >= 0 ? index : -1;
-                if (start) sm.used[index] = sm.skey[tid];
+                if (SHRINK) sm.index[sid] = sm.skey[sid] >= 0 ? index : -1;
+                if (start && SHRINK) sm.used[index] = sm.skey[sid];
+                if (start && !SHRINK) sm.seg[index] = sid;
             }
-            __syncthreads();
-            ads = max(0, min(per_tile, count - first_ad));
-        } else if (warp != 2) {
+            if (!SHRINK && sid == 0) {
+                sm.segs = count;
+                sm.seg[count] = p1;
+            }
+            sort_sync();
+            if (SHRINK) ads = max(0, min(per_tile, count - first_ad));
+        }
+        if (!SHRINK && warp != 2) {
             const int vstr = v_stride(a.r), own = p1 - p0;
             // two elements of a token's v at a time, the loads of kAhead of them together
             constexpr int kAhead = 6;
@@ -463,11 +470,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         if (!SHRINK && lane == 0 && a.r > 0) {
             const int boxes = (a.r + 63) / 64, lstage = lora_stage_bytes(a.r);
             const uint32_t bulk = (uint32_t)min(kRowsM, a.N - n0) * a.r * 2;
-            int it = 0, last = -1;
-            for (int q = p0; q < p1; ++q) {
-                const int ad = sm.skey[q];
-                if (ad < 0 || ad == last) continue;
-                last = ad;
+            int it = 0;
+            for (; it < sm.segs; ++it) {
+                const int ad = sm.skey[sm.seg[it]];
                 const int slot = it % p.lora_stages;
                 if (!wait(&sm.lempty[slot], ((it / p.lora_stages) & 1u) ^ 1u)) break;
                 if (lora_bulk(a.r)) {
@@ -478,71 +483,69 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                     for (int b = 0; b < boxes; ++b)
                         tma_load_2d(lring + slot * lstage + b * kLoraBox, &p.bmap, b * 64, ad * a.N + n0, &sm.lfull[slot], pol);
                 }
-                ++it;
             }
             for (int j = max(0, it - p.lora_stages); j < it; ++j)
                 mbar_wait_bounded(&sm.lfull[j % p.lora_stages], (j / p.lora_stages) & 1u);
         }
     } else if (warp >= 4 && warp < 8) {
-        // ===================== adapters: B_a v, 32 rows a warp, up to 8 tokens of an adapter =====================
+        // ===================== adapters: B_a v, an adapter per warp, up to 8 of its tokens at once =====================
         if (!SHRINK && a.r > 0) {
-            const int m0 = (warp - 4) * 32, steps = (a.r + 15) / 16, lstage = lora_stage_bytes(a.r);
+            const int steps = (a.r + 15) / 16, lstage = lora_stage_bytes(a.r);
             // rows of 128 bytes with permuted chunks, or of 2 r bytes as they are
             const int pitch = lora_bulk(a.r) ? a.r * 2 : 128, swizzle = lora_bulk(a.r) ? 0 : 7;
-            const int vstr = v_stride(a.r), own = p1 - p0;
+            const int vstr = v_stride(a.r), own = p1 - p0, segs = sm.segs;
             // ldmatrix: lane's row and 16-byte chunk within a 16 x 16 block
             const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
-            int it = 0;
-            for (int q = p0; q < p1;) {
-                const int ad = sm.skey[q];
-                if (ad < 0) {
-                    lacc[(q - p0) * kRowsM + m0 + lane] = 0.0f;
-                    ++q;
-                    continue;
-                }
-                const int slot = it % p.lora_stages;
+            for (int i = (warp - 4) * 32 + lane; i < (sm.seg[0] - p0) * kRowsM; i += 128) lacc[i] = 0.0f;
+            for (int it = 0; it < segs; ++it) {
+                // a slot belongs to one warp: a wait by parity holds only for a waiter that has seen
+                // the slot's phase before
+                const int slot = it % p.lora_stages, end = sm.seg[it + 1];
+                if (slot % 4 != warp - 4) continue;
                 wait(&sm.lfull[slot], (it / p.lora_stages) & 1u);
                 __syncwarp();
-                const uint32_t tile_b = smem_u32(lring + slot * lstage);
-                while (q < p1 && sm.skey[q] == ad) {
-                    int count = 1;
-                    while (count < 8 && q + count < p1 && sm.skey[q + count] == ad) ++count;
-                    float c[3][2][4] = {};          // a sum per term: short chains of MMAs
+                const uint32_t tile_b = smem_u32(lring + slot * lstage) + lrow * pitch;
+                for (int q = sm.seg[it]; q < end; q += 8) {
+                    const int count = min(8, end - q);
                     const __nv_bfloat16* v = vs + (q - p0 + lane / 4) * vstr + (lane & 3) * 2;
-                    const bool mine = lane / 4 < count;
-#pragma unroll 4
-                    for (int ks = 0; ks < steps; ++ks) {
-                        uint32_t b[3][2] = {};
-                        if (mine) {
+                    float* out = lacc + (q - p0 + (lane & 3) * 2) * kRowsM + lane / 4;
+                    const bool t0 = (lane & 3) * 2 < count, t1 = (lane & 3) * 2 + 1 < count;
+                    // up to 64 columns of B_a at a time: v's fragments stay in registers over the 128 rows
+                    for (int k0 = 0; k0 < steps; k0 += 4) {
+                        uint32_t b[4][3][2] = {};
+                        if (lane / 4 < count) {
 #pragma unroll
-                            for (int k = 0; k < 3; ++k) {
-                                b[k][0] = *reinterpret_cast<const uint32_t*>(v + k * own * vstr + ks * 16);
-                                b[k][1] = *reinterpret_cast<const uint32_t*>(v + k * own * vstr + ks * 16 + 8);
+                            for (int ks = 0; ks < 4; ++ks)
+                                if (k0 + ks < steps) {
+#pragma unroll
+                                    for (int k = 0; k < 3; ++k) {
+                                        b[ks][k][0] = *reinterpret_cast<const uint32_t*>(v + k * own * vstr + (k0 + ks) * 16);
+                                        b[ks][k][1] = *reinterpret_cast<const uint32_t*>(v + k * own * vstr + (k0 + ks) * 16 + 8);
+                                    }
+                                }
+                        }
+#pragma unroll 2
+                        for (int m = 0; m < kRowsM; m += 16) {
+                            float c[3][4] = {};             // a sum per term: short chains of MMAs
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                if (k0 + ks < steps) {
+                                    uint32_t f[4];
+                                    ldmatrix_x4(tile_b + (k0 >> 2) * kLoraBox + m * pitch + (((ks * 2 + lch) ^ (lrow & swizzle)) << 4), f);
+#pragma unroll
+                                    for (int k = 0; k < 3; ++k) mma_bf16(c[k], f[0], f[1], f[2], f[3], b[ks][k][0], b[ks][k][1]);
+                                }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float* at = out + (e & 1) * kRowsM + m + (e >> 1) * 8;
+                                const float s = c[0][e] + (c[1][e] + c[2][e]);
+                                if ((e & 1) ? t1 : t0) *at = k0 == 0 ? s : *at + s;
                             }
                         }
-                        const int ch = (ks & 3) * 2 + lch;
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt) {
-                            const int row = m0 + mt * 16 + lrow;
-                            uint32_t f[4];
-                            ldmatrix_x4(tile_b + (ks >> 2) * kLoraBox + row * pitch + ((ch ^ (row & swizzle)) << 4), f);
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) mma_bf16(c[k][mt], f[0], f[1], f[2], f[3], b[k][0], b[k][1]);
-                        }
                     }
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tok = (lane & 3) * 2 + (e & 1), row = m0 + mt * 16 + lane / 4 + (e >> 1) * 8;
-                            if (tok < count)
-                                lacc[(q - p0 + tok) * kRowsM + row] = c[0][mt][e] + (c[1][mt][e] + c[2][mt][e]);
-                        }
-                    q += count;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.lempty[slot]);
-                ++it;
             }
         }
     } else if (warp >= 8) {
