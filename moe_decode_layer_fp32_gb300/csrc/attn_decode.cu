@@ -47,6 +47,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t size) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
     return (uint32_t)h.x | ((uint32_t)h.y << 16);
@@ -99,6 +109,7 @@ struct Attn {
     static constexpr int KT = kPitch <= 128 ? 32 : 16;               // keys of a warp's tile
     static constexpr int kTileBytes = KT * kPitch;                   // K or V
     static constexpr int kTileKeys = KT * kAttnWarps;
+    static constexpr uint32_t kAllKeys = KT == 32 ? 0xffffffffu : (1u << (KT % 32)) - 1u;
     static constexpr int kChunks = kPitch / 16;                      // 16-byte chunks of a row
     static constexpr int kRowsPerIter = 32 / kChunks;
     static constexpr int kQTerms = EX ? (F8 ? 2 : 3) : 1;
@@ -127,6 +138,23 @@ struct Attn {
         if constexpr (kPitch == 64) return at_k(r, ch);
         return r * kPitch + ((ch ^ (r & 6)) << 4);
     }
+    // The lane's offsets within a stage, from which every address of a tile is a constant away.
+    struct Lane {
+        uint32_t k[2];     // reads K row lane / 4, chunk lane % 4, and the chunk 4 further on (in the permuted order)
+        uint32_t v[2];     // reads V row 2 (lane % 4) [+ 1], its chunk (8-byte piece) lane / 4
+        uint32_t wk, wv;   // writes row lane / kChunks, chunk lane % kChunks
+        __device__ __forceinline__ explicit Lane(int lane) {
+            const int row = lane / 4, col = lane % 4;
+            k[0] = at_k(row, col);
+            k[1] = kChunks > 4 ? at_k(row, 4 + col) : k[0];
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * col + e;
+                v[e] = kTileBytes + (kVElems * kElem == 16 ? at_v(r, row) : at_v(r, row / 2) + (row % 2) * 8);
+            }
+            wk = at_k(lane / kChunks, lane % kChunks);
+            wv = kTileBytes + at_v(lane / kChunks, lane % kChunks);
+        }
+    };
 
     __device__ static __forceinline__ void set_request(const AttnArgs& a, Cursor& c) {
         int n = max(a.seq_lens[c.b], 0);
@@ -151,7 +179,7 @@ struct Attn {
     __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
         const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
         if (c.left <= 0 || lane >= KT || key >= c.n) return make_int2(-1, 0);
-        const int col = key / a.c.page_size;
+        const int col = a.page_shift >= 0 ? key >> a.page_shift : key / a.c.page_size;
         const int page = a.table[c.b * a.table_ld + col];
         if (page < 0 || page >= a.c.num_pages) {
             set_status(a.status, MOE_ERR_DEVICE);
@@ -161,8 +189,8 @@ struct Attn {
     }
     // Start the copies of the warp's K and V rows of tile c into a stage; returns the
     // mask of the keys that count.  The rows of the others become zeros.
-    __device__ static __forceinline__ uint32_t issue(const AttnArgs& a, const Cursor& c, int2 place, int nsub, int warp,
-                                                     int lane, uint32_t stage) {
+    __device__ static __forceinline__ uint32_t issue(const AttnArgs& a, const Cursor& c, int2 place, int nsub, int lane,
+                                                     const Lane& ln, uint32_t stage) {
         const int g = nsub == 1 ? c.unit : c.unit / nsub;
         const uint32_t mask = __ballot_sync(0xffffffffu, place.x >= 0);
         if (mask == 0u) return 0u;   // nobody reads the stage
@@ -176,18 +204,27 @@ struct Attn {
         const uint32_t in = ch * 16 < a.c.head_dim * kElem ? 16u : 0u;
         const char* kb = static_cast<const char*>(a.c.k) + ch * 16;
         const char* vb = static_cast<const char*>(a.c.v) + ch * 16;
-        const bool all = mask == (KT == 32 ? 0xffffffffu : (1u << KT) - 1u);
+        // row i kRowsPerIter + r0: the permutations differ from row r0's by a constant per i
+        auto copy = [&](int i, long long o, long long p, uint32_t size) {
+            const int r = i * kRowsPerIter;
+            const uint32_t fk = kPitch == 512 ? (r & 1) << 6 : 0, fv = kPitch > 64 ? (r & 6) << 4 : 0;
+            cp_async16_zfill(stage + (ln.wk ^ fk) + r * kPitch, kb + o * 16, size);
+            cp_async16_zfill(stage + ((ln.wv - kTileBytes) ^ fv) + kTileBytes + r * kPitch, vb + p * 16, size);
+        };
+        if (mask == kAllKeys && !a.far) {
 #pragma unroll
-        for (int i = 0; i < KT / kRowsPerIter; ++i) {
-            const int r = i * kRowsPerIter + r0;
-            long long o = __shfl_sync(0xffffffffu, (uint32_t)ko, r), p = __shfl_sync(0xffffffffu, (uint32_t)vo, r);
-            if (a.far) {
-                o |= (long long)__shfl_sync(0xffffffffu, (uint32_t)(ko >> 32), r) << 32;
-                p |= (long long)__shfl_sync(0xffffffffu, (uint32_t)(vo >> 32), r) << 32;
+            for (int i = 0; i < KT / kRowsPerIter; ++i) {
+                const int r = i * kRowsPerIter + r0;
+                const uint32_t o = __shfl_sync(0xffffffffu, (uint32_t)ko, r), p = __shfl_sync(0xffffffffu, (uint32_t)vo, r);
+                copy(i, o, p, in);
             }
-            const uint32_t size = all || ((mask >> r) & 1u) ? in : 0u;
-            cp_async16_zfill(stage + at_k(r, ch), kb + o * 16, size);
-            cp_async16_zfill(stage + kTileBytes + at_v(r, ch), vb + p * 16, size);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KT / kRowsPerIter; ++i) {
+                const int r = i * kRowsPerIter + r0;
+                const long long o = __shfl_sync(0xffffffffu, ko, r), p = __shfl_sync(0xffffffffu, vo, r);
+                copy(i, o, p, (mask >> r) & 1u ? in : 0u);
+            }
         }
         return mask;
     }
@@ -282,7 +319,7 @@ struct Attn {
     }
 
     // One tile: scores, running maximum, weights, o.
-    __device__ static __forceinline__ void tile(const AttnArgs& a, State& st, const char* stage, uint32_t mask, int lane) {
+    __device__ static __forceinline__ void tile(const AttnArgs& a, State& st, uint32_t stage, const Lane& ln, uint32_t mask, int lane) {
         constexpr int NT = KT / 8;
         const int col = lane % 4;
         float s[NT][ROWS / 8][2];
@@ -290,10 +327,10 @@ struct Attn {
         for (int nt = 0; nt < NT; ++nt) {
             // c: first terms (rows 0-7) and second terms or heads 8-15 (rows 8-15); c2: third terms
             float c[4] = {}, c2[4] = {};
-            const int key = nt * 8 + lane / 4;
 #pragma unroll
             for (int j = 0; j < kChunks / 4; ++j) {
-                const uint4 k4 = *reinterpret_cast<const uint4*>(stage + at_k(key, 4 * j + col));
+                // row 8 nt + lane / 4, chunk 4 j + lane % 4
+                const uint4 k4 = lds128(stage + ln.k[j & 1] + nt * 8 * kPitch + (j >> 1) * 128);
                 const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
                 constexpr int SJ = F8 ? 4 : 2;
 #pragma unroll
@@ -349,7 +386,7 @@ struct Attn {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) s[nt][rr][e] *= f;
             }
-            if (mask != (KT == 32 ? 0xffffffffu : (1u << KT) - 1u)) {
+            if (mask != kAllKeys) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -400,7 +437,6 @@ struct Attn {
         }
         // o += p v: the thread reads kVElems columns of its 4 keys of each 16 and pairs the
         // keys of a column; column (8 w + n) kVElems + e is column n of MMA tile (w, e)
-        const char* vt = stage + kTileBytes;
 #pragma unroll
         for (int w = 0; w < kWindows; ++w) {
             float fresh[EX ? kVElems : 1][4];
@@ -415,12 +451,13 @@ struct Attn {
                 uint32_t v[4][4];   // keys 2 col, + 1, + 8, + 9
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int key = kg * 16 + 2 * col + (i & 1) + (i >> 1) * 8;
+                    // row 16 kg + 2 col + (i & 1) + 8 (i >> 1), chunk 8 w + lane / 4
+                    const uint32_t at = stage + ln.v[i & 1] + (kg * 16 + (i >> 1) * 8) * kPitch + w * 128;
                     if constexpr (kVElems * kElem == 16) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(vt + at_v(key, 8 * w + lane / 4));
+                        const uint4 u = lds128(at);
                         v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
                     } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(vt + at_v(key, lane / 8) + (lane / 4 % 2) * 8);
+                        const uint2 u = lds64(at);
                         v[i][0] = u.x; v[i][1] = u.y;
                     }
                 }
@@ -718,7 +755,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
 
     // ---- pipeline: `ahead` runs K::kStages - 1 tiles in front of `c`
     const uint32_t ring = smem_u32(smem) + warp * K::kStages * 2 * K::kTileBytes;
-    const char* ring_p = smem + (size_t)warp * K::kStages * 2 * K::kTileBytes;
+    const typename K::Lane ln(lane);
     float* buf = reinterpret_cast<float*>(smem + K::kRing);
     Cursor ahead = c;
     int2 place = K::place_of(a, ahead, warp, lane);
@@ -728,7 +765,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
             Cursor next = ahead;
             K::advance(a, units, next);
             const int2 place_next = K::place_of(a, next, warp, lane);
-            const uint32_t mask = K::issue(a, ahead, place, nsub, warp, lane, ring + stage_in * 2 * K::kTileBytes);
+            const uint32_t mask = K::issue(a, ahead, place, nsub, lane, ln, ring + stage_in * 2 * K::kTileBytes);
             if (lane == 0) sh.mask[warp][stage_in] = mask;
             stage_in = stage_in + 1 == K::kStages ? 0 : stage_in + 1;
             ahead = next;
@@ -754,7 +791,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
             const uint32_t mask = sh.mask[warp][stage_out];
             feed();
             // keys beyond the request (the tail of its last tile) count for nothing
-            if (mask) K::tile(a, st, ring_p + stage_out * 2 * K::kTileBytes, mask, lane);
+            if (mask) K::tile(a, st, ring + stage_out * 2 * K::kTileBytes, ln, mask, lane);
             stage_out = stage_out + 1 == K::kStages ? 0 : stage_out + 1;
             K::advance(a, units, c);
         }
@@ -825,6 +862,9 @@ size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t*
 cudaError_t launch_attn_decode(const AttnArgs& args, cudaStream_t s) {
     AttnArgs a = args;
     const bool f8 = a.c.dtype == MOE_DTYPE_FP8_E4M3;
+    a.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (a.c.page_size == 1 << i) a.page_shift = i;
     // bytes up to the last row of either tensor
     auto reach = [&](int64_t page, int64_t slot, int64_t head) {
         return (__int128)page * (a.c.num_pages - 1) + (__int128)slot * (a.c.page_size - 1) + (__int128)head * (a.c.heads - 1);

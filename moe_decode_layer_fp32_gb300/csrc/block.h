@@ -56,6 +56,7 @@ struct AttnArgs {
     const int32_t* seq_lens;
     float scale, softcap;
     int window;
+    int page_shift;            // log2 of the page size, or -1 (set by the launcher)
     int far;                   // cache offsets pass 2^32 steps of 16 bytes (set by the launcher)
     int32_t* status;
     uint32_t* done;            // counters, one per unit (zero between calls)
