@@ -31,7 +31,9 @@ namespace {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnMaxCtas = 480;          // bounds the workspace
-constexpr int kMergeFloats = 2048;         // shared merge buffer, 8 KB
+constexpr int kJoinMost = 24;              // parts joined by one CTA; more go in groups of kJoinGroup first
+constexpr int kJoinGroup = 16;
+constexpr int kTileCost = 2, kUnitCost = 1;   // what a tile and the beginning and end of a unit cost
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -80,11 +82,22 @@ __device__ __forceinline__ float tanh_fast(float x) {
 __device__ __forceinline__ float bf16_trunc(float p) { return __uint_as_float(__float_as_uint(p) & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
 
-// Where a CTA (or one of its warps) stands in the run of tiles.
+// Where a CTA (or one of its warps) stands.
 struct Cursor {
     int b, unit, tile, tiles, first, n;
-    long long left;                        // tiles of this CTA from here on
+    long long base;                        // where the unit begins in the line of all units
 };
+// Of a unit of so many tiles.
+__device__ __forceinline__ int span_of(int tiles) { return tiles > 0 ? kTileCost * tiles + kUnitCost : 0; }
+// Tiles of the cursor's unit that begin before position p.
+__device__ __forceinline__ int tiles_before(const Cursor& c, long long p) {
+    const long long n = p - c.base - kUnitCost;
+    return n <= 0 ? 0 : (int)min((n + kTileCost - 1) / kTileCost, (long long)c.tiles);
+}
+// Whether the cursor's tile begins before position `end`.
+__device__ __forceinline__ bool before(const Cursor& c, long long end) {
+    return c.base + kUnitCost + (long long)kTileCost * c.tile < end;
+}
 
 // x / y for 0 <= x, 0 < y; 64-bit division only where it must be.
 __device__ __forceinline__ long long div_u(long long x, long long y) {
@@ -123,7 +136,9 @@ struct Attn {
     static constexpr int kCtasPerSm = DP == 256 ? (F8 ? 2 : 1) : EX ? 2 : 3;
     static constexpr int kStages = kCtasPerSm == 3 && kTileBytes == 4096 ? 2 : 3;
     static constexpr size_t kRing = (size_t)kAttnWarps * kStages * 2 * kTileBytes;
-    static constexpr size_t kSmem = kRing + kMergeFloats * 4;
+    static constexpr int kQBytes = ROWS * DP * (EX ? 4 : 2);         // a unit's query rows
+    static constexpr size_t kSmem = kRing + 2 * kQBytes;
+    static_assert(ROWS * DP * 4 <= 2 * kTileBytes, "a warp's o fits the stage it read last");
     static constexpr int kPartFloats = ROWS * (DP + 2);
     static_assert(ROWS == 8 || (ROWS == 16 && !EX), "16 heads only without extra terms");
 
@@ -163,12 +178,12 @@ struct Attn {
         c.first = a.window > 0 ? max(0, n - a.window) : 0;
         c.tiles = (n - c.first + kTileKeys - 1) / kTileKeys;
     }
-    // To the next tile of the run (left > 0 says whether there is one).
-    __device__ static __forceinline__ void advance(const AttnArgs& a, int units, Cursor& c) {
-        if (--c.left <= 0) return;
+    // To the next tile; where none begins before `end`, to some position from `end` on.
+    __device__ static __forceinline__ void advance(const AttnArgs& a, int units, long long end, Cursor& c) {
         if (++c.tile < c.tiles) return;
+        c.base += span_of(c.tiles);
         c.tile = 0;
-        if (++c.unit < units) return;
+        if (c.base >= end || ++c.unit < units) return;
         c.unit = 0;
         do {
             ++c.b;
@@ -176,9 +191,9 @@ struct Attn {
         } while (c.tiles == 0);
     }
     // Page and slot of the key that lane `lane` looks after in the warp's tile; page -1: none.
-    __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
+    __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, long long end, int warp, int lane) {
         const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
-        if (c.left <= 0 || lane >= KT || key >= c.n) return make_int2(-1, 0);
+        if (!before(c, end) || lane >= KT || key >= c.n) return make_int2(-1, 0);
         const int col = a.page_shift >= 0 ? key >> a.page_shift : key / a.c.page_size;
         const int page = a.table[c.b * a.table_ld + col];
         if (page < 0 || page >= a.c.num_pages) {
@@ -242,18 +257,29 @@ struct Attn {
         else mma_bf16(c, a0, a1, a2, a3, b0, b1);
     }
 
+    // Copies of a unit's query rows into shared memory, as they are.
+    __device__ static __forceinline__ void fetch_q(const AttnArgs& a, const Cursor& c, int nsub, char* dst) {
+        const int g = c.unit / nsub, sub = c.unit % nsub;
+        const int es = a.q_dt == MOE_DTYPE_BF16 ? 2 : 4, per_row = a.c.head_dim * es / 16;   // 16-byte words
+        const long long base = c.b * a.q_bs + (g * a.group + sub * ROWS) * a.q_hs;
+        const int rows = min(ROWS, a.group - sub * ROWS);
+        for (int i = threadIdx.x; i < rows * per_row; i += kAttnThreads) {
+            const int r = i / per_row, w = i - r * per_row;
+            cp_async16(dst + r * DP * es + w * 16, static_cast<const char*>(a.q) + (base + r * a.q_hs) * es + w * 16);
+        }
+        cp_async_commit();
+    }
     // The unit's query rows: the thread holds rows lane / 4 (and + 8), elements
     // 8 (lane % 4) + {0..7} of every 32 (bf16), 16 (lane % 4) + {0..15} of every 64 (E4M3): the order
     // in which it reads K rows; a dot product does not mind the order.
-    __device__ static void load_q(const AttnArgs& a, const Cursor& c, int nsub, int lane, State& st) {
+    __device__ static void load_q(const AttnArgs& a, const Cursor& c, int nsub, int lane, const char* src, State& st) {
         const int g = c.unit / nsub, sub = c.unit % nsub;
         const float ks = a.c.k_scale ? a.c.k_scale[g] : 1.0f;
         constexpr int E = F8 ? 16 : 8, J = DP / (4 * E);
 #pragma unroll
         for (int rr = 0; rr < ROWS / 8; ++rr) {
-            const int row = sub * ROWS + rr * 8 + lane / 4;
-            const bool have = row < a.group;
-            const long long base = c.b * a.q_bs + (g * a.group + (have ? row : 0)) * a.q_hs;
+            const int row = rr * 8 + lane / 4;
+            const bool have = sub * ROWS + row < a.group;
             float f[J][E];
             float mx = 0.0f;
 #pragma unroll
@@ -262,7 +288,7 @@ struct Attn {
                 for (int h = 0; h < E / 8; ++h) {
                     const int d0 = j * 4 * E + (lane % 4) * E + h * 8;
                     float v[8] = {};
-                    if (have && d0 < a.c.head_dim) load8_f32(a.q, a.q_dt, base + d0, v);
+                    if (have && d0 < a.c.head_dim) load8_f32(src, a.q_dt, row * DP + d0, v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         f[j][h * 8 + e] = v[e];
@@ -539,7 +565,9 @@ struct Attn {
     }
 
     // Join the warps' parts of a unit: the whole unit goes to `out`, a part of one to `part`.
-    __device__ static void merge(const AttnArgs& a, const Cursor& c, int nsub, State& st, float* buf, Shared& sh, float* part) {
+    // A warp's o lies in the stage that it read last (base + warp * stride).
+    __device__ static void merge(const AttnArgs& a, const Cursor& c, int nsub, State& st, char* base, int stride, Shared& sh,
+                                 float* part) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         const int g = c.unit / nsub, sub = c.unit % nsub;
 #pragma unroll
@@ -553,70 +581,61 @@ struct Attn {
                 sh.l[warp][rr * 8 + lane / 4] = l;
             }
         }
-        // a round: kCols columns of all rows and warps in the buffer
-        constexpr int kCols = kMergeFloats / (kAttnWarps * ROWS) < DP ? kMergeFloats / (kAttnWarps * ROWS) : DP;
-        constexpr int kRoundWindow = 8 * kVElems;                 // columns of one window of accumulators
-        static_assert(kCols % kRoundWindow == 0 || kRoundWindow % kCols == 0, "rounds of whole windows");
+        float4* mine = reinterpret_cast<float4*>(base + warp * stride);
 #pragma unroll
-        for (int c0 = 0; c0 < DP; c0 += kCols) {
+        for (int w = 0; w < kWindows; ++w)
 #pragma unroll
-            for (int w = 0; w < kWindows; ++w)
+            for (int i = 0; i < 2; ++i) {
+                const int colb = (8 * w + 2 * (lane % 4) + i) * kVElems;   // kVElems columns from here
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int colb = (8 * w + 2 * (lane % 4) + i) * kVElems;   // kVElems columns from here
-                    if (colb < c0 || colb >= c0 + kCols) continue;
+                for (int rr = 0; rr < ROWS / 8; ++rr)
 #pragma unroll
-                    for (int rr = 0; rr < ROWS / 8; ++rr)
+                    for (int e = 0; e < kVElems; e += 4) {
+                        float v[4];
 #pragma unroll
-                        for (int e = 0; e < kVElems; e += 4) {
-                            float v[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float (&o)[4] = st.o[w * kVElems + e + k];
-                                v[k] = ROWS == 16 ? o[2 * rr + i] : o[i] + o[2 + i];
-                            }
-                            const int row = rr * 8 + lane / 4, f4 = (colb - c0 + e) / 4;
-                            reinterpret_cast<float4*>(buf)[(warp * ROWS + row) * (kCols / 4) + (f4 ^ (row & 7))] =
-                                make_float4(v[0], v[1], v[2], v[3]);
+                        for (int k = 0; k < 4; ++k) {
+                            const float (&o)[4] = st.o[w * kVElems + e + k];
+                            v[k] = ROWS == 16 ? o[2 * rr + i] : o[i] + o[2 + i];
                         }
-                }
-            __syncthreads();
-            for (int it = tid; it < ROWS * (kCols / 4); it += kAttnThreads) {
-                const int row = it / (kCols / 4), f4 = it % (kCols / 4);
-                float top = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh.m[w][row]);
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kAttnWarps; ++w) {
-                    const float f = weight_of(sh.m[w][row], top);
-                    // a NaN sum has no maximum: it stays NaN
-                    l = fmaf(sh.l[w][row] != sh.l[w][row] ? 1.0f : f, sh.l[w][row], l);
-                    axpy4(o, f, reinterpret_cast<const float4*>(buf)[(w * ROWS + row) * (kCols / 4) + (f4 ^ (row & 7))]);
-                }
-                const int c4 = c0 / 4 + f4;
-                if (part) {
-                    reinterpret_cast<float4*>(part)[row * (DP / 4) + c4] = o;
-                    if (c4 == 0) {
-                        part[ROWS * DP + row] = top;
-                        part[ROWS * DP + ROWS + row] = l;
+                        const int row = rr * 8 + lane / 4, f4 = (colb + e) / 4;
+                        mine[row * (DP / 4) + (f4 ^ (row & 7))] = make_float4(v[0], v[1], v[2], v[3]);
                     }
-                } else {
-                    finish(a, c.b, g, sub, row, c4, o, top, l);
-                }
             }
-            __syncthreads();
+        __syncthreads();
+#pragma unroll 2
+        for (int it = tid; it < ROWS * (DP / 4); it += kAttnThreads) {
+            const int row = it / (DP / 4), c4 = it % (DP / 4);
+            float top = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh.m[w][row]);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float f = weight_of(sh.m[w][row], top);
+                // a NaN sum has no maximum: it stays NaN
+                l = fmaf(sh.l[w][row] != sh.l[w][row] ? 1.0f : f, sh.l[w][row], l);
+                axpy4(o, f, reinterpret_cast<const float4*>(base + w * stride)[row * (DP / 4) + (c4 ^ (row & 7))]);
+            }
+            if (part) {
+                reinterpret_cast<float4*>(part)[row * (DP / 4) + c4] = o;
+                if (c4 == 0) {
+                    part[ROWS * DP + row] = top;
+                    part[ROWS * DP + ROWS + row] = l;
+                }
+            } else {
+                finish(a, c.b, g, sub, row, c4, o, top, l);
+            }
         }
+        __syncthreads();
     }
 
-    // Join the parts of CTAs c_first .. c_last, in that order: the weights of all
-    // parts first (in `buf`, as many at a time as it holds), then their sum.
-    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, int c_first, int c_last, bool tail_first,
-                                float* buf) {
+    // Join `count` parts, part_at(0), part_at(1), ..., in that order, a batch of loads at a time:
+    // to the result, or to the part `to`.
+    template <class PartAt>
+    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, int count, PartAt part_at, float* to) {
         const int g = c.unit / nsub, sub = c.unit % nsub, tid = threadIdx.x;
-        auto part = [&](int k) { return a.parts + (size_t)(2 * k + (k == c_first && tail_first ? 1 : 0)) * kPartFloats; };
-        constexpr int kMost = kMergeFloats / 2 / ROWS;          // parts whose maxima and sums fit
         constexpr int kItems = ROWS * (DP / 4) / kAttnThreads;  // float4 a thread joins
+        constexpr int kBatch = kItems <= 2 ? 8 : 4;
         static_assert(kItems * kAttnThreads == ROWS * (DP / 4), "whole items");
         float top[kItems], l[kItems];
         float4 o[kItems];
@@ -626,40 +645,65 @@ struct Attn {
             l[i] = 0.0f;
             o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        for (int k0 = c_first; k0 <= c_last; k0 += kMost) {
-            const int count = min(kMost, c_last - k0 + 1);
-            __syncthreads();
-            for (int it = tid; it < count * 2 * ROWS; it += kAttnThreads)
-                buf[it] = __ldcg(part(k0 + it / (2 * ROWS)) + ROWS * DP + it % (2 * ROWS));
-            __syncthreads();
+        for (int k0 = 0; k0 < count; k0 += kBatch) {
+            float pm[kBatch][kItems], pl[kBatch][kItems];
+            float4 po[kBatch][kItems];
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int row = (tid + i * kAttnThreads) / (DP / 4);
-                float mx = top[i];
-                for (int k = 0; k < count; ++k) mx = fmaxf(mx, buf[k * 2 * ROWS + row]);
-                const float f = weight_of(top[i], mx);
-                l[i] *= f;
-                o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
-                top[i] = mx;
-            }
-#pragma unroll 8
-            for (int k = 0; k < count; ++k) {
-                const float4* p = reinterpret_cast<const float4*>(part(k0 + k));
+            for (int k = 0; k < kBatch; ++k) {
+                const float* p = part_at(min(k0 + k, count - 1));
 #pragma unroll
                 for (int i = 0; i < kItems; ++i) {
-                    const int row = (tid + i * kAttnThreads) / (DP / 4);
-                    const float pl = buf[k * 2 * ROWS + ROWS + row], f = weight_of(buf[k * 2 * ROWS + row], top[i]);
-                    l[i] = fmaf(pl != pl ? 1.0f : f, pl, l[i]);
-                    axpy4(o[i], f, __ldcg(p + tid + i * kAttnThreads));
+                    const int it = tid + i * kAttnThreads, row = it / (DP / 4);
+                    pm[k][i] = __ldcg(p + ROWS * DP + row);
+                    pl[k][i] = __ldcg(p + ROWS * DP + ROWS + row);
+                    po[k][i] = __ldcg(reinterpret_cast<const float4*>(p) + it);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                float mx = top[i];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, pm[k][i]);
+                const float f0 = weight_of(top[i], mx);
+                l[i] *= f0;
+                o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
+                top[i] = mx;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (k0 + k >= count) break;
+                    const float f = weight_of(pm[k][i], mx);
+                    l[i] = fmaf(pl[k][i] != pl[k][i] ? 1.0f : f, pl[k][i], l[i]);
+                    axpy4(o[i], f, po[k][i]);
                 }
             }
         }
+        if (to) __syncthreads();      // `to` is one of the parts: all have been read
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int it = tid + i * kAttnThreads;
-            finish(a, c.b, g, sub, it / (DP / 4), it % (DP / 4), o[i], top[i], l[i]);
+            const int it = tid + i * kAttnThreads, row = it / (DP / 4), c4 = it % (DP / 4);
+            if (to) {
+                reinterpret_cast<float4*>(to)[it] = o[i];
+                if (c4 == 0) {
+                    to[ROWS * DP + row] = top[i];
+                    to[ROWS * DP + ROWS + row] = l[i];
+                }
+            } else {
+                finish(a, c.b, g, sub, row, c4, o[i], top[i], l[i]);
+            }
+        }
+    }
+
+    // Whether this CTA is the last of `n` to arrive at the counter (which then is zero
+    // again).  What the CTAs wrote before is visible to the last one after it.
+    __device__ static bool arrive_last(uint32_t* counter, int n, Shared& sh) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const bool last = atomic_add_acq_rel_gpu(counter, 1u) == (uint32_t)(n - 1);
+            if (last) *counter = 0u;
+            sh.last = last;
         }
         __syncthreads();
+        return sh.last;
     }
 };
 
@@ -673,8 +717,9 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
     pdl_allow_dependents();
     pdl_wait_primary();
 
-    // ---- the run of this CTA: tiles [start, end) of the `total` of all requests,
-    // found with a scan of the requests in blocks of the CTA's threads
+    // ---- the run of this CTA.  All units lie end to end, each with kUnitCost for its beginning and
+    // end and kTileCost per tile; a CTA has the tiles that begin in its equal part of that.  The
+    // part's first request is found with a scan of the requests in blocks of the CTA's threads.
     auto tiles_of = [&](int b) {
         Cursor c;
         c.b = b;
@@ -700,13 +745,13 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
         }
         return incl;
     };
-    const int t0 = tid < a.B ? tiles_of(tid) : 0;      // of the first block
+    const int s0 = tid < a.B ? span_of(tiles_of(tid)) : 0;      // of the first block
     long long sum0, total;
-    const long long incl0 = scan((long long)t0 * units, sum0);
+    const long long incl0 = scan((long long)s0 * units, sum0);
     total = sum0;
     if (a.B > kAttnThreads) {
         long long mine = 0;
-        for (int b = kAttnThreads + tid; b < a.B; b += kAttnThreads) mine += tiles_of(b);
+        for (int b = kAttnThreads + tid; b < a.B; b += kAttnThreads) mine += span_of(tiles_of(b));
         long long rest;
         __syncthreads();
         scan(mine * units, rest);
@@ -724,47 +769,51 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
             K::finish(a, b, unit / nsub, unit % nsub, row, c4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
         }
     }
-    const Share share(min((long long)gridDim.x, total), total);
+    // parts of at least a whole tile and unit
+    const Share share(min((long long)gridDim.x, div_u(total, kTileCost + kUnitCost)), total);
     if (blockIdx.x >= share.ctas) return;
     const long long start = share.start(blockIdx.x), end = share.start(blockIdx.x + 1);
-    long long before = 0, incl = incl0, all = sum0;
-    int t = t0, b0 = 0;
+    long long sum = 0, incl = incl0, all = sum0;
+    int span = s0, b0 = 0;
     while (true) {
-        const long long pre = before + incl - (long long)t * units;
-        if (start >= pre && start < before + incl) {
+        const long long pre = sum + incl - (long long)span * units;
+        if (start >= pre && start < sum + incl) {
             sh.found_b = b0 + tid;
             sh.found_pre = pre;
         }
-        before += all;
-        if (start < before) break;      // the same for all threads
+        sum += all;
+        if (start < sum) break;      // the same for all threads
         b0 += kAttnThreads;
-        t = b0 + tid < a.B ? tiles_of(b0 + tid) : 0;
+        span = b0 + tid < a.B ? span_of(tiles_of(b0 + tid)) : 0;
         __syncthreads();
-        incl = scan((long long)t * units, all);
+        incl = scan((long long)span * units, all);
     }
     __syncthreads();
     Cursor c;
     c.b = sh.found_b;
     K::set_request(a, c);
-    {
-        const long long off = start - sh.found_pre;
-        c.unit = (int)div_u(off, c.tiles);
-        c.tile = (int)(off - (long long)c.unit * c.tiles);
+    c.unit = (int)div_u(start - sh.found_pre, span_of(c.tiles));
+    c.base = sh.found_pre + (long long)c.unit * span_of(c.tiles);
+    c.tile = tiles_before(c, start);
+    if (c.tile == c.tiles) {            // the part begins with the end of a unit
+        --c.tile;
+        K::advance(a, units, end, c);
     }
-    c.left = end - start;
+    if (!before(c, end)) return;
 
     // ---- pipeline: `ahead` runs K::kStages - 1 tiles in front of `c`
     const uint32_t ring = smem_u32(smem) + warp * K::kStages * 2 * K::kTileBytes;
     const typename K::Lane ln(lane);
-    float* buf = reinterpret_cast<float*>(smem + K::kRing);
+    char* q_buf = smem + K::kRing;
+    K::fetch_q(a, c, nsub, q_buf);
     Cursor ahead = c;
-    int2 place = K::place_of(a, ahead, warp, lane);
+    int2 place = K::place_of(a, ahead, end, warp, lane);
     int stage_in = 0;
     auto feed = [&]() {
-        if (ahead.left > 0) {
+        if (before(ahead, end)) {
             Cursor next = ahead;
-            K::advance(a, units, next);
-            const int2 place_next = K::place_of(a, next, warp, lane);
+            K::advance(a, units, end, next);
+            const int2 place_next = K::place_of(a, next, end, warp, lane);
             const uint32_t mask = K::issue(a, ahead, place, nsub, lane, ln, ring + stage_in * 2 * K::kTileBytes);
             if (lane == 0) sh.mask[warp][stage_in] = mask;
             stage_in = stage_in + 1 == K::kStages ? 0 : stage_in + 1;
@@ -776,15 +825,22 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
 #pragma unroll
     for (int i = 0; i < K::kStages - 1; ++i) feed();
 
-    int stage_out = 0;
-    bool first_segment = true;
-    long long at = start;                       // linear position of c
-    while (c.left > 0) {
+    int stage_out = 0, segment = 0;
+    while (before(c, end)) {
+        // the query rows came with a group of copies before the last kStages - 2
+        cp_async_wait<K::kStages - 2>();
+        __syncthreads();
         typename K::State st;
-        K::load_q(a, c, nsub, lane, st);
+        K::load_q(a, c, nsub, lane, q_buf + (segment & 1) * K::kQBytes, st);
         const Cursor seg = c;
-        const long long unit_begin = at - c.tile, unit_end = unit_begin + c.tiles;
-        const int count = (int)min(c.left, (long long)(c.tiles - c.tile));
+        const int count = tiles_before(c, end) - c.tile;
+        {
+            // the next unit's query rows
+            Cursor next = c;
+            next.tile += count - 1;
+            K::advance(a, units, end, next);
+            if (before(next, end)) K::fetch_q(a, next, nsub, q_buf + (~segment & 1) * K::kQBytes);
+        }
         for (int i = 0; i < count; ++i) {
             cp_async_wait<K::kStages - 2>();
             __syncwarp();
@@ -793,29 +849,35 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
             // keys beyond the request (the tail of its last tile) count for nothing
             if (mask) K::tile(a, st, ring + stage_out * 2 * K::kTileBytes, ln, mask, lane);
             stage_out = stage_out + 1 == K::kStages ? 0 : stage_out + 1;
-            K::advance(a, units, c);
+            K::advance(a, units, end, c);
         }
-        at += count;
+        const int last_stage = stage_out == 0 ? K::kStages - 1 : stage_out - 1;
         const bool whole = seg.tile == 0 && count == seg.tiles;
-        float* part = whole ? nullptr : a.parts + (size_t)(2 * blockIdx.x + (first_segment ? 0 : 1)) * K::kPartFloats;
-        K::merge(a, seg, nsub, st, buf, sh, part);
+        // slot of CTA k's part: its first unit, or its last
+        auto part_of = [&](int k, bool first) { return a.parts + (size_t)(2 * k + (first ? 0 : 1)) * K::kPartFloats; };
+        K::merge(a, seg, nsub, st, smem + last_stage * 2 * K::kTileBytes, K::kStages * 2 * K::kTileBytes, sh,
+                 whole ? nullptr : part_of(blockIdx.x, segment == 0));
         if (!whole) {
-            const int c_first = share.cta_of(unit_begin), c_last = share.cta_of(unit_end - 1);
+            const int c_first = share.cta_of(seg.base + kUnitCost);
+            const int c_last = share.cta_of(seg.base + kUnitCost + (long long)kTileCost * (seg.tiles - 1));
+            // the unit is the first one of CTA c_first unless that also has the last tile before it
+            const bool head = seg.base == 0 || share.start(c_first) > seg.base - kTileCost;
+            const int n = c_last - c_first + 1;
+            auto part_at = [&](int i) { return part_of(c_first + i, i > 0 || head); };
             uint32_t* done = a.done + (long long)seg.b * units + seg.unit;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const bool last = atomic_add_acq_rel_gpu(done, 1u) == (uint32_t)(c_last - c_first);
-                if (last) *done = 0u;
-                sh.last = last;
-            }
-            __syncthreads();
-            if (sh.last) {
-                __threadfence();
-                K::join(a, seg, nsub, c_first, c_last, share.start(c_first) < unit_begin, buf);
+            if (n <= kJoinMost) {
+                if (K::arrive_last(done, n, sh)) K::join(a, seg, nsub, n, part_at, nullptr);
+            } else {
+                const int me = (int)blockIdx.x - c_first, g0 = me / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, n - g0);
+                if (K::arrive_last(a.group_done + 2 * (c_first + g0) + (g0 > 0 || head ? 0 : 1), gn, sh)) {
+                    K::join(a, seg, nsub, gn, [&](int i) { return part_at(g0 + i); }, part_at(g0));
+                    const int groups = (n + kJoinGroup - 1) / kJoinGroup;
+                    if (K::arrive_last(done, groups, sh))
+                        K::join(a, seg, nsub, groups, [&](int i) { return part_at(i * kJoinGroup); }, nullptr);
+                }
             }
         }
-        first_segment = false;
+        ++segment;
     }
     cp_async_wait<0>();
 }
@@ -848,13 +910,14 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t* done_off, size_t* parts_off) {
-    // the parts come first: their place does not depend on B, so that the counters
-    // after them stay zero whatever the calls' batch sizes are
+size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t* done_off, size_t* group_off, size_t* parts_off) {
+    // the group counters and the parts come first: their place does not depend on B, so that the
+    // counters after them stay zero whatever the calls' batch sizes are
     const int group = q_heads / heads, dp = dp_of(head_dim);
     const size_t floats = (size_t)rows_of(group, dp, false) * (dp + 2);
-    *parts_off = 512;
-    *done_off = 512 + 2 * kAttnMaxCtas * floats * sizeof(float);
+    *group_off = 512;
+    *parts_off = 512 + 2 * kAttnMaxCtas * sizeof(uint32_t);
+    *done_off = *parts_off + 2 * kAttnMaxCtas * floats * sizeof(float);
     const size_t total = *done_off + (size_t)B * heads * ((group + 7) / 8) * sizeof(uint32_t);
     return (total + 255) / 256 * 256;   // moe_workspace_init clears whole 16-byte words
 }

@@ -60,9 +60,11 @@ struct AttnArgs {
     int far;                   // cache offsets pass 2^32 steps of 16 bytes (set by the launcher)
     int32_t* status;
     uint32_t* done;            // counters, one per unit (zero between calls)
+    uint32_t* group_done;      // and one per part
     float* parts;              // partial results
 };
-size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t* done_off, size_t* parts_off);
+size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t* done_off, size_t* group_off,
+                            size_t* parts_off);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 
 struct LoraArgs {

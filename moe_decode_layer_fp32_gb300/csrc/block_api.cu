@@ -126,8 +126,8 @@ int moe_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, 
 size_t moe_attn_workspace_bytes(int B, int q_heads, int heads, int head_dim) {
     if (B < 0 || q_heads < 1 || heads < 1 || q_heads % heads != 0 || head_dim < 8 || head_dim % 8 != 0 || head_dim > 256)
         return 0;
-    size_t d, p;
-    return moe::attn_workspace_bytes(B, q_heads, heads, head_dim, &d, &p);
+    size_t d, g, p;
+    return moe::attn_workspace_bytes(B, q_heads, heads, head_dim, &d, &g, &p);
 }
 
 int moe_attn_decode(const void* q, int q_dtype, int64_t q_batch_stride, int64_t q_head_stride, int B,
@@ -150,8 +150,8 @@ int moe_attn_decode(const void* q, int q_dtype, int64_t q_batch_stride, int64_t 
     if (!q || !out || !aligned16(q) || !aligned16(out) || (q_batch_stride | q_head_stride | out_batch_stride | out_head_stride) % 8 != 0)
         return api_fail(MOE_ERR_INVALID_ARG, "%s: q or out null or unaligned, or a stride no multiple of 8", who);
     if (!block_table || !seq_lens) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
-    size_t done_off, parts_off;
-    const size_t need = moe::attn_workspace_bytes(B, q_heads, cache->heads, cache->head_dim, &done_off, &parts_off);
+    size_t done_off, group_off, parts_off;
+    const size_t need = moe::attn_workspace_bytes(B, q_heads, cache->heads, cache->head_dim, &done_off, &group_off, &parts_off);
     if (!ws || !aligned16(ws)) return api_fail(MOE_ERR_INVALID_ARG, "%s: workspace null or unaligned", who);
     if (ws_bytes < need) return api_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu required", who, ws_bytes, need);
     moe::AttnArgs a = {};
@@ -163,6 +163,7 @@ int moe_attn_decode(const void* q, int q_dtype, int64_t q_batch_stride, int64_t 
     a.scale = scale; a.softcap = softcap; a.window = window;
     a.status = static_cast<int32_t*>(ws);
     a.done = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + done_off);
+    a.group_done = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + group_off);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + parts_off);
     return launched(moe::launch_attn_decode(a, as_stream(stream)), who);
 }
