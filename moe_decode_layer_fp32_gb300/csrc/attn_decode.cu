@@ -564,12 +564,44 @@ struct Attn {
         return m == -CUDART_INF_F ? 0.0f : exp2f(m - top);
     }
 
-    // Join the warps' parts of a unit: the whole unit goes to `out`, a part of one to `part`.
-    // A warp's o lies in the stage that it read last (base + warp * stride).
-    __device__ static void merge(const AttnArgs& a, const Cursor& c, int nsub, State& st, char* base, int stride, Shared& sh,
-                                 float* part) {
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // The warps' results (sh.m, sh.l, and o of warp w at base + w * stride) become one: the unit's
+    // result, or the part `to`.
+    __device__ static void combine(const AttnArgs& a, const Cursor& c, int nsub, const char* base, int stride, Shared& sh,
+                                   float* to) {
         const int g = c.unit / nsub, sub = c.unit % nsub;
+        __syncthreads();
+#pragma unroll 2
+        for (int it = threadIdx.x; it < ROWS * (DP / 4); it += kAttnThreads) {
+            const int row = it / (DP / 4), c4 = it % (DP / 4);
+            float top = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh.m[w][row]);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float f = weight_of(sh.m[w][row], top);
+                // a NaN sum has no maximum: it stays NaN
+                l = fmaf(sh.l[w][row] != sh.l[w][row] ? 1.0f : f, sh.l[w][row], l);
+                axpy4(o, f, reinterpret_cast<const float4*>(base + w * stride)[row * (DP / 4) + (c4 ^ (row & 7))]);
+            }
+            if (to) {
+                reinterpret_cast<float4*>(to)[row * (DP / 4) + c4] = o;
+                if (c4 == 0) {
+                    to[ROWS * DP + row] = top;
+                    to[ROWS * DP + ROWS + row] = l;
+                }
+            } else {
+                finish(a, c.b, g, sub, row, c4, o, top, l);
+            }
+        }
+        __syncthreads();
+    }
+
+    // Join what the warps have of a unit.  A warp's o goes to the stage that it read last
+    // (base + warp * stride).
+    __device__ static void merge(const AttnArgs& a, const Cursor& c, int nsub, State& st, char* base, int stride, Shared& sh,
+                                 float* to) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
         for (int rr = 0; rr < ROWS / 8; ++rr) {
             float l = st.l[rr];
@@ -601,96 +633,58 @@ struct Attn {
                         mine[row * (DP / 4) + (f4 ^ (row & 7))] = make_float4(v[0], v[1], v[2], v[3]);
                     }
             }
-        __syncthreads();
-#pragma unroll 2
-        for (int it = tid; it < ROWS * (DP / 4); it += kAttnThreads) {
-            const int row = it / (DP / 4), c4 = it % (DP / 4);
-            float top = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh.m[w][row]);
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                const float f = weight_of(sh.m[w][row], top);
-                // a NaN sum has no maximum: it stays NaN
-                l = fmaf(sh.l[w][row] != sh.l[w][row] ? 1.0f : f, sh.l[w][row], l);
-                axpy4(o, f, reinterpret_cast<const float4*>(base + w * stride)[row * (DP / 4) + (c4 ^ (row & 7))]);
-            }
-            if (part) {
-                reinterpret_cast<float4*>(part)[row * (DP / 4) + c4] = o;
-                if (c4 == 0) {
-                    part[ROWS * DP + row] = top;
-                    part[ROWS * DP + ROWS + row] = l;
-                }
-            } else {
-                finish(a, c.b, g, sub, row, c4, o, top, l);
-            }
-        }
-        __syncthreads();
+        combine(a, c, nsub, base, stride, sh, to);
     }
 
-    // Join `count` parts, part_at(0), part_at(1), ..., in that order, a batch of loads at a time:
-    // to the result, or to the part `to`.
+    // Join `count` parts, part_at(0), part_at(1), ...: warp w takes parts w, w + 4, ... in order, then
+    // the warps are joined as above.  `to` may be one of the parts (all are read before it is written).
     template <class PartAt>
-    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, int count, PartAt part_at, float* to) {
-        const int g = c.unit / nsub, sub = c.unit % nsub, tid = threadIdx.x;
-        constexpr int kItems = ROWS * (DP / 4) / kAttnThreads;  // float4 a thread joins
-        constexpr int kBatch = kItems <= 2 ? 8 : 4;
-        static_assert(kItems * kAttnThreads == ROWS * (DP / 4), "whole items");
-        float top[kItems], l[kItems];
-        float4 o[kItems];
+    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, int count, PartAt part_at, char* base, int stride,
+                                Shared& sh, float* to) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        constexpr int kAll = ROWS * (DP / 4) / 32, kItems = kAll < 8 ? kAll : 8;   // float4 of a lane, at a time
+        float4* mine = reinterpret_cast<float4*>(base + warp * stride);
+        for (int i0 = 0; i0 < kAll; i0 += kItems) {
+            float top[kItems], l[kItems];
+            float4 o[kItems];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            top[i] = -CUDART_INF_F;
-            l[i] = 0.0f;
-            o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        for (int k0 = 0; k0 < count; k0 += kBatch) {
-            float pm[kBatch][kItems], pl[kBatch][kItems];
-            float4 po[kBatch][kItems];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const float* p = part_at(min(k0 + k, count - 1));
+            for (int i = 0; i < kItems; ++i) {
+                top[i] = -CUDART_INF_F;
+                l[i] = 0.0f;
+                o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll 2
+            for (int k = warp; k < count; k += kAttnWarps) {
+                const float* p = part_at(k);
+                float pm[kItems], pl[kItems];
+                float4 po[kItems];
 #pragma unroll
                 for (int i = 0; i < kItems; ++i) {
-                    const int it = tid + i * kAttnThreads, row = it / (DP / 4);
-                    pm[k][i] = __ldcg(p + ROWS * DP + row);
-                    pl[k][i] = __ldcg(p + ROWS * DP + ROWS + row);
-                    po[k][i] = __ldcg(reinterpret_cast<const float4*>(p) + it);
+                    const int it = lane + 32 * (i0 + i), row = it / (DP / 4);
+                    po[i] = __ldcg(reinterpret_cast<const float4*>(p) + it);
+                    pm[i] = __ldcg(p + ROWS * DP + row);
+                    pl[i] = __ldcg(p + ROWS * DP + ROWS + row);
+                }
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const float mx = fmaxf(top[i], pm[i]), f0 = weight_of(top[i], mx), f1 = weight_of(pm[i], mx);
+                    top[i] = mx;
+                    l[i] = fmaf(pl[i] != pl[i] ? 1.0f : f1, pl[i], l[i] * (l[i] != l[i] ? 1.0f : f0));
+                    o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
+                    axpy4(o[i], f1, po[i]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                float mx = top[i];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, pm[k][i]);
-                const float f0 = weight_of(top[i], mx);
-                l[i] *= f0;
-                o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
-                top[i] = mx;
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    if (k0 + k >= count) break;
-                    const float f = weight_of(pm[k][i], mx);
-                    l[i] = fmaf(pl[k][i] != pl[k][i] ? 1.0f : f, pl[k][i], l[i]);
-                    axpy4(o[i], f, po[k][i]);
-                }
-            }
-        }
-        if (to) __syncthreads();      // `to` is one of the parts: all have been read
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int it = tid + i * kAttnThreads, row = it / (DP / 4), c4 = it % (DP / 4);
-            if (to) {
-                reinterpret_cast<float4*>(to)[it] = o[i];
+                const int it = lane + 32 * (i0 + i), row = it / (DP / 4), c4 = it % (DP / 4);
+                mine[row * (DP / 4) + (c4 ^ (row & 7))] = o[i];
                 if (c4 == 0) {
-                    to[ROWS * DP + row] = top[i];
-                    to[ROWS * DP + ROWS + row] = l[i];
+                    sh.m[warp][row] = top[i];
+                    sh.l[warp][row] = l[i];
                 }
-            } else {
-                finish(a, c.b, g, sub, row, c4, o[i], top[i], l[i]);
             }
         }
+        combine(a, c, nsub, base, stride, sh, to);
     }
 
     // Whether this CTA is the last of `n` to arrive at the counter (which then is zero
@@ -855,8 +849,9 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
         const bool whole = seg.tile == 0 && count == seg.tiles;
         // slot of CTA k's part: its first unit, or its last
         auto part_of = [&](int k, bool first) { return a.parts + (size_t)(2 * k + (first ? 0 : 1)) * K::kPartFloats; };
-        K::merge(a, seg, nsub, st, smem + last_stage * 2 * K::kTileBytes, K::kStages * 2 * K::kTileBytes, sh,
-                 whole ? nullptr : part_of(blockIdx.x, segment == 0));
+        char* lay = smem + last_stage * 2 * K::kTileBytes;
+        constexpr int kStride = K::kStages * 2 * K::kTileBytes;
+        K::merge(a, seg, nsub, st, lay, kStride, sh, whole ? nullptr : part_of(blockIdx.x, segment == 0));
         if (!whole) {
             const int c_first = share.cta_of(seg.base + kUnitCost);
             const int c_last = share.cta_of(seg.base + kUnitCost + (long long)kTileCost * (seg.tiles - 1));
@@ -866,14 +861,14 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
             auto part_at = [&](int i) { return part_of(c_first + i, i > 0 || head); };
             uint32_t* done = a.done + (long long)seg.b * units + seg.unit;
             if (n <= kJoinMost) {
-                if (K::arrive_last(done, n, sh)) K::join(a, seg, nsub, n, part_at, nullptr);
+                if (K::arrive_last(done, n, sh)) K::join(a, seg, nsub, n, part_at, lay, kStride, sh, nullptr);
             } else {
                 const int me = (int)blockIdx.x - c_first, g0 = me / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, n - g0);
                 if (K::arrive_last(a.group_done + 2 * (c_first + g0) + (g0 > 0 || head ? 0 : 1), gn, sh)) {
-                    K::join(a, seg, nsub, gn, [&](int i) { return part_at(g0 + i); }, part_at(g0));
+                    K::join(a, seg, nsub, gn, [&](int i) { return part_at(g0 + i); }, lay, kStride, sh, part_at(g0));
                     const int groups = (n + kJoinGroup - 1) / kJoinGroup;
                     if (K::arrive_last(done, groups, sh))
-                        K::join(a, seg, nsub, groups, [&](int i) { return part_at(i * kJoinGroup); }, nullptr);
+                        K::join(a, seg, nsub, groups, [&](int i) { return part_at(i * kJoinGroup); }, lay, kStride, sh, nullptr);
                 }
             }
         }
