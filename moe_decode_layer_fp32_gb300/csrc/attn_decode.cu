@@ -85,6 +85,8 @@ __device__ __forceinline__ uint32_t pack_hi(float a, float b) { return __byte_pe
 // Where a CTA (or one of its warps) stands.
 struct Cursor {
     int b, unit, tile, tiles, first, n;
+    int last;                              // tiles of the unit that begin before the run's end
+    const int32_t* row;                    // the request's row of the block table
     long long base;                        // where the unit begins in the line of all units
 };
 // Of a unit of so many tiles.
@@ -94,10 +96,8 @@ __device__ __forceinline__ int tiles_before(const Cursor& c, long long p) {
     const long long n = p - c.base - kUnitCost;
     return n <= 0 ? 0 : (int)min((n + kTileCost - 1) / kTileCost, (long long)c.tiles);
 }
-// Whether the cursor's tile begins before position `end`.
-__device__ __forceinline__ bool before(const Cursor& c, long long end) {
-    return c.base + kUnitCost + (long long)kTileCost * c.tile < end;
-}
+// Whether the cursor's tile is one of the run.
+__device__ __forceinline__ bool inside(const Cursor& c) { return c.tile < c.last; }
 
 // x / y for 0 <= x, 0 < y; 64-bit division only where it must be.
 __device__ __forceinline__ long long div_u(long long x, long long y) {
@@ -131,8 +131,12 @@ struct Attn {
     static constexpr int kVElems = F8 ? (DP >= 128 ? 16 : 8) : 8;    // columns a thread takes of a V row at once
     static constexpr int kWindows = DP / (8 * kVElems);
     static constexpr int kAccs = DP / 8;                             // n8 tiles of o
-    // p in f16 is scaled to use its range: 2^15 at the maximum
-    static constexpr float kPShift = F8 ? 15.0f : 0.0f;
+    // The running maximum is replaced only when the new one passes it by more than 2^kSlack:
+    // until then weights may be up to that, and o needs no rescaling (which most tiles
+    // would, for the sake of one of their heads).  p in f16 is scaled to use its range: 2^7
+    // at the maximum, 2^15 with the slack.
+    static constexpr float kSlack = 8.0f;
+    static constexpr float kPShift = F8 ? 7.0f : 0.0f;
     static constexpr int kCtasPerSm = DP == 256 ? (F8 ? 2 : 1) : EX ? 2 : 3;
     static constexpr int kStages = kCtasPerSm == 3 && kTileBytes == 4096 ? 2 : 3;
     static constexpr size_t kRing = (size_t)kAttnWarps * kStages * 2 * kTileBytes;
@@ -177,25 +181,30 @@ struct Attn {
         c.n = n;
         c.first = a.window > 0 ? max(0, n - a.window) : 0;
         c.tiles = (n - c.first + kTileKeys - 1) / kTileKeys;
+        c.row = a.table + c.b * a.table_ld;
     }
-    // To the next tile; where none begins before `end`, to some position from `end` on.
+    // To the next tile; where none begins before `end`, to none of the run.
     __device__ static __forceinline__ void advance(const AttnArgs& a, int units, long long end, Cursor& c) {
         if (++c.tile < c.tiles) return;
         c.base += span_of(c.tiles);
         c.tile = 0;
-        if (c.base >= end || ++c.unit < units) return;
-        c.unit = 0;
-        do {
-            ++c.b;
-            set_request(a, c);
-        } while (c.tiles == 0);
+        c.last = 0;
+        if (c.base >= end) return;
+        if (++c.unit == units) {
+            c.unit = 0;
+            do {
+                ++c.b;
+                set_request(a, c);
+            } while (c.tiles == 0);
+        }
+        c.last = tiles_before(c, end);
     }
     // Page and slot of the key that lane `lane` looks after in the warp's tile; page -1: none.
-    __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, long long end, int warp, int lane) {
+    __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
         const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
-        if (!before(c, end) || lane >= KT || key >= c.n) return make_int2(-1, 0);
+        if (!inside(c) || lane >= KT || key >= c.n) return make_int2(-1, 0);
         const int col = a.page_shift >= 0 ? key >> a.page_shift : key / a.c.page_size;
-        const int page = a.table[c.b * a.table_ld + col];
+        const int page = c.row[col];
         if (page < 0 || page >= a.c.num_pages) {
             set_status(a.status, MOE_ERR_DEVICE);
             return make_int2(-1, 0);
@@ -424,10 +433,11 @@ struct Attn {
             __syncwarp();
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float m_new = fmaxf(st.m[rr], mx);
-            const float top = m_new == -CUDART_INF_F ? 0.0f : m_new, base = top - kPShift;
-            const float corr = exp2_fast(st.m[rr] - top);
-            if (__any_sync(0xffffffffu, m_new != st.m[rr])) {
+            const bool raise = mx > st.m[rr] + kSlack;       // also from -inf
+            if (__any_sync(0xffffffffu, raise)) {
+                // rows that stay as they are have the factor 1
+                const float corr = raise ? exp2_fast(st.m[rr] - mx) : 1.0f;
+                if (raise) st.m[rr] = mx;
                 st.l[rr] *= corr;
 #pragma unroll
                 for (int i = 0; i < kAccs; ++i) {
@@ -439,7 +449,7 @@ struct Attn {
                     }
                 }
             }
-            st.m[rr] = m_new;
+            const float base = (st.m[rr] == -CUDART_INF_F ? 0.0f : st.m[rr]) - kPShift;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float p0 = exp2_fast(s[nt][rr][0] - base), p1 = exp2_fast(s[nt][rr][1] - base);
@@ -789,11 +799,12 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
     c.unit = (int)div_u(start - sh.found_pre, span_of(c.tiles));
     c.base = sh.found_pre + (long long)c.unit * span_of(c.tiles);
     c.tile = tiles_before(c, start);
+    c.last = tiles_before(c, end);
     if (c.tile == c.tiles) {            // the part begins with the end of a unit
         --c.tile;
         K::advance(a, units, end, c);
     }
-    if (!before(c, end)) return;
+    if (!inside(c)) return;
 
     // ---- pipeline: `ahead` runs K::kStages - 1 tiles in front of `c`
     const uint32_t ring = smem_u32(smem) + warp * K::kStages * 2 * K::kTileBytes;
@@ -801,13 +812,13 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
     char* q_buf = smem + K::kRing;
     K::fetch_q(a, c, nsub, q_buf);
     Cursor ahead = c;
-    int2 place = K::place_of(a, ahead, end, warp, lane);
+    int2 place = K::place_of(a, ahead, warp, lane);
     int stage_in = 0;
     auto feed = [&]() {
-        if (before(ahead, end)) {
+        if (inside(ahead)) {
             Cursor next = ahead;
             K::advance(a, units, end, next);
-            const int2 place_next = K::place_of(a, next, end, warp, lane);
+            const int2 place_next = K::place_of(a, next, warp, lane);
             const uint32_t mask = K::issue(a, ahead, place, nsub, lane, ln, ring + stage_in * 2 * K::kTileBytes);
             if (lane == 0) sh.mask[warp][stage_in] = mask;
             stage_in = stage_in + 1 == K::kStages ? 0 : stage_in + 1;
@@ -816,24 +827,24 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
         }
         cp_async_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < K::kStages - 1; ++i) feed();
 
     int stage_out = 0, segment = 0;
-    while (before(c, end)) {
+    while (inside(c)) {
         // the query rows came with a group of copies before the last kStages - 2
         cp_async_wait<K::kStages - 2>();
         __syncthreads();
         typename K::State st;
         K::load_q(a, c, nsub, lane, q_buf + (segment & 1) * K::kQBytes, st);
         const Cursor seg = c;
-        const int count = tiles_before(c, end) - c.tile;
+        const int count = c.last - c.tile;
         {
             // the next unit's query rows
             Cursor next = c;
             next.tile += count - 1;
             K::advance(a, units, end, next);
-            if (before(next, end)) K::fetch_q(a, next, nsub, q_buf + (~segment & 1) * K::kQBytes);
+            if (inside(next)) K::fetch_q(a, next, nsub, q_buf + (~segment & 1) * K::kQBytes);
         }
         for (int i = 0; i < count; ++i) {
             cp_async_wait<K::kStages - 2>();
