@@ -30,10 +30,10 @@ namespace {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kAttnMaxCtas = 480;          // bounds the workspace
+constexpr int kAttnMaxCtas = 320;          // bounds the workspace
 constexpr int kJoinMost = 24;              // parts joined by one CTA; more go in groups of kJoinGroup first
 constexpr int kJoinGroup = 16;
-constexpr int kTileCost = 2, kUnitCost = 1;   // what a tile and the beginning and end of a unit cost
+constexpr int kTileCost = 2, kUnitCost = 3;   // what a tile and the beginning and end of a unit cost
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -41,6 +41,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                                         uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// A 16 x 32 by 32 x 8, E4M3 into fp32.
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -125,9 +134,12 @@ struct Attn {
     static constexpr uint32_t kAllKeys = KT == 32 ? 0xffffffffu : (1u << (KT % 32)) - 1u;
     static constexpr int kChunks = kPitch / 16;                      // 16-byte chunks of a row
     static constexpr int kRowsPerIter = 32 / kChunks;
-    static constexpr int kQTerms = EX ? (F8 ? 2 : 3) : 1;
+    // bf16 queries over an E4M3 cache: q is two E4M3 terms (4 bits each, its 8) and the codes of K go
+    // into the MMA as they are
+    static constexpr bool kQ8 = F8 && !EX;
+    static constexpr int kQTerms = EX ? (F8 ? 2 : 3) : kQ8 ? 2 : 1;
     static constexpr int kPTerms = EX && !F8 ? 3 : 2;
-    static constexpr int kSteps = DP / 16;                           // k16 steps of q . k
+    static constexpr int kSteps = kQ8 ? DP / 32 : DP / 16;           // MMAs of q . k along d
     static constexpr int kVElems = F8 ? (DP >= 128 ? 16 : 8) : 8;    // columns a thread takes of a V row at once
     static constexpr int kWindows = DP / (8 * kVElems);
     static constexpr int kAccs = DP / 8;                             // n8 tiles of o
@@ -137,8 +149,8 @@ struct Attn {
     // at the maximum, 2^15 with the slack.
     static constexpr float kSlack = 8.0f;
     static constexpr float kPShift = F8 ? 7.0f : 0.0f;
-    static constexpr int kCtasPerSm = DP == 256 ? (F8 ? 2 : 1) : EX ? 2 : 3;
-    static constexpr int kStages = kCtasPerSm == 3 && kTileBytes == 4096 ? 2 : 3;
+    static constexpr int kCtasPerSm = kTileBytes > 4096 ? 1 : 2;
+    static constexpr int kStages = 3;
     static constexpr size_t kRing = (size_t)kAttnWarps * kStages * 2 * kTileBytes;
     static constexpr int kQBytes = ROWS * DP * (EX ? 4 : 2);         // a unit's query rows
     static constexpr size_t kSmem = kRing + 2 * kQBytes;
@@ -321,11 +333,30 @@ struct Attn {
                     for (int i = 0; i < E; ++i) f[j][i] *= up;
             }
             st.qf[rr] = a.scale * ks * back;
+            if constexpr (kQ8) {
+                // E4M3 has no infinity: a head with one gets NaN
+                if (mx == CUDART_INF_F) st.qf[rr] = CUDART_NAN_F;
 #pragma unroll
-            for (int t = 0; t < kQTerms; ++t)
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float* u = &f[s / 2][(s % 2) * 8 + h * 4];
+                            const uint32_t w = pack_e4m3x4(u[0], u[1], u[2], u[3]);
+                            const float2 lo = unpack_e4m3x2(w), hi = unpack_e4m3x2(w >> 16);
+                            u[0] = (u[0] - lo.x) * 16.0f;
+                            u[1] = (u[1] - lo.y) * 16.0f;
+                            u[2] = (u[2] - hi.x) * 16.0f;
+                            u[3] = (u[3] - hi.y) * 16.0f;
+                            st.q[t][rr][s][h] = w;
+                        }
+            }
+#pragma unroll
+            for (int t = 0; t < (kQ8 ? 0 : kQTerms); ++t)
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    const int j = s / (E / 4), i = (s % (E / 4)) * 4;
+                    const int j = s / (E / 4) % J, i = (s % (E / 4)) * 4;
                     uint32_t w[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -367,6 +398,22 @@ struct Attn {
                 // row 8 nt + lane / 4, chunk 4 j + lane % 4
                 const uint4 k4 = lds128(stage + ln.k[j & 1] + nt * 8 * kPitch + (j >> 1) * 128);
                 const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+                if constexpr (kQ8) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t(&q0)[2] = st.q[0][0][j * 2 + i];
+                        const uint32_t(&q1)[2] = st.q[1][0][j * 2 + i];
+                        if constexpr (ROWS == 16) {
+                            const uint32_t(&r0)[2] = st.q[0][1][j * 2 + i];
+                            const uint32_t(&r1)[2] = st.q[1][1][j * 2 + i];
+                            mma_e4m3(c, q0[0], r0[0], q0[1], r0[1], w[2 * i], w[2 * i + 1]);
+                            mma_e4m3(c2, q1[0], r1[0], q1[1], r1[1], w[2 * i], w[2 * i + 1]);
+                        } else {
+                            mma_e4m3(c, q0[0], q1[0], q0[1], q1[1], w[2 * i], w[2 * i + 1]);
+                        }
+                    }
+                    continue;
+                }
                 constexpr int SJ = F8 ? 4 : 2;
 #pragma unroll
                 for (int i = 0; i < SJ; ++i) {
@@ -398,7 +445,10 @@ struct Attn {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 s[nt][0][e] = c[e];
-                if constexpr (ROWS == 16) s[nt][1][e] = c[2 + e];
+                if constexpr (kQ8) {
+                    s[nt][0][e] = fmaf(ROWS == 16 ? c2[e] : c[2 + e], 0.0625f, c[e]);
+                    if constexpr (ROWS == 16) s[nt][1][e] = fmaf(c2[2 + e], 0.0625f, c[2 + e]);
+                } else if constexpr (ROWS == 16) s[nt][1][e] = c[2 + e];
                 // an infinite first term stands: the others' products with it may be NaN
                 else if (kQTerms > 1 && fabsf(c[e]) < CUDART_INF_F) s[nt][0][e] = c[e] + (c[2 + e] + c2[e]);
             }
