@@ -947,7 +947,8 @@ template <int DP, bool F8, int ROWS, bool EX>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     using K = Attn<DP, F8, ROWS, EX>;
     auto kern = attn_kernel<DP, F8, ROWS, EX>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), (int)K::kSmem, done);
     if (e != cudaSuccess) return e;
     static_assert(K::kCtasPerSm * (K::kSmem + sizeof(typename K::Shared) + 1024) <= 228 * 1024, "CTAs that run at once");
     const int grid = std::min(K::kCtasPerSm * device_sm_count(), kAttnMaxCtas);

@@ -2,6 +2,8 @@
 // paged attention, adapter projection); internal to the library.
 #pragma once
 
+#include <atomic>
+
 #include "../../include/moe_block.h"
 #include "kernels.h"
 
@@ -87,6 +89,18 @@ constexpr int kLoraMaxT = 128;
 constexpr int kLoraMaxRank = 128;
 size_t lora_workspace_bytes(int T, int d, int r, size_t* v_off, size_t* xs_off);
 cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s);
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device: `done` is the kernel's own.
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Launch configuration of a programmatic dependent: the kernel may start
 // before the one ahead of it on the stream has ended, and waits for it

@@ -672,7 +672,8 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     const LoraArgs& a = p.l;
     constexpr int kStageBytes = kWBytes + TERMS * TP * kBlockBytes;
     auto kern = lora_project_kernel<TP, F8, TERMS, SHRINK>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kProjSmem);
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kProjSmem, done);
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count();
     // shrink: at most min(T, na) adapters are in use
