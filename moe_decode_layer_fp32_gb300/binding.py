@@ -9,6 +9,7 @@ step of the layer runs here; a missing library raises instead of falling back.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 
 import torch
@@ -445,38 +446,30 @@ def moe_unique_weight_bytes_deamoe(d, n, I_sh, I_pr, I_s, dtype_code, A_d, A_e) 
 # dimension) must be contiguous, everything else may be a view.
 
 
-# A small call costs its host time: these helpers ask each tensor for as little
-# as will do, and the calls reach the library through names bound once.
-_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
-_CODES = {_F32: MOE_DTYPE_F32, _BF16: MOE_DTYPE_BF16, torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
+# The four calls themselves go through the extension module beside the library
+# (csrc/block_bind.cpp), which reads the tensors in C++: a call costs the host less
+# that way than its launch.  Each takes its extension's place at its first use.
+
+_F32 = torch.float32
+_CODES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
+_block = None
 
 
-def _bad(t, name, what):
-    raise ValueError(f"{name}: expected {what}, got {'CUDA' if t.is_cuda else 'CPU'} {t.dtype} of shape "
-                     f"{tuple(t.shape)}, strides {t.stride()}")
-
-
-def _rows(t, name, shape):
-    """(device pointer, dtype code, row stride) of a CUDA matrix of this shape whose rows are
-    contiguous (a single row's stride means nothing)."""
-    code = _CODES.get(t.dtype)
-    if code is None or not t.is_cuda or t.shape != shape:
-        _bad(t, name, f"a CUDA tensor {tuple(shape)} of a supported dtype")
-    ld, step = t.stride()
-    if step != 1 and shape[1] != 1:
-        _bad(t, name, "contiguous rows")
-    return t.data_ptr(), code, ld if shape[0] > 1 else shape[1]
-
-
-def _heads(t, name, shape):
-    """(device pointer, dtype code, strides between tokens and heads) of a CUDA tensor [T, heads, D]."""
-    code = _CODES.get(t.dtype)
-    if code is None or not t.is_cuda or t.shape != shape:
-        _bad(t, name, f"a CUDA tensor {tuple(shape)} of a supported dtype")
-    outer, inner, step = t.stride()
-    if step != 1 and shape[2] != 1:
-        _bad(t, name, "contiguous rows")
-    return t.data_ptr(), code, outer, inner
+def _block_call(name):
+    """The extension's function; binds it to the loaded library the first time."""
+    global _block
+    if _block is None:
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block_bind.so")
+        if not os.path.exists(path):
+            raise ImportError(f"extension module not built: {path} (run __graft_entry__.build())")
+        spec = importlib.util.spec_from_file_location("_block_bind", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project")
+        mod.bind(*(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check)
+        globals().update({n: getattr(mod, n) for n in names})
+        _block = mod
+    return getattr(_block, name)
 
 
 def _want(t, name, shape, dtype):
@@ -484,17 +477,8 @@ def _want(t, name, shape, dtype):
     if t is None:
         return None
     if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _bad(t, name, f"a contiguous CUDA {dtype} tensor {tuple(shape)}")
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor {tuple(shape)}")
     return t.data_ptr()
-
-
-def _table(t):
-    """(device pointer, row stride, requests, pages) of a block table."""
-    R, pages = t.shape
-    ld, step = t.stride()
-    if t.dtype is not _I32 or not t.is_cuda or (step != 1 and pages > 1):
-        _bad(t, "block_table", "a CUDA int32 tensor [requests, pages] with contiguous rows")
-    return t.data_ptr(), ld if R > 1 else pages, R, pages
 
 
 def moe_rmsnorm(x, weight, eps: float, y, residual=None, residual_out=None, y_scale=None):
@@ -503,30 +487,7 @@ def moe_rmsnorm(x, weight, eps: float, y, residual=None, residual_out=None, y_sc
     ``residual_out`` gets x + residual (it may be ``residual`` itself);
     ``weight`` [d] or None; ``y_scale`` goes with an E4M3 ``y``: float32 [T]
     (a scale per row) or [T, d / 128] (per 128 columns)."""
-    shape = x.shape
-    T, d = shape
-    x_ptr, x_code, x_ld = _rows(x, "x", shape)
-    y_ptr, y_code, y_ld = _rows(y, "y", shape)
-    r_ptr = ro_ptr = w_ptr = s_ptr = None
-    r_code = r_ld = ro_ld = w_code = group = 0
-    if residual is not None:
-        r_ptr, r_code, r_ld = _rows(residual, "residual", shape)
-    if residual_out is not None:
-        ro_ptr, code, ro_ld = _rows(residual_out, "residual_out", shape)
-        if residual is not None and code != r_code:
-            raise ValueError("residual and residual_out must have one dtype")
-        r_code = code
-    if weight is not None:
-        w_code = _CODES.get(weight.dtype, -1)
-        w_ptr = _want(weight, "weight", (d,), weight.dtype)
-    if y_scale is not None:
-        if y_scale.dim() == 2:
-            group = 128
-        s_ptr = _want(y_scale, "y_scale", (T, d // 128) if group else (T,), _F32)
-    rc = (_lib or lib()).moe_rmsnorm(x_ptr, x_code, x_ld, r_ptr, r_code, r_ld, ro_ptr, ro_ld, w_ptr, w_code, eps, T, d,
-                                     y_ptr, y_code, y_ld, s_ptr, group, _raw_stream(_current_device()))
-    if rc:
-        _check("moe_rmsnorm", rc)
+    _block_call("moe_rmsnorm")(x, weight, eps, y, residual, residual_out, y_scale)
 
 
 class KvCache:
@@ -541,14 +502,14 @@ class KvCache:
         pages, page, heads, D = k.shape
         for name, t in (("k", k), ("v", v)):
             if t.dtype not in _CODES or not t.is_cuda or (t.stride(3) != 1 and D > 1):
-                _bad(t, name, "a CUDA tensor of a supported dtype with contiguous rows")
+                raise ValueError(f"{name}: expected a CUDA tensor of a supported dtype with contiguous rows")
         self.tensors = (k, v, k_scale, v_scale)
         self.heads, self.head_dim, self.page_size = heads, D, page
         self.args = KvCacheArgs(
             k.data_ptr(), v.data_ptr(), _want(k_scale, "k_scale", (heads,), _F32),
             _want(v_scale, "v_scale", (heads,), _F32), *k.stride()[:3], *v.stride()[:3], _CODES[k.dtype],
             pages, page, heads, D)
-        self.ref = C.byref(self.args)
+        self.address = C.addressof(self.args)
 
 
 def moe_kv_append(k, v, cache: KvCache, block_table, positions, req=None, cos_sin=None, q=None, q_out=None,
@@ -558,35 +519,7 @@ def moe_kv_append(k, v, cache: KvCache, block_table, positions, req=None, cos_si
     ``block_table`` int32 [R, pages]; ``positions`` int32 [T]; ``req`` int32 [T]
     or None (token t is request t); ``cos_sin`` float32 [positions, rot] or
     None; ``q_out`` may be ``q``; ``status`` int32 [1] or None."""
-    T = k.shape[0]
-    shape = (T, cache.heads, cache.head_dim)
-    k_ptr, code, k_t, k_h = _heads(k, "k", shape)
-    v_ptr, v_code, v_t, v_h = _heads(v, "v", shape)
-    if v_code != code:
-        raise ValueError("k and v must have one dtype")
-    q_ptr = o_ptr = cs_ptr = None
-    q_t = q_h = o_t = o_h = q_heads = max_pos = rot = 0
-    if q is not None:
-        if q_out is None:
-            raise ValueError("q without q_out")
-        q_heads = q.shape[1]
-        shape = (T, q_heads, cache.head_dim)
-        q_ptr, q_code, q_t, q_h = _heads(q, "q", shape)
-        o_ptr, o_code, o_t, o_h = _heads(q_out, "q_out", shape)
-        if q_code != code or o_code != code:
-            raise ValueError("q, q_out and k must have one dtype")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if cos_sin is not None:
-        max_pos, rot = cos_sin.shape
-        cs_ptr = _want(cos_sin, "cos_sin", (max_pos, rot), _F32)
-    table, ld, R, pages = _table(block_table)
-    rc = (_lib or lib()).moe_kv_append(
-        k_ptr, k_t, k_h, v_ptr, v_t, v_h, code, T, cache.ref, table, ld, R, pages,
-        _want(positions, "positions", (T,), _I32), _want(req, "req", (T,), _I32), cs_ptr, rot, max_pos, q_ptr, q_t, q_h,
-        o_ptr, o_t, o_h, q_heads, _want(status, "status", (1,), _I32), _raw_stream(_current_device()))
-    if rc:
-        _check("moe_kv_append", rc)
+    _block_call("moe_kv_append")(k, v, cache, block_table, positions, req, cos_sin, q, q_out, status)
 
 
 def moe_attn_workspace_bytes(B: int, q_heads: int, heads: int, head_dim: int) -> int:
@@ -608,21 +541,7 @@ def moe_attn_decode(q, cache: KvCache, block_table, seq_lens, scale: float, out,
     """Attention of one new token per request: q, out [B, q_heads, D],
     ``block_table`` int32 [B, pages], ``seq_lens`` int32 [B] (the new token
     included), ``lse`` float32 [B, q_heads] or None."""
-    shape = q.shape
-    B, hq, D = shape
-    if D != cache.head_dim:
-        raise ValueError("q must be [B, q_heads, D] of the cache's D")
-    q_ptr, q_code, q_b, q_h = _heads(q, "q", shape)
-    o_ptr, o_code, o_b, o_h = _heads(out, "out", shape)
-    table, ld, R, pages = _table(block_table)
-    if R != B:
-        raise ValueError("block_table must have a row per request")
-    rc = (_lib or lib()).moe_attn_decode(
-        q_ptr, q_code, q_b, q_h, B, hq, cache.ref, table, ld, pages, _want(seq_lens, "seq_lens", (B,), _I32), scale,
-        window, softcap, o_ptr, o_code, o_b, o_h, _want(lse, "lse", (B, hq), _F32), _ptr(ws), ws.numel(),
-        _raw_stream(_current_device()))
-    if rc:
-        _check("moe_attn_decode", rc)
+    _block_call("moe_attn_decode")(q, cache, block_table, seq_lens, scale, out, ws, window, softcap, lse)
 
 
 def moe_lora_workspace_bytes(T: int, d: int, r: int) -> int:
@@ -645,31 +564,4 @@ def moe_lora_project(x, w, y, ws, lora=None, adapter=None, x_scale=None, w_scale
 
     x [T, d] float32 or bfloat16 with bfloat16 w [N, d]; or both E4M3 with
     ``x_scale`` float32 [T] and ``w_scale`` float32 [N]."""
-    x_shape, w_shape = x.shape, w.shape
-    T, d = x_shape
-    N = w_shape[0]
-    if w_shape[1] != d:
-        raise ValueError("x must be [T, d] and w [N, d]")
-    x_ptr, x_code, x_ld = _rows(x, "x", x_shape)
-    w_ptr, w_code, w_ld = _rows(w, "w", w_shape)
-    y_ptr, y_code, y_ld = _rows(y, "y", (T, N))
-    la = lb = ls = ad = xs = wsc = None
-    n = r = 0
-    if lora is not None:
-        A, Bm, scale = lora
-        n, r, _ = A.shape
-        la = _want(A, "lora A", (n, r, d), _BF16)
-        lb = _want(Bm, "lora B", (n, N, r), _BF16)
-        ls = _want(scale, "lora scale", (n,), _F32)
-        ad = _want(adapter, "adapter", (T,), _I32)
-    elif adapter is not None:
-        raise ValueError("adapter without lora")
-    if x_scale is not None:
-        xs = _want(x_scale, "x_scale", (T,), _F32)
-    if w_scale is not None:
-        wsc = _want(w_scale, "w_scale", (N,), _F32)
-    rc = (_lib or lib()).moe_lora_project(
-        x_ptr, x_code, x_ld, xs, T, d, w_ptr, w_code, w_ld, wsc, N, la, lb, ls, n, r, ad, y_ptr, y_code, y_ld,
-        _ptr(ws), ws.numel(), _raw_stream(_current_device()))
-    if rc:
-        _check("moe_lora_project", rc)
+    _block_call("moe_lora_project")(x, w, y, ws, lora, adapter, x_scale, w_scale)

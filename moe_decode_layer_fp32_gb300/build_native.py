@@ -1,7 +1,8 @@
 """Build the native library ``libmoe_gb300.so`` in-tree for sm_103a.
 
 Each CUDA translation unit is compiled to an object in parallel, then linked
-into one shared library next to this file.  Objects are rebuilt only when a
+into one shared library next to this file; beside it goes the extension module
+that hands torch tensors to the decode-block calls.  Objects are rebuilt only when a
 source or header is newer.  Set ``MOE_PTXAS_VERBOSE=1`` to print register and
 shared-memory use per kernel.
 """
@@ -9,10 +10,12 @@ shared-memory use per kernel.
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BIND = os.path.join(PKG, "_block_bind.so")
 SOURCES = ("api.cu", "route_dispatch.cu", "ffn.cu", "ffn_tc.cu", "balance.cu", "formp.cu",
            "block_api.cu", "norm.cu", "kv_append.cu", "attn_decode.cu", "lora_project.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,6 +59,16 @@ def _run(cmd):
     return r.stdout
 
 
+def _bind_command():
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
+    lib = os.path.join(torch, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "block_bind.cpp"), "-o", BIND]
+            + [a for i in inc for a in ("-I", i)]
+            + ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = nvcc_path()
     os.makedirs(OBJDIR, exist_ok=True)
@@ -69,13 +83,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         o = os.path.join(OBJDIR, src.replace(".cu", ".o"))
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, "-c", s, "-o", o] + flags)
+    compiled = list(jobs)
+    if force or _stale(BIND, [os.path.join(CSRC, "block_bind.cpp")] + [
+            os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]):
+        jobs.append(_bind_command())
     if jobs:
         with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             for out in ex.map(_run, jobs):
                 if verbose or os.environ.get("MOE_PTXAS_VERBOSE"):
                     sys.stdout.write(out)
     objs = [os.path.join(OBJDIR, s.replace(".cu", ".o")) for s in SOURCES]
-    if force or jobs or _stale(LIB, objs):
+    if force or compiled or _stale(LIB, objs):
         _run([nvcc, "-shared", "-cudart", "shared"] + ARCH + objs + ["-o", LIB])
     return LIB
 
