@@ -25,7 +25,8 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 BIND = os.path.join(PKG, "_block_bind.so")
 SOURCES = ("api.cu", "route_dispatch.cu", "ffn.cu", "ffn_tc.cu", "balance.cu", "formp.cu",
-           "block_api.cu", "norm.cu", "kv_append.cu", "attn_decode.cu", "lora_project.cu")
+           "block_api.cu", "norm.cu", "kv_append.cu", "attn_decode.cu", "lora_project.cu",
+           "lora_gemv.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -89,6 +89,10 @@ constexpr int kLoraMaxT = 128;
 constexpr int kLoraMaxRank = 128;
 size_t lora_workspace_bytes(int T, int d, int r, size_t* v_off, size_t* xs_off);
 cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s);
+// One or two tokens on the CUDA cores; unless lora_gemv_own_v, a.v has been formed before.
+bool lora_gemv_fits(const LoraArgs& a);
+bool lora_gemv_own_v(const LoraArgs& a);
+cudaError_t launch_lora_gemv(const LoraArgs& a, cudaStream_t s);
 
 // Allows a kernel `bytes` of dynamic shared memory, once per device: `done` is the kernel's own.
 inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
@@ -157,6 +161,29 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
 __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 8 elements of any of the three types.
+__device__ __forceinline__ void load8_any(const void* p, int dt, long long i, float (&f)[8]) {
+    if (dt == MOE_DTYPE_FP8_E4M3) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i);
+        const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 u = unpack_e4m3x2(w[e]);
+            f[2 * e] = u.x;
+            f[2 * e + 1] = u.y;
+        }
+    } else {
+        load8_f32(p, dt, i, f);
+    }
+}
+
+// -1 for a token without an adapter; an index beyond the adapters is reported and counts as none.
+__device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
+    const int i = a.adapter[t];
+    if (i >= a.na) set_status(a.status, MOE_ERR_DEVICE);
+    return i >= 0 && i < a.na ? i : -1;
 }
 
 // C += A B: 16 x 16 by 16 x 8, bf16 into fp32.

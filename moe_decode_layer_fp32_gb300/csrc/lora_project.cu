@@ -42,28 +42,6 @@ constexpr int kProjSmem = 226 * 1024;
 
 // ---- v = A_a x, and the bf16 terms of fp32 activations -----------------------
 
-__device__ __forceinline__ void load8_any(const void* p, int dt, long long i, float (&f)[8]) {
-    if (dt == MOE_DTYPE_FP8_E4M3) {
-        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i);
-        const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 u = unpack_e4m3x2(w[e]);
-            f[2 * e] = u.x;
-            f[2 * e + 1] = u.y;
-        }
-    } else {
-        load8_f32(p, dt, i, f);
-    }
-}
-
-// -1 for a token without an adapter; an index beyond the adapters is reported and counts as none.
-__device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
-    const int i = a.adapter[t];
-    if (i >= a.na) set_status(a.status, MOE_ERR_DEVICE);
-    return i >= 0 && i < a.na ? i : -1;
-}
-
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkTc = 1024;             // tokens times rank from which A x goes to the tensor cores
 
@@ -763,8 +741,10 @@ cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s) {
     const bool f32 = a.x_dt == MOE_DTYPE_F32, f8 = a.x_dt == MOE_DTYPE_FP8_E4M3;
     // v = A_a x: many rows on the tensor cores, which read each adapter once for all its
     // tokens; a few are done sooner by one small kernel, together with the terms of x.
-    const bool tc = a.T * a.r >= kShrinkTc;
-    const int split_blocks = f32 || (f8 && tc)
+    const bool gemv = lora_gemv_fits(a);
+    if (gemv && (a.r == 0 || lora_gemv_own_v(a))) return launch_lora_gemv(a, s);
+    const bool tc = !gemv && a.T * a.r >= kShrinkTc;
+    const int split_blocks = (f32 && !gemv) || (f8 && tc)
                                  ? std::min(4 * device_sm_count(), (a.T * (a.d / 8) + kShrinkThreads - 1) / kShrinkThreads) : 0;
     const bool few = a.T * a.r / 8 < 4 * device_sm_count();    // 2 rows of A per block: more SMs share the reading
     const int shrink_blocks = tc ? 0 : a.T * (a.r / (few ? 2 : 8));
@@ -774,6 +754,7 @@ cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s) {
                        dim3(kShrinkThreads), 0, s, a, shrink_blocks);
     if (e == cudaSuccess && tc) e = f32 ? launch_tp<false, 3, true>(a, s) : launch_tp<false, 1, true>(a, s);
     if (e != cudaSuccess) return e;
+    if (gemv) return launch_lora_gemv(a, s);
     if (f8) return launch_tp<true, 1, false>(a, s);
     return f32 ? launch_tp<false, 3, false>(a, s) : launch_tp<false, 1, false>(a, s);
 }
