@@ -49,29 +49,61 @@ constexpr int kProjSmem = 226 * 1024;
 // ---- v = A_a x, and the bf16 terms of fp32 activations -----------------------
 
 constexpr int kShrinkThreads = 256;
-// Tokens times rank from which A x goes to the tensor cores: at 512 (32 tokens, d 7168) the small kernel
-// takes 7.5 us, at 8192 26 us against 25, which it does for shared adapters too.
-constexpr int kShrinkTc = 1024;
+constexpr int kShrinkMany = 2048;           // rows of A in all from which a warp takes two
 
-// Blocks [0, T r / ROWS): ROWS rows of A_a against x[t], d shared out over the block's
-// threads.  The blocks after them write the terms of x: three bf16 of fp32, one of E4M3
-// (which bf16 holds exactly).
-template <int ROWS>
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ LoraArgs a, int shrink_blocks) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// 8 elements of x as loaded.
+template <int DT>
+struct XRaw {
+    uint4 w[DT == MOE_DTYPE_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* p, long long i) {
+        if constexpr (DT == MOE_DTYPE_F32) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+            w[0] = q[0];
+            w[1] = q[1];
+        } else if constexpr (DT == MOE_DTYPE_BF16) {
+            w[0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i);
+            w[0].x = v.x;
+            w[0].y = v.y;
+        }
+    }
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        if constexpr (DT == MOE_DTYPE_F32) {
+            f[0] = make_float2(__uint_as_float(w[0].x), __uint_as_float(w[0].y));
+            f[1] = make_float2(__uint_as_float(w[0].z), __uint_as_float(w[0].w));
+            f[2] = make_float2(__uint_as_float(w[1].x), __uint_as_float(w[1].y));
+            f[3] = make_float2(__uint_as_float(w[1].z), __uint_as_float(w[1].w));
+        } else if constexpr (DT == MOE_DTYPE_BF16) {
+            unpack_bf16x8_f2(w[0], f);
+        } else {
+            f[0] = unpack_e4m3x2(w[0].x);
+            f[1] = unpack_e4m3x2(w[0].x >> 16);
+            f[2] = unpack_e4m3x2(w[0].y);
+            f[3] = unpack_e4m3x2(w[0].y >> 16);
+        }
+    }
+};
+
+// Blocks [0, shrink_blocks): a warp takes ROWS rows of A_a against x[t], with the loads of
+// several steps along d together and no barrier: HBM (L2 for adapters that several tokens
+// share) bounds it, and it runs beside the projection kernel's first copies of W.  The
+// blocks after them write the three bf16 terms of fp32 x.
+template <int DT, int ROWS>
+__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __grid_constant__ LoraArgs a, int shrink_blocks) {
+    constexpr int kSteps = DT == MOE_DTYPE_F32 ? 4 : 8;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunks = a.d / 8;
     pdl_allow_dependents();
     pdl_wait_primary();
-    const int groups = a.r / ROWS;
     if ((int)blockIdx.x >= shrink_blocks) {
-        const int chunks = a.d / 8;
         const long long plane = (long long)a.T * a.d;
         for (int i = (blockIdx.x - shrink_blocks) * kShrinkThreads + tid; i < a.T * chunks;
              i += (gridDim.x - shrink_blocks) * kShrinkThreads) {
             const int t = i / chunks, c = (i - t * chunks) * 8;
             float f[8];
-            load8_any(a.x, a.x_dt, t * a.x_ld + c, f);
-            const int terms = a.x_dt == MOE_DTYPE_F32 ? 3 : 1;
-            for (int p = 0; p < terms; ++p) {
+            load8_f32(a.x, MOE_DTYPE_F32, t * a.x_ld + c, f);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -88,39 +120,50 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
         }
         return;
     }
-    __shared__ float s_part[kShrinkThreads / 32][ROWS];
-    const int t = blockIdx.x / groups, j0 = (blockIdx.x - t * groups) * ROWS;
+    const int unit = blockIdx.x * (kShrinkThreads / 32) + warp;
+    if (unit >= a.T * a.r / ROWS) return;
+    const int t = unit / (a.r / ROWS), j0 = (unit - t * (a.r / ROWS)) * ROWS;
     const int ad = adapter_of(a, t);
-    float sum[ROWS] = {};
-    if (ad >= 0) {
-        const __nv_bfloat16* rows = a.la + ((long long)ad * a.r + j0) * a.d;
-#pragma unroll (ROWS == 2 ? 4 : 2)
-        for (int c = tid * 8; c < a.d; c += kShrinkThreads * 8) {
-            float x[8];
-            load8_any(a.x, a.x_dt, t * a.x_ld + c, x);
-            uint4 w[ROWS];
+    if (ad < 0) return;                  // nobody reads its v
+    const uint4* rows = reinterpret_cast<const uint4*>(a.la + ((long long)ad * a.r + j0) * a.d);
+    float2 sum[ROWS][4];
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(rows + (long long)j * a.d + c));
+    for (int j = 0; j < ROWS; ++j)
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                float u[8];
-                unpack_bf16x8(w[j], u);
+        for (int e = 0; e < 4; ++e) sum[j][e] = make_float2(0.0f, 0.0f);
+    for (int c0 = lane; c0 < chunks; c0 += 32 * kSteps) {
+        uint4 w[kSteps][ROWS];
+        XRaw<DT> x[kSteps];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum[j] = fmaf(u[e], x[e], sum[j]);
+        for (int k = 0; k < kSteps; ++k) {
+            const int c = c0 + 32 * k;
+            if (c < chunks) {
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j) w[k][j] = __ldg(rows + (long long)j * chunks + c);
+                x[k].load(a.x, t * a.x_ld + c * 8);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            if (c0 + 32 * k < chunks) {
+                float2 v[4];
+                x[k].get(v);
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j) {
+                    float2 u[4];
+                    unpack_bf16x8_f2(w[k][j], u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[j][e] = ffma2(u[e], v[e], sum[j][e]);
+                }
             }
         }
     }
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-        const float s = warp_sum(sum[j]);
-        if (lane == 0) s_part[warp][j] = s;
-    }
-    __syncthreads();
-    if (tid < ROWS) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kShrinkThreads / 32; ++w) s += s_part[w][tid];
-        a.v[t * a.r + j0 + tid] = a.x_scale ? s * a.x_scale[t] : s;
+        const float2 p = make_float2((sum[j][0].x + sum[j][1].x) + (sum[j][2].x + sum[j][3].x),
+                                     (sum[j][0].y + sum[j][1].y) + (sum[j][2].y + sum[j][3].y));
+        const float s = warp_sum(p.x + p.y);
+        if (lane == 0) a.v[t * a.r + j0 + j] = a.x_scale ? s * a.x_scale[t] : s;
     }
 }
 
@@ -128,7 +171,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
 
 struct ProjArgs {
     LoraArgs l;
-    CUtensorMap wmap, xmap;     // W [N, d] (shrink: A [na r, d], boxes of r rows); x [T, d], or its terms [3, T, d]
+    CUtensorMap wmap, xmap;     // W [N, d]; x [T, d], or its terms [3, T, d]
     CUtensorMap bmap;           // B [na N, r]
     int blocks;                 // 128-byte blocks of a row
     int split;                  // CTAs of a cluster
@@ -174,9 +217,7 @@ struct ProjShared {
     alignas(16) int key[kLoraMaxT];   // adapter of each token (beyond the tokens: INT_MAX)
     int order[kLoraMaxT];      // tokens by adapter (those without first), then by index
     int skey[kLoraMaxT];       // their adapters in that order
-    int index[kLoraMaxT];      // ... and the adapters' places among those in use (-1: none)
-    int used[kLoraMaxT];       // the adapters in use
-    int seg[kLoraMaxT + 1];    // projection: first sorted token of each adapter among the own tokens
+    int seg[kLoraMaxT + 1];    // first sorted token of each adapter among the own tokens
     int segs;
     int starts[kLoraMaxT / 32];
     float scale[kLoraMaxT];    // adapters' scales, by sorted token
@@ -211,10 +252,8 @@ __host__ __device__ inline int lora_stage_bytes(int r) {
 __host__ __device__ inline int v_stride(int r) { return (r + 15) / 16 * 16 + 8; }
 
 // TP: tokens rounded up to 16, 32, 64 or 128 (MMA columns).  F8: E4M3.  TERMS: bf16
-// terms of x (1, or 3 for fp32).  SHRINK: the same stream over the rows of A in the place
-// of W, as many whole adapters in use per tile as 128 rows hold; each token keeps the
-// rows of its own, v[t] = A_a x[t].
-template <int TP, bool F8, int TERMS, bool SHRINK>
+// terms of x (1, or 3 for fp32).
+template <int TP, bool F8, int TERMS>
 __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __grid_constant__ ProjArgs p) {
     constexpr int kAccs = TERMS > 1 ? 2 : 1;                  // the first term's sum, and the others'
     constexpr uint32_t kBufCols = kAccs * TP;
@@ -234,7 +273,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = p.split > 1 ? (int)cluster_rank() : 0;
-    const int tile = (int)(blockIdx.x / p.split), n0 = SHRINK ? 0 : tile * kRowsM;
+    const int n0 = (int)(blockIdx.x / p.split) * kRowsM;
     const int kb0 = p.blocks * rank / p.split, kb1 = p.blocks * (rank + 1) / p.split;
     const int nkb = kb1 - kb0, chunks = (nkb + kChunkBlocks - 1) / kChunkBlocks;
     // positions of the sorted tokens that this CTA adds up and writes
@@ -251,13 +290,13 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         }
         for (int i = 0; i < kLoraStages; ++i) {
             mbar_init(&sm.lfull[i], 1);
-            mbar_init(&sm.lempty[i], 1);
+            mbar_init(&sm.lempty[i], 4);
         }
         mbar_init(&sm.mma_done, 1);
         mbar_init_fence();
         tma_prefetch_map(&p.wmap);
         tma_prefetch_map(&p.xmap);
-        if (!SHRINK && a.r > 0) tma_prefetch_map(&p.bmap);
+        if (a.r > 0) tma_prefetch_map(&p.bmap);
     }
     if (warp == 1) {
         tmem_alloc(&sm.tmem, kTmemCols);
@@ -282,39 +321,27 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     const uint64_t pol = l2_policy_evict_first();
     constexpr int kColsPerBlock = F8 ? 128 : 64;
     const int early = min(nkb, p.stages);
-    // shrink: the tile's adapters are used[first_ad .. + ads)
-    const int per_tile = SHRINK ? kRowsM / a.r : 0, first_ad = tile * per_tile;
-    int ads = 0;
     auto load_w = [&](int i) {
         const int slot = i % p.stages;
-        unsigned char* dst = ring + slot * kStageBytes;
-        if constexpr (SHRINK) {
-            mbar_arrive_expect_tx(&sm.full[slot], kStageBytes - kWBytes + ads * a.r * kBlockBytes);
-            for (int k = 0; k < ads; ++k)
-                tma_load_2d(dst + k * a.r * kBlockBytes, &p.wmap, (kb0 + i) * kColsPerBlock, sm.used[first_ad + k] * a.r,
-                            &sm.full[slot], pol);
-        } else {
-            mbar_arrive_expect_tx(&sm.full[slot], kStageBytes);
-            tma_load_2d(dst, &p.wmap, (kb0 + i) * kColsPerBlock, n0, &sm.full[slot], pol);
-        }
+        mbar_arrive_expect_tx(&sm.full[slot], kStageBytes);
+        tma_load_2d(ring + slot * kStageBytes, &p.wmap, (kb0 + i) * kColsPerBlock, n0, &sm.full[slot], pol);
     };
-    if (!SHRINK && warp == 0 && lane == 0)
+    if (warp == 0 && lane == 0)
         for (int i = 0; i < early; ++i) load_w(i);
 
     pdl_wait_primary();
 
     // ---- order of the tokens: by the warps that need it first (the adapters' copies and
-    // products; in the shrink form the W copies too, so all of them), the others go ahead
-    const bool sorter = SHRINK || warp == 2 || (warp >= 4 && warp < 8);
-    constexpr int kSorters = SHRINK ? kProjThreads : 160;
-    const int sid = SHRINK ? tid : warp == 2 ? 128 + lane : tid - 128;
-    auto sort_sync = [&] { named_bar_sync(1, kSorters); };
+    // products), the others go ahead
+    const bool sorter = warp == 2 || (warp >= 4 && warp < 8);
+    const int sid = warp == 2 ? 128 + lane : tid - 128;
+    auto sort_sync = [&] { named_bar_sync(1, 160); };
     if (a.r > 0 && sorter) {
         float scale = 0.0f;
         if (sid < kLoraMaxT) {
             const int k = sid < a.T ? adapter_of(a, sid) : INT_MAX;
             sm.key[sid] = k;
-            if (!SHRINK && sid < a.T && k >= 0) scale = a.ls[k];
+            if (sid < a.T && k >= 0) scale = a.ls[k];
         }
         sort_sync();
         if (sid < a.T) {
@@ -331,35 +358,24 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             sm.scale[pos] = scale;
         }
         sort_sync();
-        // A sorted token whose adapter differs from the one before starts an adapter in use: of all
-        // tokens (shrink) or of the own ones.
-        {
-            const int q0 = SHRINK ? 0 : p0, q1 = SHRINK ? a.T : p1;
-            const bool start = sid < a.T && sid >= q0 && sid < q1 && sm.skey[sid] >= 0 &&
-                               (sid == q0 || sm.skey[sid - 1] != sm.skey[sid]);
-            const uint32_t bits = __ballot_sync(0xffffffffu, start);
-            if (sid < kLoraMaxT && lane == 0) sm.starts[sid / 32] = __popc(bits);
-            sort_sync();
-            int before = 0, count = 0;
+        // an own token whose adapter differs from the one before starts an adapter in use
+        const bool start = sid >= p0 && sid < p1 && sm.skey[sid] >= 0 && (sid == p0 || sm.skey[sid - 1] != sm.skey[sid]);
+        const uint32_t bits = __ballot_sync(0xffffffffu, start);
+        if (sid < kLoraMaxT && lane == 0) sm.starts[sid / 32] = __popc(bits);
+        sort_sync();
+        int before = 0, count = 0;
 #pragma unroll
-            for (int w = 0; w < kLoraMaxT / 32; ++w) {
-                if (w < sid / 32) before += sm.starts[w];
-                count += sm.starts[w];
-            }
-            if (sid < a.T) {
-                const int index = before + __popc(bits & (0xffffffffu >> (31 - lane))) - 1;
-                if (SHRINK) sm.index[sid] = sm.skey[sid] >= 0 ? index : -1;
-                if (start && SHRINK) sm.used[index] = sm.skey[sid];
-                if (start && !SHRINK) sm.seg[index] = sid;
-            }
-            if (!SHRINK && sid == 0) {
-                sm.segs = count;
-                sm.seg[count] = p1;
-            }
-            sort_sync();
-            if (SHRINK) ads = max(0, min(per_tile, count - first_ad));
+        for (int w = 0; w < kLoraMaxT / 32; ++w) {
+            if (w < sid / 32) before += sm.starts[w];
+            count += sm.starts[w];
         }
-        if (!SHRINK && warp != 2) {
+        if (start) sm.seg[before + __popc(bits & (0xffffffffu >> (31 - lane))) - 1] = sid;
+        if (sid == 0) {
+            sm.segs = count;
+            sm.seg[count] = p1;
+        }
+        sort_sync();
+        if (warp != 2) {
             const int vstr = v_stride(a.r), own = p1 - p0;
             // two elements of a token's v at a time, the loads of kAhead of them together
             constexpr int kAhead = 6;
@@ -391,12 +407,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     } else if (a.r == 0) {
         for (int t = tid; t < a.T; t += kProjThreads) sm.order[t] = t;
     }
-    if (SHRINK) __syncthreads();
-    const bool idle = SHRINK && ads == 0;          // a tile beyond the adapters in use
 
     if (warp == 0) {
         // ===================== TMA producer =====================
-        if (lane == 0 && !idle) {
+        if (lane == 0) {
             auto load_x = [&](int i) {
                 const int slot = i % p.stages;
                 unsigned char* dst = ring + slot * kStageBytes + kWBytes;
@@ -404,10 +418,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                 for (int t = 0; t < TERMS; ++t)
                     tma_load_3d_plain(dst + t * kXBytes, &p.xmap, (kb0 + i) * kColsPerBlock, 0, t, &sm.full[slot]);
             };
-            for (int i = 0; i < early; ++i) {
-                if (SHRINK) load_w(i);
-                load_x(i);
-            }
+            for (int i = 0; i < early; ++i) load_x(i);
             int i = early;
             for (; i < nkb; ++i) {
                 if (!wait(&sm.empty[i % p.stages], ((i / p.stages) & 1u) ^ 1u)) break;
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             const uint64_t a0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
             const uint64_t b0 = smem_desc_sw128(smem_u32(ring + kWBytes), 16, 1024);
             const uint32_t idesc = F8 ? idesc_e4m3_f32(128, TP) : idesc_bf16_f32(128, TP, false, false);
-            for (int c = 0; ok && !idle && c < chunks; ++c) {
+            for (int c = 0; ok && c < chunks; ++c) {
                 const uint32_t buf = c & 1;
                 if (!wait(&sm.acc_empty[buf], ((c >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after_sync();
@@ -453,14 +464,14 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         }
     } else if (warp == 2) {
         // ===================== adapter copies =====================
-        if (!SHRINK && lane == 0 && a.r > 0) {
+        if (lane == 0 && a.r > 0) {
             const int boxes = (a.r + 63) / 64, lstage = lora_stage_bytes(a.r);
             const uint32_t bulk = (uint32_t)min(kRowsM, a.N - n0) * a.r * 2;
-            int it = 0;
+            int it = 0, slot = 0;
+            uint32_t phase = 1;
             for (; it < sm.segs; ++it) {
                 const int ad = sm.skey[sm.seg[it]];
-                const int slot = it % p.lora_stages;
-                if (!wait(&sm.lempty[slot], ((it / p.lora_stages) & 1u) ^ 1u)) break;
+                if (!wait(&sm.lempty[slot], phase)) break;
                 if (lora_bulk(a.r)) {
                     mbar_arrive_expect_tx(&sm.lfull[slot], bulk);
                     bulk_load(lring + slot * lstage, a.lb + ((long long)ad * a.N + n0) * a.r, bulk, &sm.lfull[slot], pol);
@@ -469,34 +480,85 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                     for (int b = 0; b < boxes; ++b)
                         tma_load_2d(lring + slot * lstage + b * kLoraBox, &p.bmap, b * 64, ad * a.N + n0, &sm.lfull[slot], pol);
                 }
+                if (++slot == p.lora_stages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
             for (int j = max(0, it - p.lora_stages); j < it; ++j)
                 mbar_wait_bounded(&sm.lfull[j % p.lora_stages], (j / p.lora_stages) & 1u);
         }
     } else if (warp >= 4 && warp < 8) {
-        // ===================== adapters: B_a v, an adapter per warp, up to 8 of its tokens at once =====================
-        if (!SHRINK && a.r > 0) {
+        // ===================== adapters: B_a v, 32 of the tile's rows per warp, up to 8 tokens at once =====================
+        if (a.r > 0) {
             const int steps = (a.r + 15) / 16, lstage = lora_stage_bytes(a.r);
             // rows of 128 bytes with permuted chunks, or of 2 r bytes as they are
             const int pitch = lora_bulk(a.r) ? a.r * 2 : 128, swizzle = lora_bulk(a.r) ? 0 : 7;
             const int vstr = v_stride(a.r), own = p1 - p0, segs = sm.segs;
             // ldmatrix: lane's row and 16-byte chunk within a 16 x 16 block
-            const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
+            const int row0 = (warp - 4) * 32, lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
             for (int i = (warp - 4) * 32 + lane; i < (sm.seg[0] - p0) * kRowsM; i += 128) lacc[i] = 0.0f;
+            // one or two tokens of an adapter: the terms of v side by side in the MMA's 8 columns (token
+            // 0's in 0 to 2, token 1's in 4 to 6), a third of the MMAs
+            const int term = (lane / 4) & 3, second = lane / 16;
+            const __nv_bfloat16* v2 = vs + ((term < 3 ? term : 0) * own - p0 + second) * vstr + (lane & 3) * 2;
+            float* out2 = lacc + ((lane & 3) / 2 - p0) * kRowsM + row0 + lane / 4;
+            const int steps4 = min(steps, 4);
+            const uint32_t at0 = smem_u32(lring) + (row0 + lrow) * pitch;
+            uint32_t flip[4];                // byte of the lane's chunk in each k16 step
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) flip[ks] = ((ks * 2 + lch) ^ (lrow & swizzle)) << 4;
+            int slot = 0, first = sm.seg[0], next = sm.seg[segs > 0];
+            uint32_t phase = 0;
             for (int it = 0; it < segs; ++it) {
-                // a slot belongs to one warp: a wait by parity holds only for a waiter that has seen
-                // the slot's phase before
-                const int slot = it % p.lora_stages, end = sm.seg[it + 1];
-                if (slot % 4 != warp - 4) continue;
-                wait(&sm.lfull[slot], (it / p.lora_stages) & 1u);
+                const int end = next;
+                if (it + 2 <= segs) next = sm.seg[it + 2];
+                const bool packed = end - first <= 2;
+                uint32_t pb[4][2];
+                auto load_packed = [&](int k0, int n) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        pb[ks][0] = pb[ks][1] = 0u;
+                        if (ks < n && term < 3 && first + second < end) {
+                            pb[ks][0] = *reinterpret_cast<const uint32_t*>(v2 + first * vstr + (k0 + ks) * 16);
+                            pb[ks][1] = *reinterpret_cast<const uint32_t*>(v2 + first * vstr + (k0 + ks) * 16 + 8);
+                        }
+                    }
+                };
+                if (packed) load_packed(0, steps4);
+                wait(&sm.lfull[slot], phase);
                 __syncwarp();
-                const uint32_t tile_b = smem_u32(lring + slot * lstage) + lrow * pitch;
-                for (int q = sm.seg[it]; q < end; q += 8) {
+                const uint32_t tile_b = at0 + slot * lstage;
+                if (packed) {
+                    const bool write = (lane & 1) == 0 && first + (lane & 3) / 2 < end;
+                    float* out = out2 + first * kRowsM;
+                    for (int k0 = 0; k0 < steps; k0 += 4) {
+                        if (k0 > 0) load_packed(k0, steps - k0);
+                        float c[2][4] = {};
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (k0 + ks < steps) {
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) {
+                                    uint32_t f[4];
+                                    ldmatrix_x4(tile_b + (k0 >> 2) * kLoraBox + m * 16 * pitch + flip[ks], f);
+                                    mma_bf16(c[m], f[0], f[1], f[2], f[3], pb[ks][0], pb[ks][1]);
+                                }
+                            }
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const float lo = c[h / 2][h % 2 * 2], hi = c[h / 2][h % 2 * 2 + 1];
+                            const float s = lo + (hi + __shfl_xor_sync(0xffffffffu, lo, 1));
+                            if (write) out[h * 8] = k0 == 0 ? s : out[h * 8] + s;
+                        }
+                    }
+                } else
+                for (int q = first; q < end; q += 8) {
                     const int count = min(8, end - q);
                     const __nv_bfloat16* v = vs + (q - p0 + lane / 4) * vstr + (lane & 3) * 2;
-                    float* out = lacc + (q - p0 + (lane & 3) * 2) * kRowsM + lane / 4;
+                    float* out = lacc + (q - p0 + (lane & 3) * 2) * kRowsM + row0 + lane / 4;
                     const bool t0 = (lane & 3) * 2 < count, t1 = (lane & 3) * 2 + 1 < count;
-                    // up to 64 columns of B_a at a time: v's fragments stay in registers over the 128 rows
+                    // up to 64 columns of B_a at a time: v's fragments stay in registers over the rows
                     for (int k0 = 0; k0 < steps; k0 += 4) {
                         uint32_t b[4][3][2] = {};
                         if (lane / 4 < count) {
@@ -510,14 +572,14 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                                     }
                                 }
                         }
-#pragma unroll 2
-                        for (int m = 0; m < kRowsM; m += 16) {
+#pragma unroll
+                        for (int m = 0; m < 32; m += 16) {
                             float c[3][4] = {};             // a sum per term: short chains of MMAs
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 if (k0 + ks < steps) {
                                     uint32_t f[4];
-                                    ldmatrix_x4(tile_b + (k0 >> 2) * kLoraBox + m * pitch + (((ks * 2 + lch) ^ (lrow & swizzle)) << 4), f);
+                                    ldmatrix_x4(tile_b + (k0 >> 2) * kLoraBox + m * pitch + flip[ks], f);
 #pragma unroll
                                     for (int k = 0; k < 3; ++k) mma_bf16(c[k], f[0], f[1], f[2], f[3], b[ks][k][0], b[ks][k][1]);
                                 }
@@ -532,6 +594,11 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.lempty[slot]);
+                first = end;
+                if (++slot == p.lora_stages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
         }
     } else if (warp >= 8) {
@@ -540,7 +607,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 #pragma unroll
         for (int t = 0; t < TP; ++t) acc[t] = 0.0f;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        for (int c = 0; c < chunks && !idle; ++c) {
+        for (int c = 0; c < chunks; ++c) {
             const uint32_t buf = c & 1;
             if (!__all_sync(0xffffffffu, wait(&sm.acc_full[buf], (c >> 1) & 1u))) break;
             tc_fence_after_sync();
@@ -572,15 +639,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     const int warps = kProjThreads / 32;
     for (int q = p0 + warp; q < p1; q += warps) {
         const int t = sm.order[q];
-        int col = lane * 4;                      // of the tile's 128 rows
-        if constexpr (SHRINK) {
-            const int k = sm.index[q] - first_ad;
-            if (sm.index[q] < 0 || k < 0 || k >= ads || col >= a.r) continue;
-            col += k * a.r;
-        }
-        const int n = n0 + col;
+        const int n = n0 + lane * 4;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float* at = red + t * kRowsM + col;
+        const float* at = red + t * kRowsM + lane * 4;
         if (p.split > 1) {
 #pragma unroll 8
             for (int k = 0; k < p.split; ++k) {
@@ -590,10 +651,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         } else {
             s = *reinterpret_cast<const float4*>(at);
         }
-        if constexpr (SHRINK) {
-            const float f = a.x_scale ? a.x_scale[t] : 1.0f;
-            *reinterpret_cast<float4*>(a.v + t * a.r + lane * 4) = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
-        } else if (n < a.N) {
+        if (n < a.N) {
             if constexpr (F8) {
                 const float xs = a.x_scale[t];
                 s.x *= xs * a.w_scale[n];
@@ -653,19 +711,17 @@ bool encode_rows(CUtensorMap* m, const void* ptr, int planes, long long rows, in
 
 inline int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
-template <int TP, bool F8, int TERMS, bool SHRINK>
+template <int TP, bool F8, int TERMS>
 cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     const LoraArgs& a = p.l;
     constexpr int kStageBytes = kWBytes + TERMS * TP * kBlockBytes;
-    auto kern = lora_project_kernel<TP, F8, TERMS, SHRINK>;
+    auto kern = lora_project_kernel<TP, F8, TERMS>;
     static std::atomic<uint64_t> done;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kProjSmem, done);
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count();
-    // shrink: at most min(T, na) adapters are in use
-    const int per_tile = SHRINK ? kRowsM / a.r : 1;
-    const int tiles = SHRINK ? (std::min(a.T, a.na) + per_tile - 1) / per_tile : (a.N + kRowsM - 1) / kRowsM;
-    const bool low = !SHRINK && a.r > 0;
+    const int tiles = (a.N + kRowsM - 1) / kRowsM;
+    const bool low = a.r > 0;
     p.blocks = (a.d * (F8 ? 1 : 2) + kBlockBytes - 1) / kBlockBytes;
     // Split d while the clusters still run at once (a cluster of 8 does not fill a
     // GPC: about 7/8 of the SMs) and a CTA keeps two blocks or more.
@@ -701,13 +757,10 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     const size_t smem = std::max((size_t)(1024 + p.wring_off + std::max(p.stages * kStageBytes, a.T * kRowsM * 4)),
                                  (size_t)116 * 1024);
     if (p.stages < 1 || smem > (size_t)kProjSmem) return cudaErrorInvalidConfiguration;
-    // fp32 x comes as its terms, and so does E4M3 x for the bf16 rows of A
-    const bool terms = TERMS == 3 || (SHRINK && a.x_dt == MOE_DTYPE_FP8_E4M3);
-    const bool maps =
-        (SHRINK ? encode_rows(&p.wmap, a.la, 0, (long long)a.na * a.r, a.d, a.d, a.r, false)
-                : encode_rows(&p.wmap, a.w, 0, a.N, a.d, a.w_ld, kRowsM, F8)) &&
-        encode_rows(&p.xmap, terms ? (const void*)a.xs : a.x, TERMS, a.T, a.d, terms ? a.d : a.x_ld, TP, F8) &&
-        (!low || encode_rows(&p.bmap, a.lb, 0, (long long)a.na * a.N, a.r, a.r, kRowsM, false));
+    const bool terms = TERMS == 3;       // fp32 x comes as its terms
+    const bool maps = encode_rows(&p.wmap, a.w, 0, a.N, a.d, a.w_ld, kRowsM, F8) &&
+                      encode_rows(&p.xmap, terms ? (const void*)a.xs : a.x, TERMS, a.T, a.d, terms ? a.d : a.x_ld, TP, F8) &&
+                      (!low || encode_rows(&p.bmap, a.lb, 0, (long long)a.na * a.N, a.r, a.r, kRowsM, false));
     if (!maps) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * p.split));
@@ -725,14 +778,14 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <bool F8, int TERMS, bool SHRINK>
+template <bool F8, int TERMS>
 cudaError_t launch_tp(const LoraArgs& a, cudaStream_t s) {
     ProjArgs p = {};
     p.l = a;
-    if (a.T <= 16) return launch_project<16, F8, TERMS, SHRINK>(p, s);
-    if (a.T <= 32) return launch_project<32, F8, TERMS, SHRINK>(p, s);
-    if (a.T <= 64) return launch_project<64, F8, TERMS, SHRINK>(p, s);
-    return launch_project<128, F8, TERMS, SHRINK>(p, s);
+    if (a.T <= 16) return launch_project<16, F8, TERMS>(p, s);
+    if (a.T <= 32) return launch_project<32, F8, TERMS>(p, s);
+    if (a.T <= 64) return launch_project<64, F8, TERMS>(p, s);
+    return launch_project<128, F8, TERMS>(p, s);
 }
 
 }  // namespace
@@ -747,24 +800,24 @@ size_t lora_workspace_bytes(int T, int d, int r, size_t* v_off, size_t* xs_off) 
 
 cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s) {
     const bool f32 = a.x_dt == MOE_DTYPE_F32, f8 = a.x_dt == MOE_DTYPE_FP8_E4M3;
-    // v = A_a x: many rows on the tensor cores, which read each adapter once for all its
-    // tokens; a few are done sooner by one small kernel, together with the terms of x.
     const bool gemv = lora_gemv_fits(a);
     if (gemv && (a.r == 0 || lora_gemv_own_v(a))) return launch_lora_gemv(a, s);
-    const bool tc = !gemv && a.T * a.r >= kShrinkTc;
-    const int split_blocks = (f32 && !gemv) || (f8 && tc)
-                                 ? std::min(4 * device_sm_count(), (a.T * (a.d / 8) + kShrinkThreads - 1) / kShrinkThreads) : 0;
-    const bool few = a.T * a.r / 8 < 4 * device_sm_count();    // 2 rows of A per block: more SMs share the reading
-    const int shrink_blocks = tc ? 0 : a.T * (a.r / (few ? 2 : 8));
-    cudaError_t e = cudaSuccess;
-    if (shrink_blocks + split_blocks > 0)
-        e = launch_pdl(few ? lora_shrink_kernel<2> : lora_shrink_kernel<8>, dim3((unsigned)(shrink_blocks + split_blocks)),
-                       dim3(kShrinkThreads), 0, s, a, shrink_blocks);
-    if (e == cudaSuccess && tc) e = f32 ? launch_tp<false, 3, true>(a, s) : launch_tp<false, 1, true>(a, s);
-    if (e != cudaSuccess) return e;
+    // v = A_a x and the terms of fp32 x, in one small kernel ahead of the projection
+    const int rows = a.T * a.r >= kShrinkMany ? 2 : 1;
+    const int shrink_blocks = (a.T * a.r / rows + kShrinkThreads / 32 - 1) / (kShrinkThreads / 32);
+    const int split_blocks =
+        f32 && !gemv ? std::min(4 * device_sm_count(), (a.T * (a.d / 8) + kShrinkThreads - 1) / kShrinkThreads) : 0;
+    if (shrink_blocks + split_blocks > 0) {
+        auto kern = f32 ? (rows == 2 ? lora_shrink_kernel<MOE_DTYPE_F32, 2> : lora_shrink_kernel<MOE_DTYPE_F32, 1>)
+                    : f8 ? (rows == 2 ? lora_shrink_kernel<MOE_DTYPE_FP8_E4M3, 2> : lora_shrink_kernel<MOE_DTYPE_FP8_E4M3, 1>)
+                         : (rows == 2 ? lora_shrink_kernel<MOE_DTYPE_BF16, 2> : lora_shrink_kernel<MOE_DTYPE_BF16, 1>);
+        const cudaError_t e = launch_pdl(kern, dim3((unsigned)(shrink_blocks + split_blocks)), dim3(kShrinkThreads), 0, s, a,
+                                         shrink_blocks);
+        if (e != cudaSuccess) return e;
+    }
     if (gemv) return launch_lora_gemv(a, s);
-    if (f8) return launch_tp<true, 1, false>(a, s);
-    return f32 ? launch_tp<false, 3, false>(a, s) : launch_tp<false, 1, false>(a, s);
+    if (f8) return launch_tp<true, 1>(a, s);
+    return f32 ? launch_tp<false, 3>(a, s) : launch_tp<false, 1>(a, s);
 }
 
 }  // namespace moe
