@@ -82,7 +82,8 @@ struct LoraArgs {
     long long x_ld, w_ld, y_ld;
     int x_dt, y_dt, T, d, N, na, r;
     int32_t* status;
-    float* v;                  // [T, r]: A_a x[t], unscaled
+    float* v;                  // [T, r]: A_a x[t], unscaled ...
+    __nv_bfloat16* vt;         // ... or [3, T, r]: the bf16 terms of A_a x[t] times the adapter's scale
     __nv_bfloat16* xs;         // [3, T, d]: bf16 terms of fp32 x
 };
 constexpr int kLoraMaxT = 128;

@@ -219,6 +219,7 @@ int moe_lora_project(const void* x, int x_dtype, int64_t x_ld, const float* x_sc
     a.x_dt = x_dtype; a.y_dt = y_dtype; a.T = T; a.d = d; a.N = N; a.na = n_adapters; a.r = r;
     a.status = static_cast<int32_t*>(ws);
     a.v = reinterpret_cast<float*>(static_cast<char*>(ws) + v_off);
+    a.vt = nullptr;
     a.xs = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(ws) + xs_off);
     return launched(moe::launch_lora_project(a, as_stream(stream)), who);
 }

@@ -51,6 +51,16 @@ constexpr int kProjSmem = 226 * 1024;
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkMany = 2048;           // rows of A in all from which a warp takes two
 
+// f as three bf16 terms (an infinite or NaN first term stands alone).
+__device__ __forceinline__ void split3(float f, __nv_bfloat16 (&t)[3]) {
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        t[p] = __float2bfloat16_rn(f);
+        const float b = __bfloat162float(t[p]);
+        f = fabsf(b) <= 3.4028234e38f ? f - b : 0.0f;
+    }
+}
+
 // 8 elements of x as loaded.
 template <int DT>
 struct XRaw {
@@ -93,8 +103,9 @@ template <int DT, int ROWS>
 __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __grid_constant__ LoraArgs a, int shrink_blocks) {
     constexpr int kSteps = DT == MOE_DTYPE_F32 ? 4 : 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunks = a.d / 8;
-    pdl_allow_dependents();
+    // in this order: what the kernel before wrote is there when the projection kernel starts
     pdl_wait_primary();
+    pdl_allow_dependents();
     if ((int)blockIdx.x >= shrink_blocks) {
         const long long plane = (long long)a.T * a.d;
         for (int i = (blockIdx.x - shrink_blocks) * kShrinkThreads + tid; i < a.T * chunks;
@@ -162,8 +173,19 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __
     for (int j = 0; j < ROWS; ++j) {
         const float2 p = make_float2((sum[j][0].x + sum[j][1].x) + (sum[j][2].x + sum[j][3].x),
                                      (sum[j][0].y + sum[j][1].y) + (sum[j][2].y + sum[j][3].y));
-        const float s = warp_sum(p.x + p.y);
-        if (lane == 0) a.v[t * a.r + j0 + j] = a.x_scale ? s * a.x_scale[t] : s;
+        float f = warp_sum(p.x + p.y);
+        if (lane == 0) {
+            if (a.x_scale) f *= a.x_scale[t];
+            const int i = t * a.r + j0 + j;
+            if (a.vt) {
+                __nv_bfloat16 v[3];
+                split3(f * a.ls[ad], v);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) a.vt[(long long)k * a.T * a.r + i] = v[k];
+            } else {
+                a.v[i] = f;
+            }
+        }
     }
 }
 
@@ -220,7 +242,6 @@ struct ProjShared {
     int seg[kLoraMaxT + 1];    // first sorted token of each adapter among the own tokens
     int segs;
     int starts[kLoraMaxT / 32];
-    float scale[kLoraMaxT];    // adapters' scales, by sorted token
 };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -228,16 +249,6 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
-}
-
-// f as three bf16 terms (an infinite or NaN first term stands alone).
-__device__ __forceinline__ void split3(float f, __nv_bfloat16 (&t)[3]) {
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-        t[p] = __float2bfloat16_rn(f);
-        const float b = __bfloat162float(t[p]);
-        f = fabsf(b) <= 3.4028234e38f ? f - b : 0.0f;
-    }
 }
 
 // Tiles of B_a (128 rows): ranks of whole k16 steps up to 48 come as one bulk copy of rows as they
@@ -329,7 +340,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     if (warp == 0 && lane == 0)
         for (int i = 0; i < early; ++i) load_w(i);
 
-    pdl_wait_primary();
+    // With adapters the kernel before is the one above, which had seen the end of its own predecessor
+    // before this one started: only what it writes itself is waited for, where it is read.
+    if (a.r == 0) pdl_wait_primary();
 
     // ---- order of the tokens: by the warps that need it first (the adapters' copies and
     // products), the others go ahead
@@ -337,11 +350,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     const int sid = warp == 2 ? 128 + lane : tid - 128;
     auto sort_sync = [&] { named_bar_sync(1, 160); };
     if (a.r > 0 && sorter) {
-        float scale = 0.0f;
         if (sid < kLoraMaxT) {
             const int k = sid < a.T ? adapter_of(a, sid) : INT_MAX;
             sm.key[sid] = k;
-            if (sid < a.T && k >= 0) scale = a.ls[k];
         }
         sort_sync();
         if (sid < a.T) {
@@ -355,7 +366,6 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             }
             sm.order[pos] = sid;
             sm.skey[pos] = k;
-            sm.scale[pos] = scale;
         }
         sort_sync();
         // an own token whose adapter differs from the one before starts an adapter in use
@@ -376,32 +386,17 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         }
         sort_sync();
         if (warp != 2) {
-            const int vstr = v_stride(a.r), own = p1 - p0;
-            // two elements of a token's v at a time, the loads of kAhead of them together
-            constexpr int kAhead = 6;
-            const int pairs = vstr / 2, n = own * pairs;
-            for (int i0 = sid; i0 < n; i0 += kAhead * 128) {
-                float2 v[kAhead];
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int i = i0 + u * 128, q = i / pairs, j = (i - q * pairs) * 2;
-                    v[u] = make_float2(0.0f, 0.0f);
-                    if (i < n && j < a.r && sm.skey[p0 + q] >= 0)
-                        v[u] = *reinterpret_cast<const float2*>(a.v + sm.order[p0 + q] * a.r + j);
-                }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int i = i0 + u * 128, q = i / pairs, j = (i - q * pairs) * 2;
-                    if (i >= n) break;
-                    const float f = sm.scale[p0 + q];
-                    __nv_bfloat16 t0[3], t1[3];
-                    split3(v[u].x * f, t0);
-                    split3(v[u].y * f, t1);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        *reinterpret_cast<__nv_bfloat162*>(vs + (k * own + q) * vstr + j) = __halves2bfloat162(t0[k], t1[k]);
-                }
+            pdl_wait_primary();
+            // the terms of the own tokens' v, in 16-byte pieces, zeros beyond the rank
+            const int vstr = v_stride(a.r), own = p1 - p0, pieces = vstr / 8 - 1;
+            for (int i = sid; i < 3 * own * pieces; i += 128) {
+                const int row = i / pieces, c = (i - row * pieces) * 8, k = row / own, q = row - k * own;
+                __nv_bfloat16* dst = vs + row * vstr + c;
+                if (c >= a.r) *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                else if (sm.skey[p0 + q] >= 0) cp_async16(dst, a.vt + ((long long)k * a.T + sm.order[p0 + q]) * a.r + c);
             }
+            cp_async_commit();
+            cp_async_wait<0>();
             named_bar_sync(2, 128);
         }
     } else if (a.r == 0) {
@@ -418,6 +413,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                 for (int t = 0; t < TERMS; ++t)
                     tma_load_3d_plain(dst + t * kXBytes, &p.xmap, (kb0 + i) * kColsPerBlock, 0, t, &sm.full[slot]);
             };
+            if (TERMS > 1 && a.r > 0) pdl_wait_primary();     // the terms of x
             for (int i = 0; i < early; ++i) load_x(i);
             int i = early;
             for (; i < nkb; ++i) {
@@ -793,15 +789,17 @@ cudaError_t launch_tp(const LoraArgs& a, cudaStream_t s) {
 size_t lora_workspace_bytes(int T, int d, int r, size_t* v_off, size_t* xs_off) {
     size_t off = 512;
     *v_off = off;
-    off += ((size_t)T * r * 4 + 255) / 256 * 256;
+    off += ((size_t)T * r * 6 + 255) / 256 * 256;
     *xs_off = off;
     return off + (size_t)T * d * 6;
 }
 
-cudaError_t launch_lora_project(const LoraArgs& a, cudaStream_t s) {
+cudaError_t launch_lora_project(const LoraArgs& args, cudaStream_t s) {
+    LoraArgs a = args;
     const bool f32 = a.x_dt == MOE_DTYPE_F32, f8 = a.x_dt == MOE_DTYPE_FP8_E4M3;
     const bool gemv = lora_gemv_fits(a);
     if (gemv && (a.r == 0 || lora_gemv_own_v(a))) return launch_lora_gemv(a, s);
+    if (!gemv) a.vt = reinterpret_cast<__nv_bfloat16*>(a.v);
     // v = A_a x and the terms of fp32 x, in one small kernel ahead of the projection
     const int rows = a.T * a.r >= kShrinkMany ? 2 : 1;
     const int shrink_blocks = (a.T * a.r / rows + kShrinkThreads / 32 - 1) / (kShrinkThreads / 32);
