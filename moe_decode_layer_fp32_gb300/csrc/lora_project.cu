@@ -15,17 +15,19 @@
 // accumulators.  fp32 activations are three bf16 terms (24 bits); the two small ones
 // have accumulators of their own.
 //
-// Adapters.  v[t] = A_a x[t] is taken before, while W is fetched already: by a small kernel, or
-// for many rows by this one with the rows of A in the place of W.  The tokens are sorted by
-// adapter; the 128 rows of B_a come once for all tokens of the adapter, and a warp
-// multiplies them with v (three bf16 terms) beside the MMAs.  A token meets no
-// weights but its own adapter's, whatever the others hold.
+// Adapters.  v[t] = A_a x[t] is taken before, by a kernel of its own that streams the rows of A
+// and writes v times the adapter's scale as three bf16 terms; meanwhile this one sorts the
+// tokens by adapter and fetches W and B.  128 rows of B_a come once for all tokens of the
+// adapter, and four warps multiply 32 of them each with v beside the MMAs of W: all
+// four on one tile, so that its place in the ring is free again sooner (an adapter to
+// a warp took 337 us where this takes 170: 128 tokens, 128 adapters of rank 128).  A
+// token meets no weights but its own adapter's, whatever the others hold.
 //
 // Measured (without adapters): 16 to 32 tokens of 7168 -> 9216, bf16 (132 MB) 26.7 us, 128
 // tokens 29 us; 128 tokens of 7168 -> 7168 E4M3 (51 MB) 18 us.  The stream of W alone takes
 // 22 us of the first (6.65 TB/s): the four MMAs of a block, about 0.09 us each however few
 // the tokens are, take a little longer than the block's bytes.  With 64 adapters of
-// rank 64 (58 MB each of A and B) the third takes 59 us, 25 of them A x.
+// rank 64 (58 MB each of A and B) the third takes 43 us, 14 of them A x.
 #include <algorithm>
 #include <climits>
 
@@ -48,8 +50,11 @@ constexpr int kProjSmem = 226 * 1024;
 
 // ---- v = A_a x, and the bf16 terms of fp32 activations -----------------------
 
-constexpr int kShrinkThreads = 256;
-constexpr int kShrinkMany = 2048;           // rows of A in all from which a warp takes two
+constexpr int kShrinkThreads = 128;
+// Tokens times rank from which a warp takes two rows by itself.  Whole projections, this way and
+// the other: 2048 rows, d 7168, 8 adapters 28.7 and 32.9 us, 32 adapters 45.4 and 42.1; d 2048, fp32 13.4
+// and 15.5; 512 rows 28.5 and 28.8; 128 rows, d 2048 7.2 and 6.4.
+constexpr int kShrinkMany = 1024;
 
 // f as three bf16 terms (an infinite or NaN first term stands alone).
 __device__ __forceinline__ void split3(float f, __nv_bfloat16 (&t)[3]) {
@@ -95,12 +100,13 @@ struct XRaw {
     }
 };
 
-// Blocks [0, shrink_blocks): a warp takes ROWS rows of A_a against x[t], with the loads of
-// several steps along d together and no barrier: HBM (L2 for adapters that several tokens
-// share) bounds it, and it runs beside the projection kernel's first copies of W.  The
-// blocks after them write the three bf16 terms of fp32 x.
-template <int DT, int ROWS>
-__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __grid_constant__ LoraArgs a, int shrink_blocks) {
+// Blocks [0, shrink_blocks): A_a x[t], two rows of A_a to a warp (MANY), or one to the
+// block's four, with the loads of several steps along d together: HBM (L2 for adapters that
+// several tokens share) bounds it.  The blocks after them write the three bf16 terms of
+// fp32 x.  Blocks of 128 threads leave room for one of the projection kernel's beside them.
+template <int DT, bool MANY>
+__global__ void __launch_bounds__(kShrinkThreads, 4) lora_shrink_kernel(const __grid_constant__ LoraArgs a, int shrink_blocks) {
+    constexpr int ROWS = MANY ? 2 : 1, kWarps = kShrinkThreads / 32, kSplit = MANY ? 1 : kWarps;
     constexpr int kSteps = DT == MOE_DTYPE_F32 ? 4 : 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunks = a.d / 8;
     // in this order: what the kernel before wrote is there when the projection kernel starts
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __
         }
         return;
     }
-    const int unit = blockIdx.x * (kShrinkThreads / 32) + warp;
+    const int unit = MANY ? blockIdx.x * kWarps + warp : blockIdx.x;
     if (unit >= a.T * a.r / ROWS) return;
     const int t = unit / (a.r / ROWS), j0 = (unit - t * (a.r / ROWS)) * ROWS;
     const int ad = adapter_of(a, t);
@@ -142,12 +148,12 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __
     for (int j = 0; j < ROWS; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[j][e] = make_float2(0.0f, 0.0f);
-    for (int c0 = lane; c0 < chunks; c0 += 32 * kSteps) {
+    for (int c0 = MANY ? lane : tid; c0 < chunks; c0 += 32 * kSplit * kSteps) {
         uint4 w[kSteps][ROWS];
         XRaw<DT> x[kSteps];
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            const int c = c0 + 32 * k;
+            const int c = c0 + 32 * kSplit * k;
             if (c < chunks) {
 #pragma unroll
                 for (int j = 0; j < ROWS; ++j) w[k][j] = __ldg(rows + (long long)j * chunks + c);
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __
         }
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            if (c0 + 32 * k < chunks) {
+            if (c0 + 32 * kSplit * k < chunks) {
                 float2 v[4];
                 x[k].get(v);
 #pragma unroll
@@ -174,7 +180,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __
         const float2 p = make_float2((sum[j][0].x + sum[j][1].x) + (sum[j][2].x + sum[j][3].x),
                                      (sum[j][0].y + sum[j][1].y) + (sum[j][2].y + sum[j][3].y));
         float f = warp_sum(p.x + p.y);
-        if (lane == 0) {
+        if constexpr (!MANY) {
+            __shared__ float s_part[kWarps];
+            if (lane == 0) s_part[warp] = f;
+            __syncthreads();
+            f = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
+        }
+        if (MANY ? lane == 0 : tid == 0) {
             if (a.x_scale) f *= a.x_scale[t];
             const int i = t * a.r + j0 + j;
             if (a.vt) {
@@ -801,14 +813,14 @@ cudaError_t launch_lora_project(const LoraArgs& args, cudaStream_t s) {
     if (gemv && (a.r == 0 || lora_gemv_own_v(a))) return launch_lora_gemv(a, s);
     if (!gemv) a.vt = reinterpret_cast<__nv_bfloat16*>(a.v);
     // v = A_a x and the terms of fp32 x, in one small kernel ahead of the projection
-    const int rows = a.T * a.r >= kShrinkMany ? 2 : 1;
-    const int shrink_blocks = (a.T * a.r / rows + kShrinkThreads / 32 - 1) / (kShrinkThreads / 32);
+    const bool many = a.T * a.r >= kShrinkMany;
+    const int shrink_blocks = many ? (a.T * a.r + kShrinkThreads / 16 - 1) / (kShrinkThreads / 16) : a.T * a.r;
     const int split_blocks =
         f32 && !gemv ? std::min(4 * device_sm_count(), (a.T * (a.d / 8) + kShrinkThreads - 1) / kShrinkThreads) : 0;
     if (shrink_blocks + split_blocks > 0) {
-        auto kern = f32 ? (rows == 2 ? lora_shrink_kernel<MOE_DTYPE_F32, 2> : lora_shrink_kernel<MOE_DTYPE_F32, 1>)
-                    : f8 ? (rows == 2 ? lora_shrink_kernel<MOE_DTYPE_FP8_E4M3, 2> : lora_shrink_kernel<MOE_DTYPE_FP8_E4M3, 1>)
-                         : (rows == 2 ? lora_shrink_kernel<MOE_DTYPE_BF16, 2> : lora_shrink_kernel<MOE_DTYPE_BF16, 1>);
+        auto kern = f32  ? (many ? lora_shrink_kernel<MOE_DTYPE_F32, true> : lora_shrink_kernel<MOE_DTYPE_F32, false>)
+                    : f8 ? (many ? lora_shrink_kernel<MOE_DTYPE_FP8_E4M3, true> : lora_shrink_kernel<MOE_DTYPE_FP8_E4M3, false>)
+                         : (many ? lora_shrink_kernel<MOE_DTYPE_BF16, true> : lora_shrink_kernel<MOE_DTYPE_BF16, false>);
         const cudaError_t e = launch_pdl(kern, dim3((unsigned)(shrink_blocks + split_blocks)), dim3(kShrinkThreads), 0, s, a,
                                          shrink_blocks);
         if (e != cudaSuccess) return e;
