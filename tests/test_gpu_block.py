@@ -124,6 +124,12 @@ def test_norm_many_rows(B, T, d):
     run_norm(B, T, d, x="f32", y="e4m3", seed=T)
 
 
+@pytest.mark.parametrize("T,d", [(400, 8200), (311, 12288), (170, 16384)])
+def test_norm_many_wide_rows(B, T, d):
+    run_norm(B, T, d, res="f32", seed=d)
+    run_norm(B, T, d, x="bf16", res="bf16", y="bf16", seed=d)
+
+
 def test_norm_strides_and_in_place(B):
     run_norm(B, 9, 520, res="f32", y="bf16", pad=24, seed=3)
     run_norm(B, 9, 512, res="f32", y="f32", inplace=True, seed=4)
