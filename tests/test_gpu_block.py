@@ -243,6 +243,40 @@ def test_append(B, D, rot, x, dtype, heads_first):
         assert torch.equal(raw(c).cpu()[~touched], b.cpu()[~touched])
 
 
+@pytest.mark.parametrize("T,hq,hkv,D,rot,x", [(2600, 8, 2, 64, 32, "bf16"), (1500, 40, 20, 256, 256, "f32"),
+                                              (3001, 0, 1, 16, 16, "f32"), (2100, 9, 3, 80, 80, "bf16"), (700, 9, 3, 80, 40, "f32")])
+def test_append_many_tokens(B, T, hq, hkv, D, rot, x):
+    """Blocks that take several tokens, or slices of their heads, with padding and tokens dropped in between."""
+    R, page, g = 7, 16, gen(T)
+    per = (T + R - 1) // R
+    cols = (per + page - 1) // page
+    k, v, _, _, cache = make_cache(B, g, R * cols, page, hkv, D, "bf16", fill=0)
+    qkv = normal(g, T, hq + 2 * hkv, D, dtype=DT[x])
+    q, kn, vn = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    table = torch.randperm(R * cols, generator=g, device="cuda").to(torch.int32).view(R, cols)
+    i = torch.arange(T, dtype=torch.int32, device="cuda")
+    req, pos = i % R, i // R
+    pos[5::11] = -1                                   # padding
+    req[7::301] = R                                   # no such request
+    qo = torch.empty(T, hq, D, dtype=DT[x], device="cuda")
+    cs = cos_sin_table(per, rot)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.moe_kv_append(kn, vn, cache, table, pos, req=req, cos_sin=cs, q=q if hq else None, q_out=qo if hq else None, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == -6
+    mag = O.f64(qkv).abs().max().item() * 2
+    if hq:
+        qr = O.rotate(q, pos, cs)
+        assert_within(qo, qr, 4 * U * mag + (BF if x == "bf16" else 0.0) * qr.abs() * 1.01, "q")
+    kept = ((pos >= 0) & (req < R)).cpu()
+    t = torch.nonzero(kept).flatten()
+    at = table.cpu().long()[req.cpu()[t].long(), pos.cpu()[t].long() // page], pos.cpu()[t].long() % page
+    for name, c, want in (("k", k, O.rotate(kn, pos, cs)), ("v", v, O.f64(vn))):
+        full = torch.zeros(c.shape, dtype=torch.float64)
+        full[at] = want.cpu()[t]
+        assert_within(c, full, BF * full.abs() * 1.01 + 4 * U * mag * (full != 0), name)
+
+
 def test_append_default_requests_in_place_and_without_q(B):
     g = gen(1)
     k, v, _, _, cache = make_cache(B, g, 9, 4, 2, 64, "bf16")
