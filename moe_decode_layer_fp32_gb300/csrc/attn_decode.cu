@@ -22,10 +22,11 @@
 // more at no cost in MMAs; bf16 queries over an E4M3 cache as two E4M3 terms.
 //
 // Measured: 1 x 131071 keys of 8 heads of 128, bf16 (537 MB) 89 us, 6.0 TB/s; 128
-// requests of 1 to 4096 keys, bf16 140 us, 6.2 TB/s, and E4M3 105 us, 4.2 TB/s: there the
-// instructions bound it, about 850 for a warp's 32 keys, which two warps and three per
-// scheduler issue at the same 0.5 a clock.  Two CTAs per SM with a ring of three stages
-// beat three with two (91 and 98 us for 64 x 2048 keys in bf16).
+// requests of 1 to 4096 keys, bf16 140 us, 6.2 TB/s, and E4M3 93 us, 4.7 TB/s: there the
+// instructions bound it, about 750 for a warp's 32 keys at 0.35 a clock and scheduler (105 us with
+// a mask or shift more per conversion).  Two CTAs per SM with a ring of three stages beat
+// three with two (64 x 2048 keys: bf16 91 and 98 us, E4M3 58 and 66) and tiles of 16 keys
+// (E4M3 69).
 #include <algorithm>
 
 #include <math_constants.h>
@@ -77,10 +78,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -354,7 +351,7 @@ struct Attn {
                         for (int h = 0; h < 2; ++h) {
                             float* u = &f[s / 2][(s % 2) * 8 + h * 4];
                             const uint32_t w = pack_e4m3x4(u[0], u[1], u[2], u[3]);
-                            const float2 lo = unpack_e4m3x2(w), hi = unpack_e4m3x2(w >> 16);
+                            const float2 lo = unpack_e4m3x2<false>(w), hi = unpack_e4m3x2<true>(w);
                             u[0] = (u[0] - lo.x) * 16.0f;
                             u[1] = (u[1] - lo.y) * 16.0f;
                             u[2] = (u[2] - hi.x) * 16.0f;
@@ -430,8 +427,8 @@ struct Attn {
                     const int step = j * SJ + i;
                     uint32_t b0, b1;
                     if constexpr (F8) {
-                        b0 = e4m3x2_to_f16x2(w[i]);
-                        b1 = e4m3x2_to_f16x2(w[i] >> 16);
+                        b0 = e4m3x2_to_f16x2<false>(w[i]);
+                        b1 = e4m3x2_to_f16x2<true>(w[i]);
                     } else {
                         b0 = w[2 * i];
                         b1 = w[2 * i + 1];
@@ -566,7 +563,7 @@ struct Attn {
                     for (int h = 0; h < 2; ++h) {
                         if constexpr (F8) {
                             const uint32_t x = __byte_perm(v[2 * h][e / 4], v[2 * h + 1][e / 4], (e & 2) ? 0x7362 : 0x5140);
-                            b[h] = e4m3x2_to_f16x2((e & 1) ? x >> 16 : x);
+                            b[h] = (e & 1) ? e4m3x2_to_f16x2<true>(x) : e4m3x2_to_f16x2<false>(x);
                         } else {
                             b[h] = __byte_perm(v[2 * h][e / 2], v[2 * h + 1][e / 2], (e & 1) ? 0x7632 : 0x5410);
                         }

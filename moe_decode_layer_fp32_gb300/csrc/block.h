@@ -175,14 +175,27 @@ __device__ __forceinline__ void store8(void* p, int dt, long long i, const float
         q[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
-// Values outside E4M3's range go to +-448.
+// Values outside E4M3's range go to +-448.  (The halves of a word by name rather than by shifts and
+// masks: the conversions take either half of a register.)
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
 }
+// The two E4M3 of v's lower (HI: upper) half in f16, and in fp32.
+template <bool HI>
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+    uint32_t r;
+    if constexpr (HI) asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
+    else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(v));
+    return r;
+}
+template <bool HI>
 __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
+    const uint32_t h = e4m3x2_to_f16x2<HI>(v);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
@@ -190,10 +203,10 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
 __device__ __forceinline__ void load8_any(const void* p, int dt, long long i, float (&f)[8]) {
     if (dt == MOE_DTYPE_FP8_E4M3) {
         const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i);
-        const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float2 u = unpack_e4m3x2(w[e]);
+            const uint32_t w = e < 2 ? v.x : v.y;
+            const float2 u = e % 2 ? unpack_e4m3x2<true>(w) : unpack_e4m3x2<false>(w);
             f[2 * e] = u.x;
             f[2 * e + 1] = u.y;
         }

@@ -34,10 +34,10 @@ struct WRaw {
     }
     __device__ __forceinline__ void get(float2 (&f)[4]) const {
         if constexpr (F8) {
-            f[0] = unpack_e4m3x2(w.x);
-            f[1] = unpack_e4m3x2(w.x >> 16);
-            f[2] = unpack_e4m3x2(w.y);
-            f[3] = unpack_e4m3x2(w.y >> 16);
+            f[0] = unpack_e4m3x2<false>(w.x);
+            f[1] = unpack_e4m3x2<true>(w.x);
+            f[2] = unpack_e4m3x2<false>(w.y);
+            f[3] = unpack_e4m3x2<true>(w.y);
         } else {
             unpack_bf16x8_f2(w, f);
         }

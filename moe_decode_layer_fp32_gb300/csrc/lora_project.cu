@@ -92,10 +92,10 @@ struct XRaw {
         } else if constexpr (DT == MOE_DTYPE_BF16) {
             unpack_bf16x8_f2(w[0], f);
         } else {
-            f[0] = unpack_e4m3x2(w[0].x);
-            f[1] = unpack_e4m3x2(w[0].x >> 16);
-            f[2] = unpack_e4m3x2(w[0].y);
-            f[3] = unpack_e4m3x2(w[0].y >> 16);
+            f[0] = unpack_e4m3x2<false>(w[0].x);
+            f[1] = unpack_e4m3x2<true>(w[0].x);
+            f[2] = unpack_e4m3x2<false>(w[0].y);
+            f[3] = unpack_e4m3x2<true>(w[0].y);
         }
     }
 };
