@@ -344,13 +344,12 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     const uint64_t pol = l2_policy_evict_first();
     constexpr int kColsPerBlock = F8 ? 128 : 64;
     const int early = min(nkb, p.stages);
-    auto load_w = [&](int i) {
-        const int slot = i % p.stages;
+    auto load_w = [&](int i, int slot) {
         mbar_arrive_expect_tx(&sm.full[slot], kStageBytes);
         tma_load_2d(ring + slot * kStageBytes, &p.wmap, (kb0 + i) * kColsPerBlock, n0, &sm.full[slot], pol);
     };
     if (warp == 0 && lane == 0)
-        for (int i = 0; i < early; ++i) load_w(i);
+        for (int i = 0; i < early; ++i) load_w(i, i);
 
     // With adapters the kernel before is the one above, which had seen the end of its own predecessor
     // before this one started: only what it writes itself is waited for, where it is read.
@@ -418,20 +417,24 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     if (warp == 0) {
         // ===================== TMA producer =====================
         if (lane == 0) {
-            auto load_x = [&](int i) {
-                const int slot = i % p.stages;
+            auto load_x = [&](int i, int slot) {
                 unsigned char* dst = ring + slot * kStageBytes + kWBytes;
 #pragma unroll
                 for (int t = 0; t < TERMS; ++t)
                     tma_load_3d_plain(dst + t * kXBytes, &p.xmap, (kb0 + i) * kColsPerBlock, 0, t, &sm.full[slot]);
             };
             if (TERMS > 1 && a.r > 0) pdl_wait_primary();     // the terms of x
-            for (int i = 0; i < early; ++i) load_x(i);
-            int i = early;
+            for (int i = 0; i < early; ++i) load_x(i, i);
+            int i = early, slot = 0;        // the ring is full: from its first place on
+            uint32_t phase = 0;
             for (; i < nkb; ++i) {
-                if (!wait(&sm.empty[i % p.stages], ((i / p.stages) & 1u) ^ 1u)) break;
-                load_w(i);
-                load_x(i);
+                if (!wait(&sm.empty[slot], phase)) break;
+                load_w(i, slot);
+                load_x(i, slot);
+                if (++slot == p.stages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
             // every copy has landed before the CTA may exit
             for (int j = max(0, i - p.stages); j < i; ++j) mbar_wait_bounded(&sm.full[j % p.stages], (j / p.stages) & 1u);
@@ -442,14 +445,15 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             const uint64_t a0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
             const uint64_t b0 = smem_desc_sw128(smem_u32(ring + kWBytes), 16, 1024);
             const uint32_t idesc = F8 ? idesc_e4m3_f32(128, TP) : idesc_bf16_f32(128, TP, false, false);
+            int slot = 0;
+            uint32_t phase = 0;
             for (int c = 0; ok && c < chunks; ++c) {
                 const uint32_t buf = c & 1;
                 if (!wait(&sm.acc_empty[buf], ((c >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after_sync();
                 const int end = min(nkb, (c + 1) * kChunkBlocks);
                 for (int i = c * kChunkBlocks; i < end; ++i) {
-                    const int slot = i % p.stages;
-                    if (!wait(&sm.full[slot], (i / p.stages) & 1u)) break;
+                    if (!wait(&sm.full[slot], phase)) break;
                     tc_fence_after_sync();
                     const uint64_t ad = a0 + ((slot * kStageBytes) >> 4), bd = b0 + ((slot * kStageBytes) >> 4);
                     const bool fresh = i == c * kChunkBlocks;
@@ -463,6 +467,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                             else umma_bf16(col, ad + ks * 2, bd + ((t * kXBytes) >> 4) + ks * 2, idesc, acc);
                         }
                     umma_commit(&sm.empty[slot]);
+                    if (++slot == p.stages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
                 if (!ok) break;
                 umma_commit(&sm.acc_full[buf]);
