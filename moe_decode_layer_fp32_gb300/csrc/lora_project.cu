@@ -23,11 +23,11 @@
 // a warp took 337 us where this takes 170: 128 tokens, 128 adapters of rank 128).  A
 // token meets no weights but its own adapter's, whatever the others hold.
 //
-// Measured (without adapters): 16 to 32 tokens of 7168 -> 9216, bf16 (132 MB) 26.7 us, 128
-// tokens 29 us; 128 tokens of 7168 -> 7168 E4M3 (51 MB) 18 us.  The stream of W alone takes
-// 22 us of the first (6.65 TB/s): the four MMAs of a block, about 0.09 us each however few
-// the tokens are, take a little longer than the block's bytes.  With 64 adapters of
-// rank 64 (58 MB each of A and B) the third takes 43 us, 14 of them A x.
+// Measured (without adapters): 16 to 32 tokens of 7168 -> 9216, bf16 (132 MB) 23.7 us, 5.6 TB/s,
+// 128 tokens 26.6 us; 128 tokens of 7168 -> 7168 E4M3 (51 MB) 16 us.  The stream of W alone takes
+// 22 us of the first; what the issuing warp does for a 128-byte block between two waits bounds the
+// rest (with a division for the place in the ring, and one lane instead of a uniform warp, 26.7 us).
+// With 64 adapters of rank 64 (58 MB each of A and B) the third takes 42 us, 14 of them A x.
 #include <algorithm>
 #include <climits>
 
@@ -242,6 +242,12 @@ __device__ __forceinline__ float4 ld_cluster4(const void* p, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 struct ProjShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
@@ -440,23 +446,28 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
             for (int j = max(0, i - p.stages); j < i; ++j) mbar_wait_bounded(&sm.full[j % p.stages], (j / p.stages) & 1u);
         }
     } else if (warp == 1) {
-        // ===================== MMA issuer =====================
-        if (lane == 0) {
-            const uint64_t a0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
-            const uint64_t b0 = smem_desc_sw128(smem_u32(ring + kWBytes), 16, 1024);
-            const uint32_t idesc = F8 ? idesc_e4m3_f32(128, TP) : idesc_bf16_f32(128, TP, false, false);
-            int slot = 0;
-            uint32_t phase = 0;
-            for (int c = 0; ok && c < chunks; ++c) {
-                const uint32_t buf = c & 1;
-                if (!wait(&sm.acc_empty[buf], ((c >> 1) & 1u) ^ 1u)) break;
+        // ===================== MMA issuer (the whole warp, so that what the MMAs take is uniform) =====================
+        const uint64_t a0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
+        const uint64_t b0 = smem_desc_sw128(smem_u32(ring + kWBytes), 16, 1024);
+        const uint32_t idesc = F8 ? idesc_e4m3_f32(128, TP) : idesc_bf16_f32(128, TP, false, false);
+        auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+        int slot = 0;
+        uint32_t phase = 0;
+        bool run = true;
+        for (int c = 0; run && c < chunks; ++c) {
+            const uint32_t buf = c & 1;
+            if (!all_wait(&sm.acc_empty[buf], ((c >> 1) & 1u) ^ 1u)) break;
+            tc_fence_after_sync();
+            const int end = min(nkb, (c + 1) * kChunkBlocks);
+            for (int i = c * kChunkBlocks; i < end; ++i) {
+                if (!all_wait(&sm.full[slot], phase)) {
+                    run = false;
+                    break;
+                }
                 tc_fence_after_sync();
-                const int end = min(nkb, (c + 1) * kChunkBlocks);
-                for (int i = c * kChunkBlocks; i < end; ++i) {
-                    if (!wait(&sm.full[slot], phase)) break;
-                    tc_fence_after_sync();
-                    const uint64_t ad = a0 + ((slot * kStageBytes) >> 4), bd = b0 + ((slot * kStageBytes) >> 4);
-                    const bool fresh = i == c * kChunkBlocks;
+                const uint64_t ad = a0 + ((slot * kStageBytes) >> 4), bd = b0 + ((slot * kStageBytes) >> 4);
+                const bool fresh = i == c * kChunkBlocks;
+                if (elect_one()) {
 #pragma unroll
                     for (int t = 0; t < TERMS; ++t)
 #pragma unroll
@@ -467,14 +478,16 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                             else umma_bf16(col, ad + ks * 2, bd + ((t * kXBytes) >> 4) + ks * 2, idesc, acc);
                         }
                     umma_commit(&sm.empty[slot]);
-                    if (++slot == p.stages) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
+                    if (i + 1 == end) umma_commit(&sm.acc_full[buf]);
                 }
-                if (!ok) break;
-                umma_commit(&sm.acc_full[buf]);
+                __syncwarp();
+                if (++slot == p.stages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
+        }
+        if (elect_one()) {
             umma_commit(&sm.mma_done);
             mbar_wait_bounded(&sm.mma_done, 0);   // all MMAs have ended before TMEM is freed
         }
