@@ -20,9 +20,9 @@
  *   - Strides are in elements and may be any that keep each row's elements
  *     next to one another; `ld` is the stride between rows.
  *   - The kernels launch as programmatic dependents of the kernel before them
- *     on the stream.  Before that kernel has completed they read weights only:
- *     the norm's weight, the projection's w.  The
- *     rule of moe_decode.h on router weights holds for these too.
+ *     on the stream.  Before that kernel has completed they read the
+ *     projection's w and nothing else.  The rule of moe_decode.h on router
+ *     weights holds for it too.
  *   - Sizes count from 0 where a call says so: an empty batch is MOE_OK and
  *     launches nothing.
  */
@@ -133,6 +133,7 @@ size_t moe_attn_workspace_bytes(int B, int q_heads, int heads, int head_dim);
  * softcap 0.  A request with n <= 0 gets zeros, and a score of -inf weighs
  * nothing (a head whose scores all are -inf gets zeros too).  Slots outside that range and
  * table entries of pages wholly outside it are not read.
+ * Over an E4M3 cache a head with an infinity in a BF16 q gets NaN.
  *   q           [B, q_heads, D] F32 or BF16; out the same shape, F32 or BF16
  *   block_table int32[B, max_pages], row stride table_ld
  *   lse         float[B, q_heads] or NULL: log of the sum of exp of the scores

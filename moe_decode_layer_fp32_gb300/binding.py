@@ -1,8 +1,9 @@
-"""ctypes binding of ``libmoe_gb300.so``: argument marshalling only.
+"""Binding of ``libmoe_gb300.so``: argument marshalling only.
 
 Every function has the name of the C entry point it calls (see
 ``include/moe_decode.h`` and ``include/moe_block.h``).  Tensors are passed as device pointers, sizes are
-read from their shapes, and the stream is torch's current CUDA stream.  No
+read from their shapes, and the stream is torch's current CUDA stream.  The calls
+of the decode block's operators go through a small extension module, the others through ctypes.  No
 step of the layer runs here; a missing library raises instead of falling back.
 """
 
