@@ -703,55 +703,66 @@ struct Attn {
         combine(a, c, nsub, base, stride, sh, to);
     }
 
-    // Join `count` parts, part_at(0), part_at(1), ...: warp w takes parts w, w + 4, ... in order, then
-    // the warps are joined as above.  `to` may be one of the parts (all are read before it is written).
+    // Join `count` parts, part_at(0), part_at(1), ..., in that order: a thread has the same elements of
+    // all, with the loads of kBatch parts together (one trip to L2 for most units).  `to` may be one
+    // of the parts: its maxima and sums are written when all have read them.
     template <class PartAt>
-    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, int count, PartAt part_at, char* base, int stride,
-                                Shared& sh, float* to) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        constexpr int kAll = ROWS * (DP / 4) / 32, kItems = kAll < 8 ? kAll : 8;   // float4 of a lane, at a time
-        float4* mine = reinterpret_cast<float4*>(base + warp * stride);
-        for (int i0 = 0; i0 < kAll; i0 += kItems) {
-            float top[kItems], l[kItems];
-            float4 o[kItems];
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                top[i] = -CUDART_INF_F;
-                l[i] = 0.0f;
-                o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
+    __device__ static void join(const AttnArgs& a, const Cursor& c, int nsub, int count, PartAt part_at, Shared& sh, float* to) {
+        constexpr int kBatch = 8;
+        const int g = c.unit / nsub, sub = c.unit % nsub;
 #pragma unroll 2
-            for (int k = warp; k < count; k += kAttnWarps) {
-                const float* p = part_at(k);
-                float pm[kItems], pl[kItems];
-                float4 po[kItems];
+        for (int it = threadIdx.x; it < ROWS * (DP / 4); it += kAttnThreads) {
+            const int row = it / (DP / 4), c4 = it % (DP / 4);
+            float top = -CUDART_INF_F, l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k0 = 0; k0 < count; k0 += kBatch) {
+                float pm[kBatch], pl[kBatch];
+                float4 po[kBatch];
 #pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    const int it = lane + 32 * (i0 + i), row = it / (DP / 4);
-                    po[i] = __ldcg(reinterpret_cast<const float4*>(p) + it);
-                    pm[i] = __ldcg(p + ROWS * DP + row);
-                    pl[i] = __ldcg(p + ROWS * DP + ROWS + row);
+                for (int k = 0; k < kBatch; ++k) {
+                    pm[k] = -CUDART_INF_F;
+                    pl[k] = 0.0f;
+                    po[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (k0 + k < count) {
+                        const float* p = part_at(k0 + k);
+                        po[k] = __ldcg(reinterpret_cast<const float4*>(p) + it);
+                        pm[k] = __ldcg(p + ROWS * DP + row);
+                        pl[k] = __ldcg(p + ROWS * DP + ROWS + row);
+                    }
                 }
+                float mx = top;
 #pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    const float mx = fmaxf(top[i], pm[i]), f0 = weight_of(top[i], mx), f1 = weight_of(pm[i], mx);
-                    top[i] = mx;
-                    l[i] = fmaf(pl[i] != pl[i] ? 1.0f : f1, pl[i], l[i] * (l[i] != l[i] ? 1.0f : f0));
-                    o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
-                    axpy4(o[i], f1, po[i]);
+                for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, pm[k]);
+                const float f0 = weight_of(top, mx);
+                top = mx;
+                // a NaN sum has no maximum: it stays NaN
+                l *= l != l ? 1.0f : f0;
+                o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float f = weight_of(pm[k], top);
+                    l = fmaf(pl[k] != pl[k] ? 1.0f : f, pl[k], l);
+                    axpy4(o, f, po[k]);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int it = lane + 32 * (i0 + i), row = it / (DP / 4), c4 = it % (DP / 4);
-                mine[row * (DP / 4) + (c4 ^ (row & 7))] = o[i];
+            if (to) {
+                reinterpret_cast<float4*>(to)[it] = o;
                 if (c4 == 0) {
-                    sh.m[warp][row] = top[i];
-                    sh.l[warp][row] = l[i];
+                    sh.m[0][row] = top;
+                    sh.l[0][row] = l;
                 }
+            } else {
+                finish(a, c.b, g, sub, row, c4, o, top, l);
             }
         }
-        combine(a, c, nsub, base, stride, sh, to);
+        if (to) {
+            __syncthreads();
+            if (threadIdx.x < ROWS) {
+                to[ROWS * DP + threadIdx.x] = sh.m[0][threadIdx.x];
+                to[ROWS * DP + ROWS + threadIdx.x] = sh.l[0][threadIdx.x];
+            }
+            __syncthreads();
+        }
     }
 
     // Whether this CTA is the last of `n` to arrive at the counter (which then is zero
@@ -929,14 +940,14 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX>::kCtasPer
             auto part_at = [&](int i) { return part_of(c_first + i, i > 0 || head); };
             uint32_t* done = a.done + (long long)seg.b * units + seg.unit;
             if (n <= kJoinMost) {
-                if (K::arrive_last(done, n, sh)) K::join(a, seg, nsub, n, part_at, lay, kStride, sh, nullptr);
+                if (K::arrive_last(done, n, sh)) K::join(a, seg, nsub, n, part_at, sh, nullptr);
             } else {
                 const int me = (int)blockIdx.x - c_first, g0 = me / kJoinGroup * kJoinGroup, gn = min(kJoinGroup, n - g0);
                 if (K::arrive_last(a.group_done + 2 * (c_first + g0) + (g0 > 0 || head ? 0 : 1), gn, sh)) {
-                    K::join(a, seg, nsub, gn, [&](int i) { return part_at(g0 + i); }, lay, kStride, sh, part_at(g0));
+                    K::join(a, seg, nsub, gn, [&](int i) { return part_at(g0 + i); }, sh, part_at(g0));
                     const int groups = (n + kJoinGroup - 1) / kJoinGroup;
                     if (K::arrive_last(done, groups, sh))
-                        K::join(a, seg, nsub, groups, [&](int i) { return part_at(i * kJoinGroup); }, lay, kStride, sh, nullptr);
+                        K::join(a, seg, nsub, groups, [&](int i) { return part_at(i * kJoinGroup); }, sh, nullptr);
                 }
             }
         }
