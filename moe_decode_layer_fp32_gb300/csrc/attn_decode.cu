@@ -21,8 +21,8 @@
 // 16-bit type (f16 for E4M3, which holds its values), which keeps them to 16 bits and
 // more at no cost in MMAs; bf16 queries over an E4M3 cache as two E4M3 terms.
 //
-// Measured: 1 x 131071 keys of 8 heads of 128, bf16 (537 MB) 89 us, 6.0 TB/s; 128
-// requests of 1 to 4096 keys, bf16 140 us, 6.2 TB/s, and E4M3 93 us, 4.7 TB/s: there the
+// Measured: 1 x 131071 keys of 8 heads of 128, bf16 (537 MB) 87 us, 6.1 TB/s; 128
+// requests of 1 to 4096 keys, bf16 140 us, 6.2 TB/s, and E4M3 94 us, 4.7 TB/s: there the
 // instructions bound it, about 750 for a warp's 32 keys at 0.35 a clock and scheduler (105 us with
 // a mask or shift more per conversion).  Two CTAs per SM with a ring of three stages beat
 // three with two (64 x 2048 keys: bf16 91 and 98 us, E4M3 58 and 66) and tiles of 16 keys

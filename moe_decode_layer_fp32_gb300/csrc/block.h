@@ -217,7 +217,7 @@ __device__ __forceinline__ void load8_any(const void* p, int dt, long long i, fl
 
 // -1 for a token without an adapter; an index beyond the adapters is reported and counts as none.
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
-    const int i = a.adapter[t];
+    const int i = __ldcg(a.adapter + t);     // from L2: the projection reads it without a wait of its own
     if (i >= a.na) set_status(a.status, MOE_ERR_DEVICE);
     return i >= 0 && i < a.na ? i : -1;
 }

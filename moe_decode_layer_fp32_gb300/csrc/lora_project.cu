@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         for (int i = 0; i < early; ++i) load_w(i, i);
 
     // With adapters the kernel before is the one above, which had seen the end of its own predecessor
-    // before this one started: only what it writes itself is waited for, where it is read.
+    // before this one started: only what it writes itself is waited for, where it is read (other inputs
+    // that an earlier kernel may have written come from L2, past what L1 may still hold).
     if (a.r == 0) pdl_wait_primary();
 
     // ---- order of the tokens: by the warps that need it first (the adapters' copies and
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         }
         if (n < a.N) {
             if constexpr (F8) {
-                const float xs = a.x_scale[t];
+                const float xs = __ldcg(a.x_scale + t);
                 s.x *= xs * a.w_scale[n];
                 s.y *= xs * a.w_scale[n + 1];
                 s.z *= xs * a.w_scale[n + 2];

@@ -681,6 +681,42 @@ def test_lora_strides_and_equal_bits(B):
             assert torch.equal(y, y0)
 
 
+@pytest.mark.parametrize("x,T", [("bf16", 3), ("bf16", 48), ("e4m3", 128), ("f32", 70), ("bf16", 2)])
+def test_lora_inputs_of_the_kernel_before(B, x, T):
+    """x comes from the norm right before, the adapters' numbers from a copy before that; what an earlier
+    call left in a cache must not be seen."""
+    g, d, N, r, na = gen(T), 1024, 768, 32, 6
+    src = [normal(g, T, d) for _ in range(2)]
+    ids = [torch.randint(-1, na, (T,), generator=g, device="cuda", dtype=torch.int32) for _ in range(2)]
+    w = normal(g, N, d, std=0.02)
+    w, ws_ = (e4m3(w / 0.0004), torch.full((N,), 0.0004, device="cuda")) if x == "e4m3" else (w.to(torch.bfloat16), None)
+    lora = (normal(g, na, r, d, std=0.05, dtype=torch.bfloat16), normal(g, na, N, r, std=0.05, dtype=torch.bfloat16),
+            torch.rand(na, generator=g, device="cuda"))
+    h = torch.empty(T, d, dtype=torch.float8_e4m3fn if x == "e4m3" else DT[x], device="cuda")
+    hs = torch.empty(T, device="cuda") if x == "e4m3" else None
+    ad, ws = torch.empty(T, dtype=torch.int32, device="cuda"), B.new_lora_workspace(T, d, r)
+    y = torch.empty(T, N, device="cuda")
+
+    def step(i):
+        ad.copy_(ids[i])
+        B.moe_rmsnorm(src[i], None, 1e-6, h, y_scale=hs)
+        B.moe_lora_project(h, w, y, ws, lora=lora, adapter=ad, x_scale=hs, w_scale=ws_)
+
+    want = []
+    for i in range(2):
+        step(i)
+        torch.cuda.synchronize()
+        ref, size = O.lora_project(h, w, lora, ad, hs, ws_)
+        assert_within(y, ref, 64 * U * size, "y")
+        want.append(y.clone())
+    got = []
+    for k in range(60):
+        step(k % 2)
+        got.append(y.clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k % 2]) for k in range(60))
+
+
 def test_lora_reports_adapters_out_of_range(B):
     g = gen(3)
     x, w = normal(g, 3, 64, dtype=torch.bfloat16), normal(g, 32, 64, dtype=torch.bfloat16)
