@@ -209,12 +209,13 @@ cudaError_t launch(const LoraArgs& a, bool own_v, cudaStream_t s) {
 
 }  // namespace
 
-// Against the tensor-core kernel (us, that one second; bf16 without adapters): one token of
-// 2048 -> 2560 3.2 / 6.6, of 7168 -> 9216 21.0 / 26.0; two tokens 4.2 / 6.6 and 29.0 / 26.1, where
-// the shared memory reads of x begin to bound it: two tokens only over up to 64 MB of W.
+// Against the tensor-core kernel (us, that one second; without adapters): one token of 2048 -> 2560
+// bf16 3.1 / 5.6, of 7168 -> 9216 21.1 / 22.7; two tokens 4.1 / 5.6 and 28.9 / 22.7, of 4096 -> 4096
+// (34 MB) 10.5 / 9.6: there the shared memory reads of x bound it, so two tokens only over up to 20 MB
+// of W, or in fp32 (7168 -> 9216 29.0 / 31.1), whose three terms the other one multiplies.
 bool lora_gemv_fits(const LoraArgs& a) {
     const long long bytes = (long long)a.N * a.d * (a.x_dt == MOE_DTYPE_FP8_E4M3 ? 1 : 2);
-    return a.d <= kGemvMaxHidden && (a.T == 1 || (a.T == 2 && bytes <= 64ll << 20));
+    return a.d <= kGemvMaxHidden && (a.T == 1 || (a.T == 2 && (a.x_dt == MOE_DTYPE_F32 || bytes <= 20ll << 20)));
 }
 
 // A_a x in every block: while a block reads no more than 128 KB for it (from L2, at about 64
