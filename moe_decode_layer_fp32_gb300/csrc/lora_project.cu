@@ -5,7 +5,7 @@
 // and the tokens its columns: the W tiles go from HBM through a TMA ring straight
 // into tcgen05.mma as its A operand, whatever T is.
 //
-// Split.  A tile of 128 rows of W is one CTA, or a cluster of 2, 4 or 8 of them that
+// Split.  A tile of 128 rows of W is one CTA, or a cluster of 2 to 8 of them that
 // divide d where the tiles are fewer than the SMs; the cluster adds its parts up over
 // distributed shared memory in a fixed order, each CTA for its share of the tokens.
 //
@@ -753,11 +753,12 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
     const int tiles = (a.N + kRowsM - 1) / kRowsM;
     const bool low = a.r > 0;
     p.blocks = (a.d * (F8 ? 1 : 2) + kBlockBytes - 1) / kBlockBytes;
-    // Split d while the clusters still run at once (a cluster of 8 does not fill a
-    // GPC: about 7/8 of the SMs) and a CTA keeps two blocks or more.
+    // Split d while the clusters still run at once (clusters of 3 or 8 do not fill a
+    // GPC: 120 CTAs in threes do, 144 do not) and a CTA keeps two blocks or more.  Threes: 32 tokens of
+    // 7168 -> 5120 16.0 us against 19.8 in pairs; sixes gain 6 % there and lose 13 % at d 2048.
     p.split = 1;
-    for (int k = 2; k <= 8; k *= 2)
-        if (tiles * k <= (k == 8 ? sms * 13 / 16 : sms) && p.blocks / k >= 2) p.split = k;
+    for (int k : {2, 3, 4, 8})
+        if (tiles * k <= (k == 3 || k == 8 ? sms * 13 / 16 : sms) && p.blocks / k >= 2) p.split = k;
     // Shared memory: control words, adapter part of the own tokens, their v, B_a ring, W ring
     // (whose place the CTA's sums take at the end).
     const int lstage = low ? lora_stage_bytes(a.r) : 0;
@@ -777,7 +778,7 @@ cudaError_t launch_project(ProjArgs& p, cudaStream_t s) {
         p.stages = std::min(kMaxStages, (kProjSmem - 1024 - off) / kStageBytes);
     };
     plan();
-    while (p.stages < 2 && p.split < 8) {
+    while (p.stages < 2 && p.split <= 4) {
         p.split *= 2;     // fewer own tokens: room for the ring
         plan();
     }

@@ -643,6 +643,13 @@ def test_lora_many_tokens_and_ranks(B, x, r):
     lora_case(B, 128, 256, 136, x=x, r=r, na=2, adapter=[1] * 128, seed=r)
 
 
+@pytest.mark.parametrize("x", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("T,r", [(3, 16), (100, 16), (128, 128)])
+def test_lora_rows_in_threes(B, x, T, r):
+    """As many tiles of rows as make three CTAs share each."""
+    lora_case(B, T, 1168, 5120, x=x, r=r, na=9, seed=T + r)
+
+
 def test_lora_keeps_adapters_apart(B):
     """An adapter of NaN and infinite weights spoils its own tokens alone, whichever kernel forms A x."""
     for T, r in ((6, 8), (96, 64)):
