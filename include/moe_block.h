@@ -52,7 +52,7 @@ extern "C" {
  *   y             [T, d]: F32 or BF16 (y_scale is then NULL), or E4M3 codes
  *   y_scale       float[T] (group 0) or float[T, d / group] (group 128), rows
  *                 packed: amax / 448 of the row (of each 128 columns), 1 where
- *                 that is 0; a code is y / scale rounded to E4M3
+ *                 that is 0 in fp32; a code is y / scale rounded to E4M3
  * Limits: d a multiple of 8 in [8, 32768]; group 0 or 128 (d % 128 == 0);
  * pointers 16-byte aligned and row strides multiples of 8.
  * y may not overlap the inputs unless it is x (or residual) itself, of the

@@ -21,6 +21,7 @@ namespace moe {
 namespace {
 
 constexpr int kWalkThreads = 512;    // most threads of a block that walks over rows
+constexpr float kFewest = 0x1p-100f; // maxima and scales from here to its reciprocal are divided by directly
 
 template <bool BF>
 __device__ __forceinline__ void raw8(const char* p, float2 (&f)[4]) {
@@ -157,12 +158,23 @@ __global__ void __launch_bounds__(WALK ? kWalkThreads : 1024, !WALK ? 1 : CH <= 
         const float v = fmaf(sum, inv_d, a.eps), r0 = rsqrtf(v);
         const float rstd = r0 > 0.0f ? r0 * fmaf(-0.5f * v * r0, r0, 1.5f) : r0;
         // E4M3: with m = max |z w|, the scale is m rstd / 448 and a code z w rstd / scale =
-        // z w (448 / m): within 3 ulp of the division, which moves a code only next to a tie
-        float up = rstd;
+        // z w (448 / m): within 3 ulp of the division, which moves a code only next to a tie.  Where
+        // m or the scale is so far from 1 that 448 / m, or the few bits of a subnormal scale, would not do, z w is
+        // brought near 1 by a power of two and divided by the scale as stored.  A scale that is 0 in fp32 becomes 1.
+        float up = rstd, near_one = 1.0f;
         auto scale_of = [&](float m, float* out, bool mine) {
-            const float amax = m * rstd;
-            up = amax > 0.0f ? __fdividef(448.0f, m) : rstd;
-            if (mine) *out = amax > 0.0f ? over_448(amax) : 1.0f;
+            float s = over_448(m * rstd);
+            up = rstd;
+            near_one = 1.0f;
+            if (m >= kFewest && m <= 1.0f / kFewest && s >= kFewest) {
+                up = __fdividef(448.0f, m);
+            } else if (s > 0.0f) {
+                near_one = m > 1.0f ? kFewest : 1.0f / kFewest;
+                up = rstd / (s * near_one);
+            } else {
+                s = 1.0f;        // also beside a NaN
+            }
+            if (mine) *out = s;
         };
         if (row_scale) {
             const float mx = warp_max(lane < nw ? s_max[phase][lane] : 0.0f);
@@ -181,6 +193,10 @@ __global__ void __launch_bounds__(WALK ? kWalkThreads : 1024, !WALK ? 1 : CH <= 
                 scale_of(m, a.y_scale + t * groups + c / 16, c < chunks && lane % 16 == 0);
             }
             if (c >= chunks) continue;
+            if (near_one != 1.0f) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[j][e] = fmul2(z[j][e], make_float2(near_one, near_one));
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[j][e] = fmul2(z[j][e], make_float2(up, up));
             if (a.y_scale)
