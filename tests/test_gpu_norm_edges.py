@@ -1,4 +1,5 @@
-"""The norm's E4M3 codes at the ends of fp32's range, against the fp64 oracle.
+"""The norm's E4M3 codes at the ends of fp32's range, and its row-walking form with a scale per 128
+columns, against the fp64 oracle.
 
 Bounds (u = 2^-24): a scale is amax / 448 within 40 u, and within half a step of fp32's subnormals
 (2^-150) of that; a code times its scale is y within 2^-4 of y (half a step of E4M3), 2^-10 of the scale
@@ -9,7 +10,7 @@ import torch
 
 from oracle import block_oracle as O
 from tests.helpers import ensure_built
-from tests.test_gpu_block import DT, U, assert_within, gen, normal
+from tests.test_gpu_block import DT, U, assert_within, gen, normal, run_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,9 @@ def test_norm_codes_below_the_smallest_scale(B):
     c = O.f64(y)
     assert (c[0] == 0).all() and (c[1, 128:] == 0).all() and c[1, 3] == 448
     assert torch.isnan(c[2]).all()
+
+
+@pytest.mark.parametrize("T,d", [(1000, 128), (700, 1152), (400, 4224), (461, 7168), (331, 8320), (310, 16384)])
+@pytest.mark.parametrize("x,res", [("bf16", "bf16"), ("f32", None), ("bf16", None), ("f32", "f32")])
+def test_norm_walk_with_a_scale_per_128_columns(B, T, d, x, res):
+    run_norm(B, T, d, x=x, res=res, y="e4m3", group=128, seed=T + d)
