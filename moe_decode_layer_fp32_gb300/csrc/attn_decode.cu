@@ -90,9 +90,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// tanh(x) = 1 - 2 / (1 + e^2x), to about 2^-22 of 1 (not of small results).
+// tanh(x) = 1 - 2 / (1 + e^2x), to about 2^-22 of 1 (not of small results).  Large x: the division
+// gives 0 from a divisor of 2^126 on, an infinite one included; NaN stays NaN.
 __device__ __forceinline__ float tanh_fast(float x) {
-    return 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(fminf(2.0f * kLog2e * x, 126.0f)));
+    return 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(2.0f * kLog2e * x));
 }
 // bf16 parts by truncation: p = hi + rest exactly, rest of p's sign.
 __device__ __forceinline__ float bf16_trunc(float p) { return __uint_as_float(__float_as_uint(p) & 0xffff0000u); }

@@ -1,0 +1,101 @@
+"""Attention over the paged cache at the ends of its range, against the fp64 oracle: NaN and infinite
+queries and keys."""
+
+import math
+
+import pytest
+import torch
+
+from oracle import block_oracle as O
+from tests.helpers import ensure_built
+from tests.test_gpu_block import BF, DT, U, assert_within, attn_case, gen, make_cache, normal, raw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return ensure_built()
+
+
+class One:
+    """One request of n keys, pages in order; `run` returns (out, lse) and `want` the oracle's."""
+
+    def __init__(self, B, n, hq, hkv, D, q="bf16", dtype="bf16", seed=0, page=16):
+        self.B, self.n, self.hq = B, n, hq
+        g = gen(seed)
+        pages = (n + page - 1) // page
+        self.k, self.v, self.ks, self.vs, self.cache = make_cache(B, g, pages, page, hkv, D, dtype)
+        self.table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+        self.q = normal(g, 1, hq, D, dtype=DT[q])
+        self.page, self.D = page, D
+
+    def put(self, t, key, head, dim, value):
+        raw(t)[key // self.page, key % self.page, head, dim] = raw(torch.tensor([value]).to(t.dtype))[0].item()
+
+    def run(self, softcap=0.0, scale=None, out=None):
+        o = torch.empty(self.q.shape, dtype=DT[out] if out else self.q.dtype, device="cuda")
+        lse = torch.empty(1, self.hq, device="cuda")
+        ws = self.B.new_attn_workspace(1, self.hq, self.k.shape[2], self.D)
+        self.scale = self.D ** -0.5 if scale is None else scale
+        self.B.moe_attn_decode(self.q, self.cache, self.table, torch.tensor([self.n], dtype=torch.int32, device="cuda"),
+                               self.scale, o, ws, softcap=softcap, lse=lse)
+        torch.cuda.synchronize()
+        assert self.B.moe_read_status(ws)[0] == 0
+        return o[0], lse[0]
+
+    def rows(self):
+        return (O.cached_rows(self.k, self.ks, self.table[0], 0, self.n),
+                O.cached_rows(self.v, self.vs, self.table[0], 0, self.n))
+
+    def want(self, softcap=0.0):
+        return O.decode_attention(self.q[0], self.rows(), self.scale, softcap)
+
+
+def bound_of(want, out_dtype, top):
+    return 1e-4 * top + (1.01 * BF * want.abs() if out_dtype == torch.bfloat16 else 0.0)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("q", ["bf16", "f32"])
+def test_attn_nan_queries_and_keys(B, q, hq, dtype, softcap):
+    """A NaN in a query spoils its own head, one in a key all heads of its key-value head, with a cap or without."""
+    for n in (100, 3000):
+        c = One(B, n, 2 * hq, 2, 64, q, dtype, seed=n)
+        c.q[0, 1, 7] = math.nan
+        o, lse = c.run(softcap)
+        want, _ = c.want(softcap)
+        bad = torch.zeros(2 * hq, dtype=torch.bool)
+        bad[1] = True
+        assert torch.isnan(o[1]).all() and torch.isnan(lse[1])
+        top = c.rows()[1].abs().max().item()
+        assert_within(o.cpu()[~bad], want[~bad], bound_of(want[~bad], o.dtype, top), "other heads")
+        c.put(c.k, n // 2, 1, 9, math.nan)
+        o, _ = c.run(softcap)
+        want, _ = c.want(softcap)
+        bad[hq:] = True
+        assert torch.isnan(o[hq:]).all()
+        assert_within(o.cpu()[~bad], want[~bad], bound_of(want[~bad], o.dtype, top), "the other key-value head")
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+def test_attn_infinite_bf16_queries(B, hq):
+    """Over a bf16 cache the scores are infinite (+-cap with a cap); over an E4M3 cache the head gets NaN."""
+    for dtype in ("bf16", "e4m3"):
+        c = One(B, 200, hq, 1, 64, "bf16", dtype, seed=hq)
+        c.q[0, 2, 3] = math.inf
+        for i in range(200):      # no zero beside the infinity
+            c.put(c.k, i, 0, 3, 1.0 if i % 3 else -1.0)
+        others = [h for h in range(hq) if h != 2]
+        for cap in (0.0, 30.0):
+            o, _ = c.run(cap)
+            want, _ = c.want(cap)
+            assert_within(o[others], want[others], bound_of(want[others], o.dtype, c.rows()[1].abs().max().item()), "others")
+            if dtype == "e4m3" or cap == 0.0:
+                assert torch.isnan(o[2]).all()
+            else:
+                assert_within(o[2], want[2], bound_of(want[2], o.dtype, 4.0), "capped")
