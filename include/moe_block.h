@@ -133,7 +133,7 @@ size_t moe_attn_workspace_bytes(int B, int q_heads, int heads, int head_dim);
  * softcap 0.  A request with n <= 0 gets zeros, and a score of -inf weighs
  * nothing (a head whose scores all are -inf gets zeros too).  Slots outside that range and
  * table entries of pages wholly outside it are not read.
- * Over an E4M3 cache a head with an infinity in a BF16 q gets NaN.
+ * Over an E4M3 cache a head with an infinity in a BF16 q gets NaN (a BF16 out and softcap <= 256).
  *   q           [B, q_heads, D] F32 or BF16; out the same shape, F32 or BF16
  *   block_table int32[B, max_pages], row stride table_ld
  *   lse         float[B, q_heads] or NULL: log of the sum of exp of the scores

@@ -45,6 +45,10 @@ constexpr int kJoinGroup = 16;
 // What a tile and the beginning and end of a unit cost.  Unit costs of 1, 3, 5 and 8: 155, 137, 137, 137 us
 // for 128 ragged bf16 requests, 131, 108, 110, 115 for E4M3.
 constexpr int kTileCost = 2, kUnitCost = 3;
+// The fast tanh is off by 2^-22 of the cap: up to 256, 2^-14 of a weight, where a bf16 output is rounded to
+// 2^-9.  Larger caps take the kernel of fp32 outputs, with tanhf (64 x 2048 keys, bf16 91 and 94 us, E4M3 60
+// and 60; with 16 heads to a key-value head, which that kernel takes in two parts, 96 and 181, 88 and 110).
+constexpr float kFastCap = 256.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -131,7 +135,7 @@ struct Share {
 };
 
 // DP: head_dim rounded up to 64, 128 or 256.  F8: E4M3 cache.  ROWS: query heads of a
-// unit, 8 or 16.  EX: fp32 queries or output, whose terms keep 22 bits or more.
+// unit, 8 or 16.  EX: fp32 queries or output, or a large cap: terms keep 22 bits or more.
 template <int DP, bool F8, int ROWS, bool EX>
 struct Attn {
     static constexpr int kElem = F8 ? 1 : 2;
@@ -976,7 +980,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 
 template <int DP, bool F8>
 cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
-    const bool exact = a.q_dt == MOE_DTYPE_F32 || a.o_dt == MOE_DTYPE_F32;
+    const bool exact = a.q_dt == MOE_DTYPE_F32 || a.o_dt == MOE_DTYPE_F32 || a.softcap > kFastCap;
     if (exact) return launch<DP, F8, 8, true>(a, s);
     if constexpr (DP <= 128) {
         if (rows_of(a.group, DP, false) == 16) return launch<DP, F8, 16, false>(a, s);

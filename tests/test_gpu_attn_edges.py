@@ -1,5 +1,5 @@
 """Attention over the paged cache at the ends of its range, against the fp64 oracle: NaN and infinite
-queries and keys."""
+queries and keys, large caps."""
 
 import math
 
@@ -99,3 +99,10 @@ def test_attn_infinite_bf16_queries(B, hq):
                 assert torch.isnan(o[2]).all()
             else:
                 assert_within(o[2], want[2], bound_of(want[2], o.dtype, 4.0), "capped")
+
+
+@pytest.mark.parametrize("softcap", [300.0, 1e5])
+@pytest.mark.parametrize("q,dtype", [("bf16", "bf16"), ("bf16", "e4m3"), ("f32", "bf16")])
+@pytest.mark.parametrize("hq", [8, 32])
+def test_attn_large_softcap(B, softcap, q, dtype, hq):
+    attn_case(B, [1, 64, 300, 3000], hq, 2, 128, 32, q=q, dtype=dtype, softcap=softcap, seed=9)
