@@ -160,6 +160,8 @@ struct Attn {
     // would, for the sake of one of their heads).  p in f16 is scaled to use its range: 2^7
     // at the maximum, 2^15 with the slack.
     static constexpr float kSlack = 8.0f;
+    static constexpr float kLeast = 0x1p-126f;                       // bf16's least normal number, and two of it
+    static constexpr uint32_t kLeast2 = 0x00800080u;
     static constexpr float kPShift = F8 ? 7.0f : 0.0f;
     static constexpr int kCtasPerSm = kTileBytes > 4096 ? 1 : 2;
     static constexpr int kStages = 3;
@@ -524,7 +526,8 @@ struct Attn {
                         p0 -= r.x;
                         p1 -= r.y;
                     } else if (!EX && t == 1) {
-                        pf[t][nt][rr] = pack_bf16x2(p0, p1);
+                        // 16 heads: both terms go into one sum, so that with an infinite v neither may be 0
+                        pf[t][nt][rr] = ROWS == 16 ? pack_bf16x2(fmaxf(p0, kLeast), fmaxf(p1, kLeast)) : pack_bf16x2(p0, p1);
                     } else {
                         pf[t][nt][rr] = pack_hi(p0, p1);
                         p0 -= bf16_trunc(p0);
@@ -582,8 +585,10 @@ struct Attn {
                         mma(acc, p0[0], 0u, p0b[0], 0u, b[0], b[1]);
                     } else {
                         mma(acc, p0[0], pf[1][2 * kg][0], p0b[0], pf[1][2 * kg + 1][0], b[0], b[1]);
+                        // third terms beside the second ones; the least bf16 instead of 0 leaves the first
+                        // terms' sum as it is, next to an infinite v too
                         if constexpr (kPTerms == 3)
-                            mma(acc, 0u, pf[2][2 * kg][0], 0u, pf[2][2 * kg + 1][0], b[0], b[1]);
+                            mma(acc, kLeast2, pf[2][2 * kg][0], kLeast2, pf[2][2 * kg + 1][0], b[0], b[1]);
                     }
                 }
             }
@@ -699,7 +704,8 @@ struct Attn {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float (&o)[4] = st.o[w * kVElems + e + k];
-                            v[k] = ROWS == 16 ? o[2 * rr + i] : o[i] + o[2 + i];
+                            // an infinite sum of first terms stands: a second term may be 0, and its sum NaN
+                            v[k] = ROWS == 16 ? o[2 * rr + i] : fabsf(o[i]) < CUDART_INF_F ? o[i] + o[2 + i] : o[i];
                         }
                         const int row = rr * 8 + lane / 4, f4 = (colb + e) / 4;
                         mine[row * (DP / 4) + (f4 ^ (row & 7))] = make_float4(v[0], v[1], v[2], v[3]);

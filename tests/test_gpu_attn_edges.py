@@ -1,5 +1,5 @@
 """Attention over the paged cache at the ends of its range, against the fp64 oracle: NaN and infinite
-queries and keys, large caps."""
+queries, keys and values, large caps."""
 
 import math
 
@@ -106,3 +106,20 @@ def test_attn_infinite_bf16_queries(B, hq):
 @pytest.mark.parametrize("hq", [8, 32])
 def test_attn_large_softcap(B, softcap, q, dtype, hq):
     attn_case(B, [1, 64, 300, 3000], hq, 2, 128, 32, q=q, dtype=dtype, softcap=softcap, seed=9)
+
+
+@pytest.mark.parametrize("q,out", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("hq", [4, 16])
+def test_attn_infinite_values(B, q, out, hq):
+    """An infinite cached value makes its column infinite and leaves the others alone."""
+    for n in (5, 100, 3000):
+        c = One(B, n, 2 * hq, 2, 64, q, "bf16", seed=n)
+        c.put(c.v, n // 2, 1, 9, math.inf)
+        c.put(c.v, n - 1, 1, 40, -math.inf)
+        o, _ = c.run(out=out)
+        want, _ = c.want()
+        assert torch.equal(torch.isinf(want), torch.isinf(o.cpu())), "infinities"
+        at = torch.isinf(want)
+        assert torch.equal(O.f64(o)[at], want[at])
+        rest = torch.where(at, torch.zeros_like(want), want)
+        assert_within(torch.where(at, torch.zeros_like(want), O.f64(o)), rest, bound_of(rest, o.dtype, 5.0), "the others")
