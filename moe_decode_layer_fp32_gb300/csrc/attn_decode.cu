@@ -338,7 +338,7 @@ struct Attn {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 int e = 0;
                 if (mx > 0.0f && mx < CUDART_INF_F) frexpf(mx, &e);
-                e = min(max(8 - e, -100), 100);
+                e = min(8 - e, 126);             // 8 - e >= -120: both factors are normal numbers
                 const float up = ldexpf(1.0f, e);
                 back = ldexpf(1.0f, -e);
 #pragma unroll
@@ -346,7 +346,7 @@ struct Attn {
 #pragma unroll
                     for (int i = 0; i < E; ++i) f[j][i] *= up;
             }
-            st.qf[rr] = a.scale * ks * back;
+            st.qf[rr] = a.scale * (ks * back);   // in this order: a small scale of k goes with a large q
             if constexpr (kQ8) {
                 // E4M3 has no infinity: a head with one gets NaN
                 if (mx == CUDART_INF_F) st.qf[rr] = CUDART_NAN_F;

@@ -1,5 +1,5 @@
 """Attention over the paged cache at the ends of its range, against the fp64 oracle: NaN and infinite
-queries, keys and values, large caps."""
+queries, keys and values, large caps, queries and scales far from 1."""
 
 import math
 
@@ -123,3 +123,16 @@ def test_attn_infinite_values(B, q, out, hq):
         assert torch.equal(O.f64(o)[at], want[at])
         rest = torch.where(at, torch.zeros_like(want), want)
         assert_within(torch.where(at, torch.zeros_like(want), O.f64(o)), rest, bound_of(rest, o.dtype, 5.0), "the others")
+
+
+@pytest.mark.parametrize("q", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [-116, -110, 110, 122])
+def test_attn_e4m3_queries_far_from_one(B, q, power):
+    """q of 2^power over keys whose scale is 2^-power."""
+    c = One(B, 200, 4, 1, 64, q, "e4m3", seed=3)
+    c.q.mul_(2.0 ** power)
+    c.ks.mul_(2.0 ** -power)
+    o, lse = c.run()
+    want, wl = c.want()
+    assert_within(o[:], want, bound_of(want, o.dtype, c.rows()[1].abs().max().item()), "out")
+    assert_within(lse, wl, 1e-4 + 4 * U * wl.abs(), "lse")
