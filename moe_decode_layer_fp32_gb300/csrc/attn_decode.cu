@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t pack_hi(float a, float b) { return __byte_pe
 
 // Where a CTA (or one of its warps) stands.
 struct Cursor {
-    int b, unit, tile, tiles, first, n;
+    int b, unit, tile, tiles, first, keys; // keys from the first on
     int last;                              // tiles of the unit that begin before the run's end
     const int32_t* row;                    // the request's row of the block table
     long long base;                        // where the unit begins in the line of all units
@@ -204,9 +204,9 @@ struct Attn {
     __device__ static __forceinline__ void set_request(const AttnArgs& a, Cursor& c) {
         int n = max(a.seq_lens[c.b], 0);
         n = (int)min((long long)n, (long long)a.max_pages * a.c.page_size);
-        c.n = n;
         c.first = a.window > 0 ? max(0, n - a.window) : 0;
-        c.tiles = (n - c.first + kTileKeys - 1) / kTileKeys;
+        c.keys = n - c.first;
+        c.tiles = (int)(((uint32_t)c.keys + kTileKeys - 1) / kTileKeys);
         c.row = a.table + c.b * a.table_ld;
     }
     // To the next tile; where none begins before `end`, to none of the run.
@@ -227,8 +227,10 @@ struct Attn {
     }
     // Page and slot of the key that lane `lane` looks after in the warp's tile; page -1: none.
     __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
-        const int key = c.first + c.tile * kTileKeys + warp * KT + lane;
-        if (!inside(c) || lane >= KT || key >= c.n) return make_int2(-1, 0);
+        // unsigned: the end of the last tile may lie beyond 2^31
+        const uint32_t at = (uint32_t)c.tile * kTileKeys + warp * KT + lane;
+        if (!inside(c) || lane >= KT || at >= (uint32_t)c.keys) return make_int2(-1, 0);
+        const int key = c.first + (int)at;
         const int col = a.page_shift >= 0 ? key >> a.page_shift : key / a.c.page_size;
         const int page = c.row[col];
         if (page < 0 || page >= a.c.num_pages) {

@@ -1,5 +1,5 @@
 """Attention over the paged cache at the ends of its range, against the fp64 oracle: NaN and infinite
-queries, keys and values, large caps, queries and scales far from 1."""
+queries, keys and values, large caps, queries and scales far from 1, lengths near 2^31."""
 
 import math
 
@@ -136,3 +136,29 @@ def test_attn_e4m3_queries_far_from_one(B, q, power):
     want, wl = c.want()
     assert_within(o[:], want, bound_of(want, o.dtype, c.rows()[1].abs().max().item()), "out")
     assert_within(lse, wl, 1e-4 + 4 * U * wl.abs(), "lse")
+
+
+@pytest.mark.parametrize("window", [0, 1000])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_lengths_near_the_limit_of_int(B, window, dtype):
+    """2^31 - 1 keys, all in one row of memory (a page whose slots have stride 0)."""
+    n, D = 2 ** 31 - 1, 16
+    g = gen(5)
+    row = normal(g, 1, D).to(DT[dtype])
+    kv = row.view(torch.uint8 if dtype == "e4m3" else torch.int16).as_strided((1, n, 1, D), (D, 0, D, 1)).view(DT[dtype])
+    s = torch.full((1,), 0.5, device="cuda") if dtype == "e4m3" else None
+    cache = B.KvCache(kv, kv, s, s)
+    q, o = normal(g, 1, 2, D, dtype=torch.bfloat16), torch.empty(1, 2, D, device="cuda")
+    lse, ws = torch.empty(1, 2, device="cuda"), B.new_attn_workspace(1, 2, 1, D)
+    table, seq = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+    B.moe_attn_decode(q, cache, table, seq, 0.25, o, ws, window=window, lse=lse)
+    torch.cuda.synchronize()
+    assert B.moe_read_status(ws)[0] == 0
+    v = O.f64(row)[0] * (0.5 if s is not None else 1.0)
+    # a warp adds up 2^31 / 1216 equal weights in tiles of 32 (one addition to o, four to a thread's part of
+    # the sum), each rounded to 2^-24
+    tol = 5 * 2 ** 31 / 1216 / 32 * U if not window else 1e-5
+    assert_within(o[0], v.expand(2, D), tol * v.abs().expand(2, D) + 1e-30, "out")
+    score = (O.f64(q)[0] @ v) * 0.25
+    want = score + math.log(window or n)
+    assert_within(lse[0], want, 1e-4 + tol, "lse")
