@@ -1,5 +1,6 @@
 """Attention over the paged cache at the ends of its range, against the fp64 oracle: NaN and infinite
-queries, keys and values, large caps, queries and scales far from 1, lengths near 2^31."""
+queries, keys and values, large caps, queries and scales far from 1, lengths near 2^31, and the digits that
+fp32 queries and outputs keep."""
 
 import math
 
@@ -162,3 +163,31 @@ def test_attn_lengths_near_the_limit_of_int(B, window, dtype):
     score = (O.f64(q)[0] @ v) * 0.25
     want = score + math.log(window or n)
     assert_within(lse[0], want, 1e-4 + tol, "lse")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_fp32_keeps_its_digits(B, dtype):
+    """fp32 queries and outputs keep 22 bits.  A score of one key is the logarithm of its sum: one product
+    (2^-22), a scale or two and the change of base and back (with 7 added to it and taken off again), under 16
+    roundings of 2^-24.  And with scores of one product each, up to 1, over positive values: 2^-22 for q's
+    terms and for the exponential, 2^-23 for p's, 4 cuts of 2^-23 in a tile's sum, and 2^-24 for each of 6
+    roundings of the score, 8 tiles, 8 parts and 8 terms of the sum of weights: 48 2^-24, under 2^-18
+    (weights of 16 bits, truncated, would be off by 2^-17 on average)."""
+    c = One(B, 1, 4, 1, 64, "f32", dtype, seed=1)
+    c.q.mul_(4.0)
+    raw(c.k).zero_()
+    c.put(c.k, 0, 0, 5, 1.625)
+    _, lse = c.run(scale=3.7 / (c.ks[0].item() if c.ks is not None else 1.0))
+    _, wl = c.want()
+    assert_within(lse, wl, 16 * U * (wl.abs() + 7), "score")
+    c = One(B, 900, 4, 1, 64, "f32", dtype, seed=2)
+    c.q.uniform_(-1.0, 1.0, generator=gen(4))
+    k5, v = raw(c.k)[..., 5].clone(), c.v.float().abs()
+    raw(c.k).zero_()
+    raw(c.k)[..., 5] = k5
+    c.v.copy_(v.to(c.v.dtype))
+    kmax = c.rows()[0].abs().max().item()
+    o, lse = c.run(scale=1.0 / kmax)
+    want, wl = c.want()
+    assert (want > 0).all()
+    assert_within(o, want, 2.0 ** -18 * want, "out")
