@@ -29,6 +29,7 @@
 // rest (with a division for the place in the ring, and one lane instead of a uniform warp, 26.7 us).
 // With 64 adapters of rank 64 (58 MB each of A and B) the third takes 42 us, 14 of them A x.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "block.h"
@@ -120,16 +121,19 @@ __global__ void __launch_bounds__(kShrinkThreads, 4) lora_shrink_kernel(const __
             float f[8];
             load8_f32(a.x, MOE_DTYPE_F32, t * a.x_ld + c, f);
 #pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += 0.0f;       // every NaN has its first fraction bit set
+#pragma unroll
             for (int p = 0; p < 3; ++p) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+                    // truncated, so that all terms have x's sign: 8 bits each
+                    w[e] = __byte_perm(__float_as_uint(f[2 * e]), __float_as_uint(f[2 * e + 1]), 0x7632);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float b = __uint_as_float(h ? w[e] & 0xffff0000u : w[e] << 16);
                         // an infinite or NaN first term stands alone
-                        f[2 * e + h] = fabsf(b) <= 3.4028234e38f ? f[2 * e + h] - b : 0.0f;
+                        f[2 * e + h] = fabsf(b) <= FLT_MAX ? f[2 * e + h] - b : 0.0f;
                     }
                 }
                 *reinterpret_cast<uint4*>(a.xs + p * plane + (long long)t * a.d + c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -633,9 +637,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         }
     } else if (warp >= 8) {
         // ===================== epilogue: blocks of sums into registers =====================
-        float acc[TP];
+        float2 acc[TP / 2];
 #pragma unroll
-        for (int t = 0; t < TP; ++t) acc[t] = 0.0f;
+        for (int t = 0; t < TP / 2; ++t) acc[t] = make_float2(0.0f, 0.0f);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         for (int c = 0; c < chunks; ++c) {
             const uint32_t buf = c & 1;
@@ -648,7 +652,13 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
                     float v[16];
                     tmem_ld16(tmem + buf * kBufCols + g * TP + t + lanes, v);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[t + e] += v[e];
+                    for (int e = 0; e < 16; e += 2) {
+                        float2 u = make_float2(v[e], v[e + 1]);
+                        // beside an infinite first term (of an infinite weight) the others are infinite of
+                        // its sign, or NaN where a term is 0: that one stands
+                        if (g > 0) u = make_float2(fminf(u.x, FLT_MAX), fminf(u.y, FLT_MAX));
+                        acc[(t + e) / 2] = fadd2(acc[(t + e) / 2], u);
+                    }
                 }
             tc_fence_before_sync();
             __syncwarp();
@@ -658,7 +668,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         const int m = (warp & 3) * 32 + lane;
 #pragma unroll
         for (int t = 0; t < TP; ++t)
-            if (t < a.T) red[t * kRowsM + m] = acc[t];
+            if (t < a.T) red[t * kRowsM + m] = t % 2 ? acc[t / 2].y : acc[t / 2].x;
     }
     tc_fence_before_sync();
     if (p.split > 1) cluster_sync_all();

@@ -1,0 +1,48 @@
+"""The projection with adapters: infinite weights, against the fp64
+oracle (tolerance: 64 u of sum |w x|, u = 2^-24, as in test_gpu_block.py)."""
+
+import math
+
+import pytest
+import torch
+
+from oracle import block_oracle as O
+from tests.helpers import ensure_built
+from tests.test_gpu_block import DT, U, assert_within, e4m3, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return ensure_built()
+
+
+def check(y, want, size, at):
+    """y equals the oracle's infinities at `at` and is near it elsewhere."""
+    got = O.f64(y)
+    assert torch.isinf(want[at]).all() and torch.equal(got[at], want[at]), "infinities"
+    zero = torch.zeros_like(want)
+    assert_within(torch.where(at, zero, got), torch.where(at, zero, want), torch.where(at, zero, 64 * U * size), "the others")
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 33, 128])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_lora_infinite_weights(B, T, x):
+    """A row of W with an infinity gives infinities of x's sign, whatever bits x has."""
+    g, d, N = gen(T), 1024, 264
+    xt = normal(g, T, d, dtype=DT[x])
+    xt[0] = xt[0].to(torch.bfloat16).to(DT[x])      # nothing beyond a bf16
+    w = normal(g, N, d, std=0.02, dtype=torch.bfloat16)
+    w[7, 300], w[200, 1000] = math.inf, -math.inf
+    y = torch.empty(T, N, device="cuda")
+    B.moe_lora_project(xt, w, y, B.new_lora_workspace(T, d))
+    fin = w.clone()
+    fin[7, 300], fin[200, 1000] = 0, 0
+    want, size = O.lora_project(xt, fin)
+    want[:, 7], want[:, 200] = torch.sign(O.f64(xt)[:, 300]) * math.inf, torch.sign(O.f64(xt)[:, 1000]) * -math.inf
+    at = torch.zeros(T, N, dtype=torch.bool)
+    at[:, [7, 200]] = True
+    check(y, want, size, at)
