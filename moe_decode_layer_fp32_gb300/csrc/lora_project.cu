@@ -582,7 +582,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const float lo = c[h / 2][h % 2 * 2], hi = c[h / 2][h % 2 * 2 + 1];
-                            const float s = lo + (hi + __shfl_xor_sync(0xffffffffu, lo, 1));
+                            // an infinite product of the first term (an infinity in B_a) stands: the others' may
+                            // be NaN or of the other sign
+                            const float third = __shfl_xor_sync(0xffffffffu, lo, 1);
+                            const float s = fabsf(lo) <= FLT_MAX ? lo + (hi + third) : lo;
                             if (write) out[h * 8] = k0 == 0 ? s : out[h * 8] + s;
                         }
                     }
@@ -620,7 +623,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 float* at = out + (e & 1) * kRowsM + m + (e >> 1) * 8;
-                                const float s = c[0][e] + (c[1][e] + c[2][e]);
+                                const float s = fabsf(c[0][e]) <= FLT_MAX ? c[0][e] + (c[1][e] + c[2][e]) : c[0][e];
                                 if ((e & 1) ? t1 : t0) *at = k0 == 0 ? s : *at + s;
                             }
                         }

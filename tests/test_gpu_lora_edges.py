@@ -46,3 +46,28 @@ def test_lora_infinite_weights(B, T, x):
     at = torch.zeros(T, N, dtype=torch.bool)
     at[:, [7, 200]] = True
     check(y, want, size, at)
+
+
+@pytest.mark.parametrize("T,r,na", [(1, 16, 2), (2, 128, 2), (6, 16, 4), (6, 72, 4), (100, 16, 3), (100, 128, 3), (64, 24, 40)])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_lora_infinite_adapter_weights(B, T, r, na, x):
+    """An infinity in B_a gives the adapter's tokens one of v's sign."""
+    g, d, N = gen(T + r), 512, 264
+    xt, w = normal(g, T, d, dtype=DT[x]), normal(g, N, d, std=0.02, dtype=torch.bfloat16)
+    la, lb = normal(g, na, r, d, std=0.05, dtype=torch.bfloat16), normal(g, na, N, r, std=0.05, dtype=torch.bfloat16)
+    la[1, 3] = 0.0
+    la[1, 3, 8] = 0.5                               # v = x[8] / 2 exactly: x's bits alone
+    scale = torch.ones(na, device="cuda")
+    ad = torch.tensor([t % na if T > 2 else 1 for t in range(T)], dtype=torch.int32, device="cuda")
+    fin = lb.clone()
+    lb[1, 5, 3], lb[1, 250, 3] = math.inf, -math.inf
+    fin[1, 5, 3], fin[1, 250, 3] = 0, 0
+    y = torch.empty(T, N, device="cuda")
+    B.moe_lora_project(xt, w, y, B.new_lora_workspace(T, d, r), lora=(la, lb, scale), adapter=ad)
+    want, size = O.lora_project(xt, w, (la, fin, scale), ad)
+    mine = (ad == 1).cpu()
+    sign = torch.sign(O.f64(xt)[mine, 8])
+    at = torch.zeros(T, N, dtype=torch.bool)
+    at[mine, 5], at[mine, 250] = True, True
+    want[mine, 5], want[mine, 250] = sign * math.inf, -sign * math.inf
+    check(y, want, size, at)
