@@ -697,10 +697,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         if (n < a.N) {
             if constexpr (F8) {
                 const float xs = __ldcg(a.x_scale + t);
-                s.x *= xs * a.w_scale[n];
-                s.y *= xs * a.w_scale[n + 1];
-                s.z *= xs * a.w_scale[n + 2];
-                s.w *= xs * a.w_scale[n + 3];
+                s.x *= xs * __ldcg(a.w_scale + n);
+                s.y *= xs * __ldcg(a.w_scale + n + 1);
+                s.z *= xs * __ldcg(a.w_scale + n + 2);
+                s.w *= xs * __ldcg(a.w_scale + n + 3);
             }
             if (a.r > 0) {
                 const float4 l = *reinterpret_cast<const float4*>(lacc + (q - p0) * kRowsM + lane * 4);

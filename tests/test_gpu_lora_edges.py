@@ -1,4 +1,4 @@
-"""The projection with adapters: infinite weights, against the fp64
+"""The projection with adapters: infinite weights, scales written right before the call, against the fp64
 oracle (tolerance: 64 u of sum |w x|, u = 2^-24, as in test_gpu_block.py)."""
 
 import math
@@ -71,3 +71,37 @@ def test_lora_infinite_adapter_weights(B, T, r, na, x):
     at[mine, 5], at[mine, 250] = True, True
     want[mine, 5], want[mine, 250] = sign * math.inf, -sign * math.inf
     check(y, want, size, at)
+
+
+@pytest.mark.parametrize("T", [3, 128])
+def test_lora_weight_scales_of_the_kernel_before(B, T):
+    """w_scale (and lora's own) written by a copy right before the call, with adapters: what an earlier call
+    left in a cache must not be seen."""
+    g, d, N, r, na = gen(T), 1024, 768, 32, 6
+    x, xs = e4m3(normal(g, T, d, std=100.0)), torch.full((T,), 0.01, device="cuda")
+    w = e4m3(normal(g, N, d, std=100.0))
+    scales = [0.0002 * (1 + torch.rand(N, generator=g, device="cuda")) for _ in range(2)]
+    lscales = [torch.rand(na, generator=g, device="cuda") for _ in range(2)]
+    a, b = normal(g, na, r, d, std=0.05, dtype=torch.bfloat16), normal(g, na, N, r, std=0.05, dtype=torch.bfloat16)
+    ad = torch.randint(-1, na, (T,), generator=g, device="cuda", dtype=torch.int32)
+    ws_, ls = torch.empty(N + 1, device="cuda")[1:], torch.empty(na, device="cuda")     # 4-byte aligned
+    y, ws = torch.empty(T, N, device="cuda"), B.new_lora_workspace(T, d, r)
+
+    def step(i):
+        ws_.copy_(scales[i])
+        ls.copy_(lscales[i])
+        B.moe_lora_project(x, w, y, ws, lora=(a, b, ls), adapter=ad, x_scale=xs, w_scale=ws_)
+
+    want = []
+    for i in range(2):
+        step(i)
+        torch.cuda.synchronize()
+        ref, size = O.lora_project(x, w, (a, b, ls), ad, xs, ws_)
+        assert_within(y, ref, 64 * U * size, "y")
+        want.append(y.clone())
+    got = []
+    for k in range(60):
+        step(k % 2)
+        got.append(y.clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k % 2]) for k in range(60))
