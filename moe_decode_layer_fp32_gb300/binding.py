@@ -467,7 +467,7 @@ def _block_call(name):
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project")
-        mod.bind(*(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check)
+        mod.bind(*(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check, KvCache)
         globals().update({n: getattr(mod, n) for n in names})
         _block = mod
     return getattr(_block, name)

@@ -20,6 +20,7 @@ decltype(&moe_kv_append) g_append = nullptr;
 decltype(&moe_attn_decode) g_attn = nullptr;
 decltype(&moe_lora_project) g_lora = nullptr;
 PyObject* g_on_error = nullptr;      // (name, code) -> raises
+PyTypeObject* g_cache_type = nullptr;
 PyObject* g_address = nullptr;       // "address"
 
 // A ValueError has been set.
@@ -112,12 +113,13 @@ Workspace workspace(PyObject* o) {
 }
 
 const moe_kv_cache* cache_of(PyObject* o) {
+    if (!PyObject_TypeCheck(o, g_cache_type)) refuse("cache: expected a KvCache");
     PyObject* a = PyObject_GetAttr(o, g_address);
     if (!a) throw Refused();
     auto* c = static_cast<const moe_kv_cache*>(PyLong_AsVoidPtr(a));
     Py_DECREF(a);
     if (!c) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "cache: expected a KvCache");
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "cache: no address");
         throw Refused();
     }
     return c;
@@ -334,18 +336,20 @@ PyObject* py_lora(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
     });
 }
 
-// bind(rmsnorm, kv_append, attn_decode, lora_project, on_error): addresses of the library's
-// functions, and what raises for an error code.
+// bind(rmsnorm, kv_append, attn_decode, lora_project, on_error, cache type): addresses of the library's
+// functions, what raises for an error code, and the class of caches.
 PyObject* py_bind(PyObject*, PyObject* args) {
     unsigned long long f[4];
-    PyObject* on_error;
-    if (!PyArg_ParseTuple(args, "KKKKO", &f[0], &f[1], &f[2], &f[3], &on_error)) return nullptr;
+    PyObject *on_error, *cache_type;
+    if (!PyArg_ParseTuple(args, "KKKKOO!", &f[0], &f[1], &f[2], &f[3], &on_error, &PyType_Type, &cache_type)) return nullptr;
     g_rmsnorm = reinterpret_cast<decltype(g_rmsnorm)>(f[0]);
     g_append = reinterpret_cast<decltype(g_append)>(f[1]);
     g_attn = reinterpret_cast<decltype(g_attn)>(f[2]);
     g_lora = reinterpret_cast<decltype(g_lora)>(f[3]);
     Py_INCREF(on_error);
     Py_XSETREF(g_on_error, on_error);
+    Py_INCREF(cache_type);
+    Py_XSETREF(g_cache_type, reinterpret_cast<PyTypeObject*>(cache_type));
     Py_RETURN_NONE;
 }
 
@@ -355,7 +359,7 @@ PyMethodDef kMethods[] = {
     {"moe_kv_append", FAST(py_append), "moe_kv_append of include/moe_block.h"},
     {"moe_attn_decode", FAST(py_attn), "moe_attn_decode of include/moe_block.h"},
     {"moe_lora_project", FAST(py_lora), "moe_lora_project of include/moe_block.h"},
-    {"bind", py_bind, METH_VARARGS, "addresses of the library's functions"},
+    {"bind", py_bind, METH_VARARGS, "addresses of the library's functions, and what they need of Python"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_block_bind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,28 @@
+"""The binding of the decode-block calls on the host (no GPU needed): what it takes for a cache."""
+
+import ctypes as C
+
+import pytest
+import torch
+
+from tests.helpers import ensure_built
+
+
+@pytest.fixture(scope="module")
+def B():
+    return ensure_built()
+
+
+def test_only_a_cache_is_taken_for_one(B):
+    """An object that has an ``address`` of its own is no cache, wherever that points."""
+    class Other:
+        args = B.KvCacheArgs(heads=2, head_dim=64)
+        address = C.addressof(args)
+
+    x = torch.zeros(1, 2, 64)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    for other in (Other(), Other, None, 7):
+        with pytest.raises(ValueError, match="KvCache"):
+            B.moe_kv_append(x, x, other, i, i[0])
+        with pytest.raises(ValueError, match="KvCache"):
+            B.moe_attn_decode(x, other, i, i[0], 1.0, x, i)
