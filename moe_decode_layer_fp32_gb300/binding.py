@@ -449,28 +449,26 @@ def moe_unique_weight_bytes_deamoe(d, n, I_sh, I_pr, I_s, dtype_code, A_d, A_e) 
 
 # The four calls themselves go through the extension module beside the library
 # (csrc/block_bind.cpp), which reads the tensors in C++: a call costs the host less
-# that way than its launch.  Each takes its extension's place at its first use.
+# that way than its launch.
 
 _F32 = torch.float32
 _CODES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
 _block = None
 
 
-def _block_call(name):
-    """The extension's function; binds it to the loaded library the first time."""
+def _load_block():
+    """The extension module, bound to the loaded library (the first call of any of the four)."""
     global _block
-    if _block is None:
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block_bind.so")
-        if not os.path.exists(path):
-            raise ImportError(f"extension module not built: {path} (run __graft_entry__.build())")
-        spec = importlib.util.spec_from_file_location("_block_bind", path)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
-        names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project")
-        mod.bind(*(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check, KvCache)
-        globals().update({n: getattr(mod, n) for n in names})
-        _block = mod
-    return getattr(_block, name)
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block_bind.so")
+    if not os.path.exists(path):
+        raise ImportError(f"extension module not built: {path} (run __graft_entry__.build())")
+    spec = importlib.util.spec_from_file_location("_block_bind", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project")
+    mod.bind(*(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check, KvCache)
+    _block = mod
+    return mod
 
 
 def _want(t, name, shape, dtype):
@@ -488,7 +486,7 @@ def moe_rmsnorm(x, weight, eps: float, y, residual=None, residual_out=None, y_sc
     ``residual_out`` gets x + residual (it may be ``residual`` itself);
     ``weight`` [d] or None; ``y_scale`` goes with an E4M3 ``y``: float32 [T]
     (a scale per row) or [T, d / 128] (per 128 columns)."""
-    _block_call("moe_rmsnorm")(x, weight, eps, y, residual, residual_out, y_scale)
+    (_block or _load_block()).moe_rmsnorm(x, weight, eps, y, residual, residual_out, y_scale)
 
 
 class KvCache:
@@ -520,7 +518,7 @@ def moe_kv_append(k, v, cache: KvCache, block_table, positions, req=None, cos_si
     ``block_table`` int32 [R, pages]; ``positions`` int32 [T]; ``req`` int32 [T]
     or None (token t is request t); ``cos_sin`` float32 [positions, rot] or
     None; ``q_out`` may be ``q``; ``status`` int32 [1] or None."""
-    _block_call("moe_kv_append")(k, v, cache, block_table, positions, req, cos_sin, q, q_out, status)
+    (_block or _load_block()).moe_kv_append(k, v, cache, block_table, positions, req, cos_sin, q, q_out, status)
 
 
 def moe_attn_workspace_bytes(B: int, q_heads: int, heads: int, head_dim: int) -> int:
@@ -542,7 +540,7 @@ def moe_attn_decode(q, cache: KvCache, block_table, seq_lens, scale: float, out,
     """Attention of one new token per request: q, out [B, q_heads, D],
     ``block_table`` int32 [B, pages], ``seq_lens`` int32 [B] (the new token
     included), ``lse`` float32 [B, q_heads] or None."""
-    _block_call("moe_attn_decode")(q, cache, block_table, seq_lens, scale, out, ws, window, softcap, lse)
+    (_block or _load_block()).moe_attn_decode(q, cache, block_table, seq_lens, scale, out, ws, window, softcap, lse)
 
 
 def moe_lora_workspace_bytes(T: int, d: int, r: int) -> int:
@@ -565,4 +563,4 @@ def moe_lora_project(x, w, y, ws, lora=None, adapter=None, x_scale=None, w_scale
 
     x [T, d] float32 or bfloat16 with bfloat16 w [N, d]; or both E4M3 with
     ``x_scale`` float32 [T] and ``w_scale`` float32 [N]."""
-    _block_call("moe_lora_project")(x, w, y, ws, lora, adapter, x_scale, w_scale)
+    (_block or _load_block()).moe_lora_project(x, w, y, ws, lora, adapter, x_scale, w_scale)

@@ -26,3 +26,24 @@ def test_only_a_cache_is_taken_for_one(B):
             B.moe_kv_append(x, x, other, i, i[0])
         with pytest.raises(ValueError, match="KvCache"):
             B.moe_attn_decode(x, other, i, i[0], 1.0, x, i)
+
+
+def test_functions_stay_the_modules_own(B, monkeypatch):
+    """A call leaves the module's functions, their signatures and a caller's patch of one as they are."""
+    import inspect
+
+    names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project")
+    before = {n: getattr(B, n) for n in names}
+    def patch(*args, **kw):
+        return "patched"
+
+    monkeypatch.setattr(B, "moe_kv_append", patch)
+    x = torch.zeros(2, 64)
+    with pytest.raises(ValueError):
+        B.moe_rmsnorm(x, None, 1e-5, x)
+    assert B.moe_kv_append() == "patched"
+    monkeypatch.undo()
+    for n in names:
+        assert getattr(B, n) is before[n] and getattr(B, n).__doc__
+        assert list(inspect.signature(getattr(B, n)).parameters)
+    assert "residual_out" in inspect.signature(B.moe_rmsnorm).parameters
