@@ -499,6 +499,8 @@ class KvCache:
         if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4:
             raise ValueError("k and v must both be [pages, page_size, heads, D], of one dtype")
         pages, page, heads, D = k.shape
+        if max(k.shape) >= 1 << 31:
+            raise ValueError("k and v: a size does not fit 32 bits")
         for name, t in (("k", k), ("v", v)):
             if t.dtype not in _CODES or not t.is_cuda or (t.stride(3) != 1 and D > 1):
                 raise ValueError(f"{name}: expected a CUDA tensor of a supported dtype with contiguous rows")

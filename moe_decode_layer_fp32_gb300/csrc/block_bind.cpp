@@ -41,6 +41,12 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
     return t;
 }
 
+// A size as the C ABI takes it.
+int size32(int64_t n, const char* name) {
+    if (n > INT_MAX) refuse("%s: a size of %lld does not fit 32 bits", name, (long long)n);
+    return (int)n;
+}
+
 int code_of(const at::Tensor& t, const char* name) {
     switch (t.scalar_type()) {
         case at::kFloat: return MOE_DTYPE_F32;
@@ -98,8 +104,8 @@ Table table(PyObject* o) {
     const at::Tensor& t = tensor(o, "block_table");
     if (t.dim() != 2 || t.scalar_type() != at::kInt || (t.size(1) > 1 && t.stride(1) != 1))
         refuse("block_table: expected int32 [requests, pages] with contiguous rows");
-    return {static_cast<const int32_t*>(t.data_ptr()), t.size(0) > 1 ? t.stride(0) : t.size(1), (int)t.size(0),
-            (int)t.size(1)};
+    return {static_cast<const int32_t*>(t.data_ptr()), t.size(0) > 1 ? t.stride(0) : t.size(1),
+            size32(t.size(0), "block_table"), size32(t.size(1), "block_table")};
 }
 
 struct Workspace {
@@ -207,7 +213,7 @@ PyObject* py_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
         sig.parse(args, nargs, kwnames, a);
         const at::Tensor& xt = tensor(a[0], "x");
         if (xt.dim() != 2) refuse("x: expected [T, d]");
-        const int64_t T = xt.size(0), d = xt.size(1);
+        const int T = size32(xt.size(0), "x"), d = size32(xt.size(1), "x");
         const Rows x = rows(a[0], "x", T, d), y = rows(a[3], "y", T, d);
         Rows r = {nullptr, 0, 0}, ro = {nullptr, 0, 0};
         if (given(a[4])) r = rows(a[4], "residual", T, d);
@@ -231,7 +237,7 @@ PyObject* py_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
             }
         }
         return done("moe_rmsnorm", g_rmsnorm(x.p, x.code, x.ld, r.p, r.p ? r.code : ro.code, r.ld, ro.p, ro.ld, w, w_code,
-                                             (float)number(a[2], 0.0), (int)T, (int)d, y.p, y.code, y.ld,
+                                             (float)number(a[2], 0.0), T, d, y.p, y.code, y.ld,
                                              static_cast<float*>(s), group, stream()));
     });
 }
@@ -245,27 +251,27 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject
         const moe_kv_cache* c = cache_of(a[2]);
         const at::Tensor& kt = tensor(a[0], "k");
         if (kt.dim() != 3) refuse("k: expected [T, heads, D]");
-        const int64_t T = kt.size(0), D = c->head_dim;
+        const int T = size32(kt.size(0), "k"), D = c->head_dim;
         const Heads k = heads(a[0], "k", T, c->heads, D), v = heads(a[1], "v", T, c->heads, D);
         if (k.code != v.code) refuse("k and v must have one dtype");
         Heads q = {nullptr, 0, 0, 0}, o = {nullptr, 0, 0, 0};
-        int64_t hq = 0;
+        int hq = 0;
         if (given(a[7]) != given(a[8])) refuse("q and q_out go together");
         if (given(a[7])) {
             const at::Tensor& qt = tensor(a[7], "q");
             if (qt.dim() != 3) refuse("q: expected [T, q_heads, D]");
-            hq = qt.size(1);
+            hq = size32(qt.size(1), "q");
             q = heads(a[7], "q", T, hq, D);
             o = heads(a[8], "q_out", T, hq, D);
             if (q.code != k.code || o.code != k.code) refuse("q, q_out and k must have one dtype");
         }
         const float* cs = nullptr;
-        int64_t max_pos = 0, rot = 0;
+        int max_pos = 0, rot = 0;
         if (given(a[6])) {
             const at::Tensor& t = tensor(a[6], "cos_sin");
             if (t.dim() != 2) refuse("cos_sin: expected [positions, rot]");
-            max_pos = t.size(0);
-            rot = t.size(1);
+            max_pos = size32(t.size(0), "cos_sin");
+            rot = size32(t.size(1), "cos_sin");
             cs = static_cast<const float*>(exactly(a[6], "cos_sin", at::kFloat, {max_pos, rot}));
         }
         const Table t = table(a[3]);
@@ -273,8 +279,8 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject
         auto* req = static_cast<const int32_t*>(exactly(a[5], "req", at::kInt, {T}));
         auto* st = static_cast<int32_t*>(exactly(a[9], "status", at::kInt, {1}));
         return done("moe_kv_append",
-                    g_append(k.p, k.outer, k.inner, v.p, v.outer, v.inner, k.code, (int)T, c, t.p, t.ld, t.R, t.pages, pos, req,
-                             cs, (int)rot, (int)max_pos, q.p, q.outer, q.inner, o.p, o.outer, o.inner, (int)hq, st, stream()));
+                    g_append(k.p, k.outer, k.inner, v.p, v.outer, v.inner, k.code, T, c, t.p, t.ld, t.R, t.pages, pos, req,
+                             cs, rot, max_pos, q.p, q.outer, q.inner, o.p, o.outer, o.inner, hq, st, stream()));
     });
 }
 
@@ -287,7 +293,7 @@ PyObject* py_attn(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
         const moe_kv_cache* c = cache_of(a[1]);
         const at::Tensor& qt = tensor(a[0], "q");
         if (qt.dim() != 3) refuse("q: expected [B, q_heads, D]");
-        const int64_t B = qt.size(0), hq = qt.size(1), D = c->head_dim;
+        const int B = size32(qt.size(0), "q"), hq = size32(qt.size(1), "q"), D = c->head_dim;
         const Heads q = heads(a[0], "q", B, hq, D), o = heads(a[5], "out", B, hq, D);
         const Table t = table(a[2]);
         if (t.R != B) refuse("block_table must have a row per request");
@@ -295,7 +301,7 @@ PyObject* py_attn(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
         auto* lse = static_cast<float*>(exactly(a[9], "lse", at::kFloat, {B, hq}));
         const Workspace ws = workspace(a[6]);
         return done("moe_attn_decode",
-                    g_attn(q.p, q.code, q.outer, q.inner, (int)B, (int)hq, c, t.p, t.ld, t.pages, lens, (float)number(a[4], 0.0),
+                    g_attn(q.p, q.code, q.outer, q.inner, B, hq, c, t.p, t.ld, t.pages, lens, (float)number(a[4], 0.0),
                            integer(a[7], 0), (float)number(a[8], 0.0), o.p, o.code, o.outer, o.inner, lse, ws.p, ws.bytes,
                            stream()));
     });
@@ -308,17 +314,17 @@ PyObject* py_lora(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
         sig.parse(args, nargs, kwnames, a);
         const at::Tensor &xt = tensor(a[0], "x"), &wt = tensor(a[1], "w");
         if (xt.dim() != 2 || wt.dim() != 2) refuse("x must be [T, d] and w [N, d]");
-        const int64_t T = xt.size(0), d = xt.size(1), N = wt.size(0);
+        const int T = size32(xt.size(0), "x"), d = size32(xt.size(1), "x"), N = size32(wt.size(0), "w");
         const Rows x = rows(a[0], "x", T, d), w = rows(a[1], "w", N, d), y = rows(a[2], "y", T, N);
         void *la = nullptr, *lb = nullptr, *ls = nullptr, *ad = nullptr;
-        int64_t n = 0, r = 0;
+        int n = 0, r = 0;
         if (given(a[4])) {
             if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 3) refuse("lora: expected a tuple (A, B, scale)");
             PyObject* A = PyTuple_GET_ITEM(a[4], 0);
             const at::Tensor& at_ = tensor(A, "lora A");
             if (at_.dim() != 3) refuse("lora A: expected [adapters, r, d]");
-            n = at_.size(0);
-            r = at_.size(1);
+            n = size32(at_.size(0), "lora A");
+            r = size32(at_.size(1), "lora A");
             la = exactly(A, "lora A", at::kBFloat16, {n, r, d});
             lb = exactly(PyTuple_GET_ITEM(a[4], 1), "lora B", at::kBFloat16, {n, N, r});
             ls = exactly(PyTuple_GET_ITEM(a[4], 2), "lora scale", at::kFloat, {n});
@@ -330,8 +336,8 @@ PyObject* py_lora(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
         auto* wsc = static_cast<const float*>(exactly(a[7], "w_scale", at::kFloat, {N}));
         const Workspace ws = workspace(a[3]);
         return done("moe_lora_project",
-                    g_lora(x.p, x.code, x.ld, xs, (int)T, (int)d, w.p, w.code, w.ld, wsc, (int)N, la, lb,
-                           static_cast<const float*>(ls), (int)n, (int)r, static_cast<const int32_t*>(ad), y.p, y.code, y.ld,
+                    g_lora(x.p, x.code, x.ld, xs, T, d, w.p, w.code, w.ld, wsc, N, la, lb,
+                           static_cast<const float*>(ls), n, r, static_cast<const int32_t*>(ad), y.p, y.code, y.ld,
                            ws.p, ws.bytes, stream()));
     });
 }
