@@ -506,10 +506,11 @@ class KvCache:
                 raise ValueError(f"{name}: expected a CUDA tensor of a supported dtype with contiguous rows")
         self.tensors = (k, v, k_scale, v_scale)
         self.heads, self.head_dim, self.page_size = heads, D, page
+        # the stride of a single page, slot or head means nothing
+        strides = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in range(3)]
         self.args = KvCacheArgs(
             k.data_ptr(), v.data_ptr(), _want(k_scale, "k_scale", (heads,), _F32),
-            _want(v_scale, "v_scale", (heads,), _F32), *k.stride()[:3], *v.stride()[:3], _CODES[k.dtype],
-            pages, page, heads, D)
+            _want(v_scale, "v_scale", (heads,), _F32), *strides, _CODES[k.dtype], pages, page, heads, D)
         self.address = C.addressof(self.args)
 
 

@@ -75,13 +75,13 @@ struct Heads {
     int code;
     int64_t outer, inner;
 };
-// [T, heads, D] with contiguous rows.
+// [T, heads, D] with contiguous rows (the stride of a single token or head means nothing).
 Heads heads(PyObject* o, const char* name, int64_t T, int64_t h, int64_t D) {
     const at::Tensor& t = tensor(o, name);
     if (t.dim() != 3 || t.size(0) != T || t.size(1) != h || t.size(2) != D)
         refuse("%s: expected shape [%lld, %lld, %lld]", name, (long long)T, (long long)h, (long long)D);
     if (t.stride(2) != 1 && D != 1) refuse("%s: expected contiguous rows", name);
-    return {t.data_ptr(), code_of(t, name), t.stride(0), t.stride(1)};
+    return {t.data_ptr(), code_of(t, name), T > 1 ? t.stride(0) : h * D, h > 1 ? t.stride(1) : D};
 }
 
 // A contiguous tensor of this type and shape; None is nullptr.

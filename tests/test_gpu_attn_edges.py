@@ -191,3 +191,34 @@ def test_attn_fp32_keeps_its_digits(B, dtype):
     want, wl = c.want()
     assert (want > 0).all()
     assert_within(o, want, 2.0 ** -18 * want, "out")
+
+
+def test_attn_views_with_a_size_of_one(B):
+    """The stride of a dimension of size one means nothing."""
+    g = gen(6)
+    # one request out of a wider, odd row; one head of an odd number of elements in between
+    wide = normal(g, 4 * 64 + 3, dtype=torch.bfloat16)
+    for q in (wide[:256].as_strided((1, 4, 64), (259, 64, 1)), normal(g, 3, 1, 64, dtype=torch.bfloat16).as_strided((3, 1, 64), (64, 77, 1))):
+        nb, hq, _ = q.shape
+        kb, vb = normal(g, 8, 16, 1, 64, dtype=torch.bfloat16), normal(g, 8, 16, 1, 64, dtype=torch.bfloat16)
+        odd = [t.as_strided((8, 16, 1, 64), (16 * 64, 64, 13, 1)) for t in (kb, vb)]
+        cache = B.KvCache(*odd)
+        table = torch.arange(2 * nb, dtype=torch.int32, device="cuda").view(nb, 2)
+        seq = torch.full((nb,), 27, dtype=torch.int32, device="cuda")
+        o = torch.empty(nb * hq * 64 + 8, dtype=torch.bfloat16, device="cuda")[:nb * hq * 64].as_strided(q.shape, q.stride())
+        B.moe_attn_decode(q, cache, table, seq, 0.125, o, B.new_attn_workspace(nb, hq, 1, 64))
+        for b in range(nb):
+            rk, rv = (O.cached_rows(t, None, table[b], 0, 27) for t in (kb, vb))
+            want, _ = O.decode_attention(q[b], (rk, rv), 0.125)
+            assert_within(o[b], want, bound_of(want, o.dtype, rv.abs().max().item()), f"request {b}")
+    # a cache of one page, and one of pages of one slot
+    for shape, strides in (((1, 16, 2, 64), (5, 128, 64, 1)), ((16, 1, 2, 64), (128, 3, 64, 1))):
+        kb, vb = normal(g, 16 * 128, dtype=torch.bfloat16), normal(g, 16 * 128, dtype=torch.bfloat16)
+        k, v = kb.as_strided(shape, strides), vb.as_strided(shape, strides)
+        table = torch.arange(shape[0], dtype=torch.int32, device="cuda").view(1, -1)
+        q, o = normal(g, 1, 2, 64), torch.empty(1, 2, 64, device="cuda")
+        B.moe_attn_decode(q, B.KvCache(k, v), table, torch.tensor([11], dtype=torch.int32, device="cuda"), 0.125, o,
+                          B.new_attn_workspace(1, 2, 2, 64))
+        rows = [O.f64(t).view(16, 2, 64)[:11] for t in (kb, vb)]
+        want, _ = O.decode_attention(q[0], rows, 0.125)
+        assert_within(o[0], want, bound_of(want, o.dtype, rows[1].abs().max().item()), str(shape))

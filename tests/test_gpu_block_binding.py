@@ -1,10 +1,12 @@
-"""What the binding of the decode-block calls does with sizes beyond 32 bits, on the GPU."""
+"""What the binding of the decode-block calls does with sizes beyond 32 bits and with tensors of more than
+one layout, on the GPU."""
 
 import pytest
 import torch
 
+from oracle import block_oracle as O
 from tests.helpers import ensure_built
-from tests.test_gpu_block import gen, make_cache
+from tests.test_gpu_block import assert_within, cos_sin_table, gen, make_cache, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +31,20 @@ def test_sizes_beyond_32_bits_are_refused(B):
         B.moe_kv_append(row, row, cache, table, numbers, req=numbers)
     with pytest.raises(ValueError, match="32 bits"):
         B.moe_attn_decode(row, cache, table.expand(n, 2), numbers, 0.125, row, B.new_attn_workspace(1, 2, 2, 64))
+
+
+def test_append_views_with_a_size_of_one(B):
+    """One token, or one head, whose meaningless stride is no multiple of 8."""
+    g = gen(2)
+    for shape, strides in (((1, 2, 64), (133, 64, 1)), ((3, 1, 64), (64, 9, 1))):
+        T, hkv, D = shape
+        k, v, _, _, cache = make_cache(B, g, 6, 4, hkv, D, "bf16", fill=0)
+        kn, vn, q, qo = (normal(g, T * hkv * D, dtype=torch.bfloat16).as_strided(shape, strides) for _ in range(4))
+        table = torch.arange(6, dtype=torch.int32, device="cuda")[:2 * T].view(T, 2)
+        pos = torch.tensor([5, 0, 7][:T], dtype=torch.int32, device="cuda")
+        B.moe_kv_append(kn, vn, cache, table, pos, cos_sin=cos_sin_table(8, 64), q=q, q_out=qo)
+        want = O.rotate(q, pos, cos_sin_table(8, 64))
+        assert_within(qo, want, 1e-5 + 1.01 * 2.0 ** -8 * want.abs(), "q")
+        for t in range(T):
+            p, i = O.slot_of(table, t, int(pos[t]), 4)
+            assert torch.equal(v[p, i], vn[t])
