@@ -2,7 +2,8 @@
 
 Each CUDA translation unit is compiled to an object in parallel, then linked
 into one shared library next to this file; beside it goes the extension module
-that hands torch tensors to the decode-block calls.  Objects are rebuilt only when a
+that hands torch tensors to the decode-block calls, where torch, g++ and Python's
+headers are there (the library needs none of them).  Objects are rebuilt only when a
 source or header is newer.  Set ``MOE_PTXAS_VERBOSE=1`` to print register and
 shared-memory use per kernel.
 """
@@ -61,13 +62,23 @@ def _run(cmd):
 
 
 def _bind_command():
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-    inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
-    lib = os.path.join(torch, "lib")
+    """(command, None) of the extension module, or (None, what it lacks on this machine)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None, "torch"
+    torch = os.path.dirname(spec.origin)
+    include, lib, python = os.path.join(torch, "include"), os.path.join(torch, "lib"), sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "c10", "cuda", "CUDAStream.h")):
+        return None, "a torch with CUDA"
+    if shutil.which("g++") is None:
+        return None, "g++"
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        return None, "Python's headers"
+    inc = [INCLUDE, include, os.path.join(include, "torch", "csrc", "api", "include"), python,
+           os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "block_bind.cpp"), "-o", BIND]
             + [a for i in inc for a in ("-I", i)]
-            + ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"])
+            + ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]), None
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -84,18 +95,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
         o = os.path.join(OBJDIR, src.replace(".cu", ".o"))
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, "-c", s, "-o", o] + flags)
-    compiled = list(jobs)
+    bind = None
     if force or _stale(BIND, [os.path.join(CSRC, "block_bind.cpp")] + [
             os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]):
-        jobs.append(_bind_command())
-    if jobs:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            for out in ex.map(_run, jobs):
-                if verbose or os.environ.get("MOE_PTXAS_VERBOSE"):
-                    sys.stdout.write(out)
+        bind, lacks = _bind_command()
+        if bind is None:
+            print(f"decode-block calls not built: no {lacks}", file=sys.stderr)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        extension = ex.submit(_run, bind) if bind else None
+        for out in ex.map(_run, jobs):
+            if verbose or os.environ.get("MOE_PTXAS_VERBOSE"):
+                sys.stdout.write(out)
+    # the library needs nothing of the extension's, whose failure comes after it
     objs = [os.path.join(OBJDIR, s.replace(".cu", ".o")) for s in SOURCES]
-    if force or compiled or _stale(LIB, objs):
+    if force or jobs or _stale(LIB, objs):
         _run([nvcc, "-shared", "-cudart", "shared"] + ARCH + objs + ["-o", LIB])
+    if extension:
+        extension.result()
     return LIB
 
 
