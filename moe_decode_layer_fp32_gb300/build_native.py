@@ -4,7 +4,7 @@ Each CUDA translation unit is compiled to an object in parallel, then linked
 into one shared library next to this file; beside it goes the extension module
 that hands torch tensors to the decode-block calls, where torch, g++ and Python's
 headers are there (the library needs none of them).  Objects are rebuilt only when a
-source or header is newer.  Set ``MOE_PTXAS_VERBOSE=1`` to print register and
+source or header is newer, the extension also for another torch.  Set ``MOE_PTXAS_VERBOSE=1`` to print register and
 shared-memory use per kernel.
 """
 
@@ -81,6 +81,20 @@ def _bind_command():
             + ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]), None
 
 
+def _read(path: str):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _bind_stamp(cmd) -> str:
+    """What the extension was built by and against: a torch of another version has another C++ ABI."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    return " ".join(cmd) + "\n" + (_read(os.path.join(torch, "version.py")) or "")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = nvcc_path()
     os.makedirs(OBJDIR, exist_ok=True)
@@ -95,12 +109,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         o = os.path.join(OBJDIR, src.replace(".cu", ".o"))
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, "-c", s, "-o", o] + flags)
-    bind = None
-    if force or _stale(BIND, [os.path.join(CSRC, "block_bind.cpp")] + [
-            os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]):
-        bind, lacks = _bind_command()
-        if bind is None:
-            print(f"decode-block calls not built: no {lacks}", file=sys.stderr)
+    bind, lacks = _bind_command()
+    if bind is None:
+        print(f"decode-block calls not built: no {lacks}", file=sys.stderr)
+    else:
+        stamp_path, stamp = os.path.join(OBJDIR, "block_bind.stamp"), _bind_stamp(bind)
+        if not force and _read(stamp_path) == stamp and not _stale(BIND, [os.path.join(CSRC, "block_bind.cpp")] + [
+                os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]):
+            bind = None
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
         extension = ex.submit(_run, bind) if bind else None
         for out in ex.map(_run, jobs):
@@ -112,6 +128,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         _run([nvcc, "-shared", "-cudart", "shared"] + ARCH + objs + ["-o", LIB])
     if extension:
         extension.result()
+        with open(stamp_path, "w") as f:
+            f.write(stamp)
     return LIB
 
 

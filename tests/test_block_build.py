@@ -51,3 +51,25 @@ def test_a_failing_extension_leaves_the_library(fake):
     with pytest.raises(RuntimeError, match="command failed"):
         N.build()
     assert os.path.exists(N.LIB)
+
+
+def test_another_torch_rebuilds_the_extension(fake, monkeypatch, tmp_path):
+    """Only the extension, and only when torch's version, its place or the command changed."""
+    torch = tmp_path / "torch"
+    for f in ("include/c10/cuda/CUDAStream.h", "__init__.py", "version.py"):
+        (torch / f).parent.mkdir(parents=True, exist_ok=True)
+        (torch / f).write_text("__version__ = '1'")
+    find = N.importlib.util.find_spec
+    spec = type("Spec", (), {"origin": str(torch / "__init__.py")})
+    monkeypatch.setattr(N.importlib.util, "find_spec", lambda n, *a: spec if n == "torch" else find(n, *a))
+    N.build()
+    fake.ran.clear()
+    N.build()
+    assert fake.ran == []
+    (torch / "version.py").write_text("__version__ = '2'")
+    os.utime(torch / "version.py", (0, 0))          # installed files may be older than the build
+    N.build()
+    assert [c[0] for c in fake.ran] == ["g++"]
+    fake.ran.clear()
+    N.build()
+    assert fake.ran == []
