@@ -143,14 +143,11 @@ def _ptr(t):
     return t.data_ptr()
 
 
-# The current device's current stream as a pointer.  The same value as
-# torch.cuda.current_stream().cuda_stream without building a Stream object,
-# which took longer than the launch itself (2.9 of 3.8 us on a Grace host).
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
 def _stream():
-    return _raw_stream(_current_device())
+    """The current device's current stream as a pointer: the value of
+    torch.cuda.current_stream().cuda_stream without building a Stream object,
+    which took longer than the launch itself (2.9 of 3.8 us on a Grace host)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_code(t) -> int:

@@ -47,3 +47,18 @@ def test_functions_stay_the_modules_own(B, monkeypatch):
         assert getattr(B, n) is before[n] and getattr(B, n).__doc__
         assert list(inspect.signature(getattr(B, n)).parameters)
     assert "residual_out" in inspect.signature(B.moe_rmsnorm).parameters
+
+
+def test_import_without_cuda_in_torch(B):
+    """The binding imports, and calls that need no stream work, on a torch without CUDA's private names."""
+    import subprocess
+    import sys
+
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "from moe_decode_layer_fp32_gb300 import binding as B\n"
+            "print(B.moe_lora_workspace_bytes(2, 64, 16))\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert int(r.stdout) == B.moe_lora_workspace_bytes(2, 64, 16)
