@@ -46,6 +46,12 @@ class KvCacheArgs(C.Structure):
                 + [(f, C.c_int) for f in ("dtype", "num_pages", "page_size", "heads", "head_dim")])
 
 
+class KvCacheHandle(C.Structure):
+    """``moe_kv_cache`` and the device that it is on, as the extension module reads them."""
+
+    _fields_ = [("args", KvCacheArgs), ("device", C.c_int)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, code: int, msg: str):
         super().__init__(f"{fn} failed: {ERRORS.get(code, code)}: {msg}")
@@ -501,14 +507,18 @@ class KvCache:
         for name, t in (("k", k), ("v", v)):
             if t.dtype not in _CODES or not t.is_cuda or (t.stride(3) != 1 and D > 1):
                 raise ValueError(f"{name}: expected a CUDA tensor of a supported dtype with contiguous rows")
+        if any(t is not None and t.device != k.device for t in (v, k_scale, v_scale)):
+            raise ValueError("k, v and their scales must be on one device")
         self.tensors = (k, v, k_scale, v_scale)
         self.heads, self.head_dim, self.page_size = heads, D, page
         # the stride of a single page, slot or head means nothing
         strides = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in range(3)]
-        self.args = KvCacheArgs(
+        self.handle = KvCacheHandle(KvCacheArgs(
             k.data_ptr(), v.data_ptr(), _want(k_scale, "k_scale", (heads,), _F32),
-            _want(v_scale, "v_scale", (heads,), _F32), *strides, _CODES[k.dtype], pages, page, heads, D)
-        self.address = C.addressof(self.args)
+            _want(v_scale, "v_scale", (heads,), _F32), *strides, _CODES[k.dtype], pages, page, heads, D),
+            k.get_device())
+        self.args = self.handle.args
+        self.address = C.addressof(self.handle)
 
 
 def moe_kv_append(k, v, cache: KvCache, block_table, positions, req=None, cos_sin=None, q=None, q_out=None,

@@ -8,6 +8,7 @@
 // code goes to the Python function given there, which raises.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -34,10 +35,18 @@ struct Refused {};
     throw Refused();
 }
 
+// What a call reads and writes has to be on the current device, on whose stream it runs.
+thread_local int t_device;           // -1: not asked yet in this call
+void check_device(int device, const char* name) {
+    if (t_device < 0) t_device = c10::cuda::current_device();
+    if (device != t_device) refuse("%s: on device %d, but the current one is %d", name, device, t_device);
+}
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) refuse("%s: expected a tensor", name);
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) refuse("%s: expected a CUDA tensor", name);
+    check_device(t.get_device(), name);
     return t;
 }
 
@@ -118,17 +127,22 @@ Workspace workspace(PyObject* o) {
     return {t.data_ptr(), t.nbytes()};
 }
 
+struct CacheHandle {                 // KvCacheHandle of binding.py
+    moe_kv_cache cache;
+    int device;
+};
 const moe_kv_cache* cache_of(PyObject* o) {
     if (!PyObject_TypeCheck(o, g_cache_type)) refuse("cache: expected a KvCache");
     PyObject* a = PyObject_GetAttr(o, g_address);
     if (!a) throw Refused();
-    auto* c = static_cast<const moe_kv_cache*>(PyLong_AsVoidPtr(a));
+    auto* c = static_cast<const CacheHandle*>(PyLong_AsVoidPtr(a));
     Py_DECREF(a);
     if (!c) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "cache: no address");
         throw Refused();
     }
-    return c;
+    check_device(c->device, "cache");
+    return &c->cache;
 }
 
 double number(PyObject* o, double otherwise) {
@@ -197,6 +211,7 @@ PyObject* done(const char* name, int rc) {
 // Runs f; what it throws becomes a Python exception.
 template <class F>
 PyObject* guarded(F f) {
+    t_device = -1;
     try {
         return f();
     } catch (const Refused&) {

@@ -48,3 +48,15 @@ def test_append_views_with_a_size_of_one(B):
         for t in range(T):
             p, i = O.slot_of(table, t, int(pos[t]), 4)
             assert torch.equal(v[p, i], vn[t])
+
+
+def test_a_cache_of_another_device_is_refused(B):
+    """What a call reads is on the current device, whose stream it takes."""
+    _, _, _, _, cache = make_cache(B, gen(0), 2, 16, 2, 64, "bf16")
+    x, i = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    B.moe_kv_append(x, x, cache, i, i[0])
+    cache.handle.device += 1          # as of a cache on the next GPU
+    with pytest.raises(ValueError, match="device"):
+        B.moe_kv_append(x, x, cache, i, i[0])
+    with pytest.raises(ValueError, match="device"):
+        B.moe_attn_decode(x, cache, i, i[0], 1.0, x, B.new_attn_workspace(1, 2, 2, 64))
