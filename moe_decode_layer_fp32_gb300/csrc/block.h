@@ -107,6 +107,27 @@ inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>
     return e;
 }
 
+// Blocks of a kernel that an SM holds.  The runtime is asked once per device, threads and shared memory:
+// `last` is the kernel's own, 0 or the last question (24 bits of shared memory, 12 of threads, 12 of
+// device + 1) and its answer.
+inline cudaError_t blocks_per_sm(const void* kern, int threads, size_t smem, std::atomic<uint64_t>& last, int* blocks) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t asked = (uint64_t)smem << 40 | (uint64_t)threads << 28 | (uint64_t)(dev + 1) << 16;
+    const uint64_t have = last.load(std::memory_order_relaxed);
+    if ((have & ~(uint64_t)0xffff) == asked) {
+        *blocks = (int)(have & 0xffff);
+        return cudaSuccess;
+    }
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, kern, threads, smem);
+    if (e == cudaSuccess) {
+        *blocks = *blocks > 0 ? *blocks : 1;
+        last.store(asked | (uint64_t)*blocks, std::memory_order_relaxed);
+    }
+    return e;
+}
+
 // Launch configuration of a programmatic dependent: the kernel may start
 // before the one ahead of it on the stream has ended, and waits for it
 // (griddepcontrol.wait) before it reads anything that one may have written.

@@ -271,12 +271,12 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s) {
         if (smem <= (size_t)kAppendSmem || nq + nkv <= 2) break;
     }
     auto kern = bf ? kv_append_kernel<true> : kv_append_kernel<false>;
-    static std::atomic<uint64_t> done[2];
+    static std::atomic<uint64_t> done[2], blocks[2];
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kAppendSmem, done[bf]);
     int per_sm = 0;
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kAppendThreads, smem);
+    if (e == cudaSuccess) e = blocks_per_sm(reinterpret_cast<const void*>(kern), kAppendThreads, smem, blocks[bf], &per_sm);
     if (e != cudaSuccess) return e;
-    const int grid = std::min(a.T * slices, std::max(1, per_sm) * sms);
+    const int grid = std::min(a.T * slices, per_sm * sms);
     return launch_pdl(kern, dim3((unsigned)grid), dim3(kAppendThreads), smem, s, a, slices, nq, nkv);
 }
 

@@ -218,12 +218,12 @@ cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
     size_t smem = 0;
     if (WALK) {
         smem = (size_t)CH * threads * ((x ? 16 : 32) + (a.residual ? r ? 16 : 32 : 0));
-        static std::atomic<uint64_t> done[4];
+        static std::atomic<uint64_t> done[4], blocks[4];
         cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 224 * 1024, done[2 * x + r]);
         int per_sm = 0;
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+        if (e == cudaSuccess) e = blocks_per_sm(reinterpret_cast<const void*>(kern), threads, smem, blocks[2 * x + r], &per_sm);
         if (e != cudaSuccess) return e;
-        grid = std::min(grid, std::max(1, per_sm) * device_sm_count());
+        grid = std::min(grid, per_sm * device_sm_count());
     }
     return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)threads), smem, s, a);
 }
