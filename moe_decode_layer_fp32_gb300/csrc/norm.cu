@@ -21,7 +21,7 @@ namespace moe {
 namespace {
 
 constexpr int kWalkThreads = 512;    // most threads of a block that walks over rows
-constexpr float kFewest = 0x1p-100f; // maxima and scales from here to its reciprocal are divided by directly
+constexpr float kFewest = 0x1p-50f;  // 448 is divided directly by maxima from here to its reciprocal
 
 template <bool BF>
 __device__ __forceinline__ void raw8(const char* p, float2 (&f)[4]) {
@@ -159,17 +159,19 @@ __global__ void __launch_bounds__(WALK ? kWalkThreads : 1024, !WALK ? 1 : CH <= 
         const float rstd = r0 > 0.0f ? r0 * fmaf(-0.5f * v * r0, r0, 1.5f) : r0;
         // E4M3: with m = max |z w|, the scale is m rstd / 448 and a code z w rstd / scale =
         // z w (448 / m): within 3 ulp of the division, which moves a code only next to a tie.  Where
-        // m or the scale is so far from 1 that 448 / m, or the few bits of a subnormal scale, would not do, z w is
-        // brought near 1 by a power of two and divided by the scale as stored.  A scale that is 0 in fp32 becomes 1.
+        // m is so far from 1 that 448 / m, or the few bits of a subnormal scale, might not do, z w is brought
+        // near 1 by a power of two and divided by the scale as stored.  A scale that is 0 in fp32 becomes 1.
         float up = rstd, near_one = 1.0f;
+        // m in [kFewest, 1 / kFewest) as one unsigned comparison of its bits; none where rstd is 0 or NaN
+        const uint32_t plain = rstd >= kFewest * kFewest ? __float_as_uint(1.0f / kFewest) - __float_as_uint(kFewest) : 0u;
         auto scale_of = [&](float m, float* out, bool mine) {
             float s = over_448(m * rstd);
             up = rstd;
             near_one = 1.0f;
-            if (m >= kFewest && m <= 1.0f / kFewest && s >= kFewest) {
+            if (__float_as_uint(m) - __float_as_uint(kFewest) < plain) {
                 up = __fdividef(448.0f, m);
             } else if (s > 0.0f) {
-                near_one = m > 1.0f ? kFewest : 1.0f / kFewest;
+                near_one = m > 1.0f ? 0x1p-100f : 0x1p100f;
                 up = rstd / (s * near_one);
             } else {
                 s = 1.0f;        // also beside a NaN
