@@ -74,7 +74,8 @@ int moe_rmsnorm(const void* x, int x_dtype, int64_t x_ld, const void* residual, 
  * and the same for v.  BF16, or E4M3 with one fp32 scale per head (a value is
  * scale[h] * e4m3(code)); k_scale and v_scale are NULL for BF16.
  * Limits: head_dim a multiple of 8 (16 for E4M3) up to 256; pages of any size
- * >= 1; k and v 16-byte aligned, strides multiples of 16 bytes.
+ * >= 1; k and v 16-byte aligned, strides multiples of 16 bytes; scales positive,
+ * from 2^-126 to 2^126.
  */
 typedef struct moe_kv_cache {
     void* k;
@@ -105,7 +106,7 @@ typedef struct moe_kv_cache {
  * A token of negative position is padding: nothing is written for it but a
  * copy of its q.  A token whose request is outside [0, R), whose position has no
  * page in the table or no row in cos_sin, or whose page is outside the cache
- * is dropped (status).  Two tokens of one slot: either may win.
+ * is dropped (status).  Two tokens of one slot: its row may mix theirs.
  * Limits: rot even, 0 <= rot <= D.
  */
 int moe_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,

@@ -22,11 +22,17 @@
 // more at no cost in MMAs; bf16 queries over an E4M3 cache as two E4M3 terms.
 //
 // Measured: 1 x 131071 keys of 8 heads of 128, bf16 (537 MB) 87 us, 6.1 TB/s; 128
-// requests of 1 to 4096 keys, bf16 140 us, 6.2 TB/s, and E4M3 94 us, 4.7 TB/s: there the
-// instructions bound it, about 750 for a warp's 32 keys at 0.35 a clock and scheduler (105 us with
-// a mask or shift more per conversion).  Two CTAs per SM with a ring of three stages beat
-// three with two (64 x 2048 keys: bf16 91 and 98 us, E4M3 58 and 66) and tiles of 16 keys
-// (E4M3 69).
+// requests of 1 to 4096 keys, bf16 137 us, 6.3 TB/s, and E4M3 95 us, 4.6 TB/s: there the
+// chains of dependent instructions bound it, about 750 for a warp's 32 keys, which a scheduler's two
+// warps (255 registers each) issue at 0.35 a clock (105 us with a mask or shift more per conversion).
+// Two CTAs per SM with a ring of three stages beat three with two (64 x 2048 keys: bf16 91 and 98 us,
+// E4M3 58 and 66) and tiles of 16 keys (E4M3 69).
+//
+// Beyond 128 columns o, the scores and q do not fit the registers (120 to 970 bytes of spills) and a bf16
+// cache leaves one CTA to an SM: 64 x 2048 keys of 4 heads of 256, 16 query heads, bf16 105 us (75 % of
+// the cache's bytes at the copy rate), fp32 q 271, over E4M3 93 and 73.  More than 8 query heads of a key-value head
+// are one unit of 16 rows up to 128 columns without extra terms; otherwise every 8 of them are a unit of
+// their own and read the keys again: 64 / 4 heads of 128, bf16 54 us, fp32 q 92, over E4M3 49 and 59.
 #include <algorithm>
 
 #include <math_constants.h>
@@ -42,8 +48,9 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnMaxCtas = 320;          // bounds the workspace
 constexpr int kJoinMost = 24;              // parts joined by one CTA; more go in groups of kJoinGroup first
 constexpr int kJoinGroup = 16;
-// What a tile and the beginning and end of a unit cost.  Unit costs of 1, 3, 5 and 8: 155, 137, 137, 137 us
-// for 128 ragged bf16 requests, 131, 108, 110, 115 for E4M3.
+// What a tile and the beginning and end of a unit cost.  Unit costs of 1, 3, 5 and 8: 204, 137, 136, 136 us
+// for 128 ragged bf16 requests in order of length, 134, 92, 94, 98 for E4M3 with a cap, 10.2, 10.1, 10.8,
+// 12.0 for one request of 777 keys.
 constexpr int kTileCost = 2, kUnitCost = 3;
 // The fast tanh is off by 2^-22 of the cap: up to 256, 2^-14 of a weight, where a bf16 output is rounded to
 // 2^-9.  Larger caps take the kernel of fp32 outputs, with tanhf (64 x 2048 keys, bf16 91 and 94 us, E4M3 60
@@ -581,10 +588,7 @@ struct Attn {
                     float (&acc)[4] = EX ? fresh[EX ? e : 0] : st.o[w * kVElems + e];
                     if constexpr (ROWS == 16) {
                         mma(acc, p0[0], p0[1], p0b[0], p0b[1], b[0], b[1]);
-                        if constexpr (kPTerms == 2)
-                            mma(acc, pf[1][2 * kg][0], pf[1][2 * kg][1], pf[1][2 * kg + 1][0], pf[1][2 * kg + 1][1], b[0], b[1]);
-                    } else if constexpr (kPTerms == 1) {
-                        mma(acc, p0[0], 0u, p0b[0], 0u, b[0], b[1]);
+                        mma(acc, pf[1][2 * kg][0], pf[1][2 * kg][1], pf[1][2 * kg + 1][0], pf[1][2 * kg + 1][1], b[0], b[1]);
                     } else {
                         mma(acc, p0[0], pf[1][2 * kg][0], p0b[0], pf[1][2 * kg + 1][0], b[0], b[1]);
                         // third terms beside the second ones; the least bf16 instead of 0 leaves the first

@@ -2,7 +2,7 @@
 // read pointers, types, sizes and strides from the tensors, check that they fit one
 // another, and call the C ABI on the current stream.  A decode step makes such a call
 // every few microseconds; the same marshalling through ctypes took 7 to 12 us a
-// call on the GB300's host, and takes 3 to 5 here, most of it the launch.
+// call on the GB300's host, and takes 2.7 to 3.1 here, most of it the launch.
 //
 // The functions' addresses come from the loaded library (bind()), and a call's error
 // code goes to the Python function given there, which raises.

@@ -20,7 +20,7 @@
 // tokens by adapter and fetches W and B.  128 rows of B_a come once for all tokens of the
 // adapter, and four warps multiply 32 of them each with v beside the MMAs of W: all
 // four on one tile, so that its place in the ring is free again sooner (an adapter to
-// a warp took 337 us where this takes 170: 128 tokens, 128 adapters of rank 128).  A
+// a warp took 337 us where this takes 160: 128 tokens, 128 adapters of rank 128).  A
 // token meets no weights but its own adapter's, whatever the others hold.
 //
 // Measured (without adapters): 16 to 32 tokens of 7168 -> 9216, bf16 (132 MB) 23.7 us, 5.6 TB/s,
