@@ -27,7 +27,7 @@
 // 128 tokens 26.6 us; 128 tokens of 7168 -> 7168 E4M3 (51 MB) 16 us.  The stream of W alone takes
 // 22 us of the first; what the issuing warp does for a 128-byte block between two waits bounds the
 // rest (with a division for the place in the ring, and one lane instead of a uniform warp, 26.7 us).
-// With 64 adapters of rank 64 (58 MB each of A and B) the third takes 42 us, 14 of them A x.
+// With 64 adapters of rank 64 (58 MB each of A and B) the third takes 44 us, 14 of them A x.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -679,10 +679,13 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
     tc_fence_after_sync();
 
     // ---- the cluster's sum of this CTA's tokens, scales, adapter part, output
-    const int warps = kProjThreads / 32;
+    const int warps = kProjThreads / 32, n = n0 + lane * 4;
+    float4 wsc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (F8) {
+        if (n < a.N) wsc = make_float4(__ldcg(a.w_scale + n), __ldcg(a.w_scale + n + 1), __ldcg(a.w_scale + n + 2), __ldcg(a.w_scale + n + 3));
+    }
     for (int q = p0 + warp; q < p1; q += warps) {
         const int t = sm.order[q];
-        const int n = n0 + lane * 4;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const float* at = red + t * kRowsM + lane * 4;
         if (p.split > 1) {
@@ -697,10 +700,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) lora_project_kernel(const __g
         if (n < a.N) {
             if constexpr (F8) {
                 const float xs = __ldcg(a.x_scale + t);
-                s.x *= xs * __ldcg(a.w_scale + n);
-                s.y *= xs * __ldcg(a.w_scale + n + 1);
-                s.z *= xs * __ldcg(a.w_scale + n + 2);
-                s.w *= xs * __ldcg(a.w_scale + n + 3);
+                s.x *= xs * wsc.x;
+                s.y *= xs * wsc.y;
+                s.z *= xs * wsc.z;
+                s.w *= xs * wsc.w;
             }
             if (a.r > 0) {
                 const float4 l = *reinterpret_cast<const float4*>(lacc + (q - p0) * kRowsM + lane * 4);
