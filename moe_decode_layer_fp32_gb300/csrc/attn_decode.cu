@@ -28,7 +28,7 @@
 // Two CTAs per SM with a ring of three stages beat three with two (64 x 2048 keys: bf16 91 and 98 us,
 // E4M3 58 and 66) and tiles of 16 keys (E4M3 69).
 //
-// Beyond 128 columns o, the scores and q do not fit the registers (120 to 970 bytes of spills) and a bf16
+// Beyond 128 columns o, the scores and q do not fit the registers (120 to 920 bytes of spills) and a bf16
 // cache leaves one CTA to an SM: 64 x 2048 keys of 4 heads of 256, 16 query heads, bf16 105 us (75 % of
 // the cache's bytes at the copy rate), fp32 q 271, over E4M3 93 and 73.  More than 8 query heads of a key-value head
 // are one unit of 16 rows up to 128 columns without extra terms; otherwise every 8 of them are a unit of
@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t pack_hi(float a, float b) { return __byte_pe
 
 // Where a CTA (or one of its warps) stands.
 struct Cursor {
-    int b, unit, tile, tiles, first, keys; // keys from the first on
+    int b, unit, tile, tiles, first, n;
     int last;                              // tiles of the unit that begin before the run's end
     const int32_t* row;                    // the request's row of the block table
     long long base;                        // where the unit begins in the line of all units
@@ -211,9 +211,9 @@ struct Attn {
     __device__ static __forceinline__ void set_request(const AttnArgs& a, Cursor& c) {
         int n = max(a.seq_lens[c.b], 0);
         n = (int)min((long long)n, (long long)a.max_pages * a.c.page_size);
+        c.n = n;
         c.first = a.window > 0 ? max(0, n - a.window) : 0;
-        c.keys = n - c.first;
-        c.tiles = (int)(((uint32_t)c.keys + kTileKeys - 1) / kTileKeys);
+        c.tiles = (n - c.first) / kTileKeys + ((n - c.first) % kTileKeys != 0);
         c.row = a.table + c.b * a.table_ld;
     }
     // To the next tile; where none begins before `end`, to none of the run.
@@ -235,9 +235,9 @@ struct Attn {
     // Page and slot of the key that lane `lane` looks after in the warp's tile; page -1: none.
     __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
         // unsigned: the end of the last tile may lie beyond 2^31
-        const uint32_t at = (uint32_t)c.tile * kTileKeys + warp * KT + lane;
-        if (!inside(c) || lane >= KT || at >= (uint32_t)c.keys) return make_int2(-1, 0);
-        const int key = c.first + (int)at;
+        const uint32_t at = (uint32_t)c.first + (uint32_t)c.tile * kTileKeys + warp * KT + lane;
+        if (!inside(c) || lane >= KT || at >= (uint32_t)c.n) return make_int2(-1, 0);
+        const int key = (int)at;
         const int col = a.page_shift >= 0 ? key >> a.page_shift : key / a.c.page_size;
         const int page = c.row[col];
         if (page < 0 || page >= a.c.num_pages) {
@@ -711,7 +711,7 @@ struct Attn {
                         for (int k = 0; k < 4; ++k) {
                             const float (&o)[4] = st.o[w * kVElems + e + k];
                             // an infinite sum of first terms stands: a second term may be 0, and its sum NaN
-                            v[k] = ROWS == 16 ? o[2 * rr + i] : fabsf(o[i]) < CUDART_INF_F ? o[i] + o[2 + i] : o[i];
+                            v[k] = ROWS == 16 ? o[2 * rr + i] : o[i] + (fabsf(o[i]) < CUDART_INF_F ? o[2 + i] : 0.0f);
                         }
                         const int row = rr * 8 + lane / 4, f4 = (colb + e) / 4;
                         mine[row * (DP / 4) + (f4 ^ (row & 7))] = make_float4(v[0], v[1], v[2], v[3]);
