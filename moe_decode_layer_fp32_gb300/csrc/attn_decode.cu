@@ -28,9 +28,9 @@
 // Two CTAs per SM with a ring of three stages beat three with two (64 x 2048 keys: bf16 91 and 98 us,
 // E4M3 58 and 66) and tiles of 16 keys (E4M3 69).
 //
-// Beyond 128 columns o, the scores and q do not fit the registers (120 to 920 bytes of spills) and a bf16
-// cache leaves one CTA to an SM: 64 x 2048 keys of 4 heads of 256, 16 query heads, bf16 105 us (75 % of
-// the cache's bytes at the copy rate), fp32 q 271, over E4M3 93 and 73.  More than 8 query heads of a key-value head
+// Beyond 128 columns o, the scores and q do not fit the registers (124 to 960 bytes of spills) and a bf16
+// cache leaves one CTA to an SM: 64 x 2048 keys of 4 heads of 256, 16 query heads, bf16 102 us (77 % of
+// the cache's bytes at the copy rate), fp32 q 264, over E4M3 90 and 73.  More than 8 query heads of a key-value head
 // are one unit of 16 rows up to 128 columns without extra terms; otherwise every 8 of them are a unit of
 // their own and read the keys again: 64 / 4 heads of 128, bf16 54 us, fp32 q 92, over E4M3 49 and 59.
 #include <algorithm>
@@ -149,7 +149,9 @@ struct Attn {
     static constexpr int kPitch = DP * kElem;                        // bytes of a row in shared memory
     static constexpr int KT = kPitch <= 128 ? 32 : 16;               // keys of a warp's tile
     static constexpr int kTileBytes = KT * kPitch;                   // K or V
+    static constexpr int kTileShift = KT == 32 ? 7 : 6;
     static constexpr int kTileKeys = KT * kAttnWarps;
+    static_assert(kTileKeys == 1 << kTileShift, "tiles counted by a shift");
     static constexpr uint32_t kAllKeys = KT == 32 ? 0xffffffffu : (1u << (KT % 32)) - 1u;
     static constexpr int kChunks = kPitch / 16;                      // 16-byte chunks of a row
     static constexpr int kRowsPerIter = 32 / kChunks;
@@ -213,7 +215,7 @@ struct Attn {
         n = (int)min((long long)n, (long long)a.max_pages * a.c.page_size);
         c.n = n;
         c.first = a.window > 0 ? max(0, n - a.window) : 0;
-        c.tiles = (n - c.first) / kTileKeys + ((n - c.first) % kTileKeys != 0);
+        c.tiles = ((n - c.first - 1) >> kTileShift) + 1;     // without a sum that may pass 2^31; 0 for no keys
         c.row = a.table + c.b * a.table_ld;
     }
     // To the next tile; where none begins before `end`, to none of the run.
@@ -711,7 +713,7 @@ struct Attn {
                         for (int k = 0; k < 4; ++k) {
                             const float (&o)[4] = st.o[w * kVElems + e + k];
                             // an infinite sum of first terms stands: a second term may be 0, and its sum NaN
-                            v[k] = ROWS == 16 ? o[2 * rr + i] : o[i] + (fabsf(o[i]) < CUDART_INF_F ? o[2 + i] : 0.0f);
+                            v[k] = ROWS == 16 ? o[2 * rr + i] : fabsf(o[i]) < CUDART_INF_F ? o[i] + o[2 + i] : o[i];
                         }
                         const int row = rr * 8 + lane / 4, f4 = (colb + e) / 4;
                         mine[row * (DP / 4) + (f4 ^ (row & 7))] = make_float4(v[0], v[1], v[2], v[3]);
