@@ -18,9 +18,11 @@ between two uses of a replica exceed the 129 MB L2 many times over: weights
 are read cold.
 
 value = unique weight bytes of all timed layer passes / device time (GB/s).
-per_batch gives, per layer and batch size, µs per layer, unique MB, GB/s, the
-fraction of the measured HBM bandwidth and each stage alone; next_rows the
-same for the matrix form P and FP8 weights (not part of the step).
+per_batch gives, per layer and batch size, µs per layer and the fraction of the
+measured HBM bandwidth; next_rows the same for the matrix form P and FP8 weights
+(not part of the step).  The whole tables (unique MB, GB/s, each stage alone, the
+FFN's path) follow on stderr as one line that begins with "detail: ", so that the
+result line stays short enough for whoever keeps only the end of an output.
 Inputs are synthetic (seeded), see moe_decode_layer_fp32_gb300.synth.
 
 --workload NAME times one layer alone.  --impl reference times the CPU oracle
@@ -590,7 +592,7 @@ def run_ours(args, rank, world, local):
                    "l2": "inputs larger than L2: consecutive steps use distinct layer replicas of each "
                          "workload (>=4x L2 between reuses of a replica)",
                    "parallelism": f"replicas x{world}"},
-        "per_batch": per_workload,
+        "per_batch": {"columns": ["us_per_layer", "frac"], **short_table(per_workload)},
         "roofline": roofline,
         "e2e": e2e,
         "gpu_launches": launches,
@@ -598,9 +600,15 @@ def run_ours(args, rank, world, local):
         "cpu_baseline": cpu,
     }
     if next_rows is not None:
-        out["next_rows"] = next_rows
+        out["next_rows"] = {"columns": ["us_per_layer", "frac"], **short_table(next_rows)}
     if rank == 0:
+        print("detail: " + json.dumps({"per_batch": per_workload, "next_rows": next_rows}), file=sys.stderr, flush=True)
         print(json.dumps(out))
+
+
+def short_table(tables):
+    """{layer: {T: [us_per_layer, frac]}} of {layer: what measure_batches gives}."""
+    return {name: {T: [e["us_per_layer"], e["frac"]] for T, e in t.items()} for name, t in tables.items()}
 
 
 def suite_config(Ws):
