@@ -117,6 +117,33 @@ int moe_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, 
                   void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, int q_heads,
                   int32_t* status, void* stream);
 
+/*
+ * moe_kv_append with a root-mean-square norm of every head of q and k before the
+ * rotation, which may be by positions of several axes (time, height, width).
+ * In fp32, rounded once:
+ *   u = x / sqrt(mean(x^2) + eps) * weight      over the D elements of a head
+ *   then u[i], u[i + rot / 2] turned by row p of cos_sin, elements i and
+ *   rot / 2 + i, where p = positions[t], or axis_positions[axis[i]][t] with axes
+ *   q_weight, k_weight  [D] of weight_dtype (F32 or BF16), or NULL for ones
+ *   axis_positions      int32[axes, T] or NULL (axes 0).  positions then says
+ *                       only which slot a token takes
+ *   axis                host bytes [rot / 2]: the axis of each pair, copied
+ *                       by the call
+ * v is written as it is.  The q of padding and of a token dropped for its
+ * place in cos_sin (any of its axes' positions) is normed and not turned.
+ * The other arguments, the slots and the tokens dropped are moe_kv_append's.
+ * Limits: eps finite and >= 0; axes <= 255 with every axis[i] < axes.
+ */
+int moe_qk_norm_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                       int64_t v_token_stride, int64_t v_head_stride, int in_dtype, int T,
+                       const moe_kv_cache* cache, const int32_t* block_table, int64_t table_ld, int R,
+                       int max_pages, const int32_t* positions, const int32_t* req, const float* cos_sin,
+                       int rot, int max_pos, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                       void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, int q_heads,
+                       const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                       const int32_t* axis_positions, int axes, const uint8_t* axis, int32_t* status,
+                       void* stream);
+
 /* Workspace bytes of moe_attn_decode for up to B requests (0: bad sizes).  Zero
  * it once with moe_workspace_init; one workspace serves any number of calls, one
  * after another, of the same q_heads, heads and head_dim.  Its status word is

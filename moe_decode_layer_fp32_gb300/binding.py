@@ -103,6 +103,8 @@ _SIGS = {
     "moe_rmsnorm": (_I, [_P, _I, _I64, _P, _I, _I64, _P, _I64, _P, _I, _F, _I, _I, _P, _I, _I64, _P, _I, _P]),
     "moe_kv_append": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _I64, _I, _I, _P, _P,
                            _P, _I, _I, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _P]),
+    "moe_qk_norm_append": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _I64, _I, _I, _P, _P,
+                                _P, _I, _I, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _P, _I, _F, _P, _I, _P, _P, _P]),
     "moe_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "moe_attn_decode": (_I, [_P, _I, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _I64, _I, _P, _F, _I, _F, _P,
                              _I, _I64, _I64, _P, _P, _SZ, _P]),
@@ -450,7 +452,7 @@ def moe_unique_weight_bytes_deamoe(d, n, I_sh, I_pr, I_s, dtype_code, A_d, A_e) 
 # dimension) must be contiguous, everything else may be a view.
 
 
-# The four calls themselves go through the extension module beside the library
+# The calls themselves go through the extension module beside the library
 # (csrc/block_bind.cpp), which reads the tensors in C++: a call costs the host less
 # that way than its launch.
 
@@ -460,7 +462,7 @@ _block = None
 
 
 def _load_block():
-    """The extension module, bound to the loaded library (the first call of any of the four)."""
+    """The extension module, bound to the loaded library (the first call of any of its functions)."""
     global _block
     path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block_bind.so")
     if not os.path.exists(path):
@@ -468,8 +470,8 @@ def _load_block():
     spec = importlib.util.spec_from_file_location("_block_bind", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
-    names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project")
-    mod.bind(*(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check, KvCache)
+    names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project", "moe_qk_norm_append")
+    mod.bind(tuple(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check, KvCache)
     _block = mod
     return mod
 
@@ -529,6 +531,18 @@ def moe_kv_append(k, v, cache: KvCache, block_table, positions, req=None, cos_si
     or None (token t is request t); ``cos_sin`` float32 [positions, rot] or
     None; ``q_out`` may be ``q``; ``status`` int32 [1] or None."""
     (_block or _load_block()).moe_kv_append(k, v, cache, block_table, positions, req, cos_sin, q, q_out, status)
+
+
+def moe_qk_norm_append(q, k, v, q_weight, k_weight, eps: float, cache: KvCache, block_table, positions, q_out, req=None,
+                       cos_sin=None, axis_positions=None, axis=None, status=None):
+    """``moe_kv_append`` with a root-mean-square norm of every head of q and k first.
+
+    ``q_weight`` and ``k_weight`` [D] or None (of one dtype); ``q`` and ``q_out`` may
+    both be None.  Positions of several axes (time, height, width): ``axis_positions``
+    int32 [axes, T], and ``axis`` bytes with the axis of each of the rot / 2
+    pairs; ``positions`` then only names the slots."""
+    (_block or _load_block()).moe_qk_norm_append(q, k, v, q_weight, k_weight, eps, cache, block_table, positions, q_out, req,
+                                                 cos_sin, axis_positions, axis, status)
 
 
 def moe_attn_workspace_bytes(B: int, q_heads: int, heads: int, head_dim: int) -> int:

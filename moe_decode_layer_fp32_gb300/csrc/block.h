@@ -45,6 +45,16 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
+struct QkAppendArgs : AppendArgs {
+    const void* q_weight;      // null: ones
+    const void* k_weight;
+    int w_dt, axes;            // axes 0: the rotation is that of `positions`
+    float eps;
+    const int32_t* axis_positions;   // [axes, T]
+    uint8_t axis[128];         // of each pair
+};
+cudaError_t launch_qk_norm_append(const QkAppendArgs& a, cudaStream_t s);
+
 struct AttnArgs {
     const void* q;
     void* out;

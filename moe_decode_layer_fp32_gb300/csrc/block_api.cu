@@ -50,6 +50,40 @@ int check_cache(const moe_kv_cache* c, const char* who) {
     return MOE_OK;
 }
 
+// The arguments of an append, checked.
+int append_args(moe::AppendArgs& a, const char* who, const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                int64_t v_token_stride, int64_t v_head_stride, int in_dtype, int T, const moe_kv_cache* cache,
+                const int32_t* block_table, int64_t table_ld, int R, int max_pages, const int32_t* positions,
+                const int32_t* req, const float* cos_sin, int rot, int max_pos, const void* q, int64_t q_token_stride,
+                int64_t q_head_stride, void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, int q_heads,
+                int32_t* status) {
+    int rc = check_cache(cache, who);
+    if (rc) return rc;
+    if (!is_act(in_dtype)) return api_fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d of k, v", who, in_dtype);
+    if (T < 0 || R < 0 || max_pages < 0 || table_ld < max_pages)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: need T, R, max_pages >= 0 and table_ld >= max_pages (%d, %d, %d, %lld)",
+                        who, T, R, max_pages, (long long)table_ld);
+    if (rot < 0 || rot % 2 != 0 || rot > cache->head_dim || (rot > 0) != (cos_sin != nullptr) || (rot > 0 && max_pos < 1))
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: rot=%d must be even, at most head_dim=%d, and go with cos_sin of max_pos >= 1 rows",
+                        who, rot, cache->head_dim);
+    if ((q != nullptr) != (q_out != nullptr) || (q && q_heads < 1))
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: q and q_out go together, with q_heads >= 1", who);
+    if (T == 0) return MOE_OK;
+    if (!k || !v || !positions || !block_table) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+    const uintptr_t size = in_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)q | (uintptr_t)q_out) % size != 0)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: k, v or q not aligned to its elements", who);
+    a.k = k; a.v = v; a.q = q; a.q_out = q_out;
+    a.k_ts = k_token_stride; a.k_hs = k_head_stride; a.v_ts = v_token_stride; a.v_hs = v_head_stride;
+    a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.o_ts = qo_token_stride; a.o_hs = qo_head_stride;
+    a.in_dt = in_dtype; a.T = T; a.q_heads = q ? q_heads : 0;
+    a.c = *cache;
+    a.table = block_table; a.table_ld = table_ld; a.R = R; a.max_pages = max_pages;
+    a.positions = positions; a.req = req; a.cos_sin = cos_sin; a.rot = rot; a.max_pos = max_pos;
+    a.status = status;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -95,32 +129,45 @@ int moe_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, 
                   void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, int q_heads,
                   int32_t* status, void* stream) {
     const char* who = "moe_kv_append";
-    int rc = check_cache(cache, who);
-    if (rc) return rc;
-    if (!is_act(in_dtype)) return api_fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d of k, v", who, in_dtype);
-    if (T < 0 || R < 0 || max_pages < 0 || table_ld < max_pages)
-        return api_fail(MOE_ERR_INVALID_ARG, "%s: need T, R, max_pages >= 0 and table_ld >= max_pages (%d, %d, %d, %lld)",
-                        who, T, R, max_pages, (long long)table_ld);
-    if (rot < 0 || rot % 2 != 0 || rot > cache->head_dim || (rot > 0) != (cos_sin != nullptr) || (rot > 0 && max_pos < 1))
-        return api_fail(MOE_ERR_INVALID_ARG, "%s: rot=%d must be even, at most head_dim=%d, and go with cos_sin of max_pos >= 1 rows",
-                        who, rot, cache->head_dim);
-    if ((q != nullptr) != (q_out != nullptr) || (q && q_heads < 1))
-        return api_fail(MOE_ERR_INVALID_ARG, "%s: q and q_out go together, with q_heads >= 1", who);
-    if (T == 0) return MOE_OK;
-    if (!k || !v || !positions || !block_table) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
-    const uintptr_t size = in_dtype == MOE_DTYPE_BF16 ? 2 : 4;
-    if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)q | (uintptr_t)q_out) % size != 0)
-        return api_fail(MOE_ERR_INVALID_ARG, "%s: k, v or q not aligned to its elements", who);
     moe::AppendArgs a = {};
-    a.k = k; a.v = v; a.q = q; a.q_out = q_out;
-    a.k_ts = k_token_stride; a.k_hs = k_head_stride; a.v_ts = v_token_stride; a.v_hs = v_head_stride;
-    a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.o_ts = qo_token_stride; a.o_hs = qo_head_stride;
-    a.in_dt = in_dtype; a.T = T; a.q_heads = q ? q_heads : 0;
-    a.c = *cache;
-    a.table = block_table; a.table_ld = table_ld; a.R = R; a.max_pages = max_pages;
-    a.positions = positions; a.req = req; a.cos_sin = cos_sin; a.rot = rot; a.max_pos = max_pos;
-    a.status = status;
+    const int rc = append_args(a, who, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, in_dtype, T,
+                               cache, block_table, table_ld, R, max_pages, positions, req, cos_sin, rot, max_pos, q,
+                               q_token_stride, q_head_stride, q_out, qo_token_stride, qo_head_stride, q_heads, status);
+    if (rc || T == 0) return rc;
     return launched(moe::launch_kv_append(a, as_stream(stream)), who);
+}
+
+int moe_qk_norm_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                       int64_t v_token_stride, int64_t v_head_stride, int in_dtype, int T,
+                       const moe_kv_cache* cache, const int32_t* block_table, int64_t table_ld, int R,
+                       int max_pages, const int32_t* positions, const int32_t* req, const float* cos_sin,
+                       int rot, int max_pos, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                       void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, int q_heads,
+                       const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                       const int32_t* axis_positions, int axes, const uint8_t* axis, int32_t* status,
+                       void* stream) {
+    const char* who = "moe_qk_norm_append";
+    moe::QkAppendArgs a = {};
+    const int rc = append_args(a, who, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, in_dtype, T,
+                               cache, block_table, table_ld, R, max_pages, positions, req, cos_sin, rot, max_pos, q,
+                               q_token_stride, q_head_stride, q_out, qo_token_stride, qo_head_stride, q_heads, status);
+    if (rc) return rc;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return api_fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", who);
+    if ((q_weight || k_weight) && !is_act(weight_dtype)) return api_fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d of the weights", who, weight_dtype);
+    const uintptr_t size = weight_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    if (((uintptr_t)q_weight | (uintptr_t)k_weight) % size != 0)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: q_weight or k_weight not aligned to its elements", who);
+    if (axes < 0 || axes > 255 || (axes > 0) != (axis != nullptr) || (axes > 0 && rot == 0) ||
+        (T > 0 && (axes > 0) != (axis_positions != nullptr)))
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: axes=%d must be 0 to 255, and go with axis_positions, axis and a rotation", who, axes);
+    for (int i = 0; axes && i < rot / 2; ++i) {
+        if (axis[i] >= axes) return api_fail(MOE_ERR_INVALID_ARG, "%s: axis[%d]=%d of %d axes", who, i, axis[i], axes);
+        a.axis[i] = axis[i];
+    }
+    if (T == 0) return MOE_OK;
+    a.q_weight = q_weight; a.k_weight = k_weight; a.w_dt = weight_dtype; a.eps = eps;
+    a.axes = axes; a.axis_positions = axis_positions;
+    return launched(moe::launch_qk_norm_append(a, as_stream(stream)), who);
 }
 
 size_t moe_attn_workspace_bytes(int B, int q_heads, int heads, int head_dim) {

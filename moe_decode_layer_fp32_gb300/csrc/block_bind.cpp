@@ -18,8 +18,10 @@ namespace {
 
 decltype(&moe_rmsnorm) g_rmsnorm = nullptr;
 decltype(&moe_kv_append) g_append = nullptr;
+decltype(&moe_qk_norm_append) g_qk_append = nullptr;
 decltype(&moe_attn_decode) g_attn = nullptr;
 decltype(&moe_lora_project) g_lora = nullptr;
+constexpr int kFunctions = 5;
 PyObject* g_on_error = nullptr;      // (name, code) -> raises
 PyTypeObject* g_cache_type = nullptr;
 PyObject* g_address = nullptr;       // "address"
@@ -257,45 +259,104 @@ PyObject* py_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
     });
 }
 
+// What the two appends have in common, from the arguments (cos_sin, q, q_out and status may be missing).
+struct AppendCall {
+    const moe_kv_cache* c;
+    int T, hq, max_pos, rot;
+    Heads k, v, q, o;
+    const float* cs;
+    Table t;
+    const int32_t *pos, *req;
+    int32_t* st;
+    AppendCall(PyObject* ok, PyObject* ov, PyObject* cache, PyObject* block_table, PyObject* positions, PyObject* oreq,
+               PyObject* cos_sin, PyObject* oq, PyObject* q_out, PyObject* status) {
+        c = cache_of(cache);
+        const at::Tensor& kt = tensor(ok, "k");
+        if (kt.dim() != 3) refuse("k: expected [T, heads, D]");
+        T = size32(kt.size(0), "k");
+        const int D = c->head_dim;
+        k = heads(ok, "k", T, c->heads, D);
+        v = heads(ov, "v", T, c->heads, D);
+        if (k.code != v.code) refuse("k and v must have one dtype");
+        q = o = {nullptr, 0, 0, 0};
+        hq = 0;
+        if (given(oq) != given(q_out)) refuse("q and q_out go together");
+        if (given(oq)) {
+            const at::Tensor& qt = tensor(oq, "q");
+            if (qt.dim() != 3) refuse("q: expected [T, q_heads, D]");
+            hq = size32(qt.size(1), "q");
+            q = heads(oq, "q", T, hq, D);
+            o = heads(q_out, "q_out", T, hq, D);
+            if (q.code != k.code || o.code != k.code) refuse("q, q_out and k must have one dtype");
+        }
+        cs = nullptr;
+        max_pos = rot = 0;
+        if (given(cos_sin)) {
+            const at::Tensor& ct = tensor(cos_sin, "cos_sin");
+            if (ct.dim() != 2) refuse("cos_sin: expected [positions, rot]");
+            max_pos = size32(ct.size(0), "cos_sin");
+            rot = size32(ct.size(1), "cos_sin");
+            cs = static_cast<const float*>(exactly(cos_sin, "cos_sin", at::kFloat, {max_pos, rot}));
+        }
+        t = table(block_table);
+        pos = static_cast<const int32_t*>(exactly(positions, "positions", at::kInt, {T}));
+        req = static_cast<const int32_t*>(exactly(oreq, "req", at::kInt, {T}));
+        st = static_cast<int32_t*>(exactly(status, "status", at::kInt, {1}));
+    }
+};
+
 PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
     static Signature<10> sig = {"moe_kv_append",
                                 {"k", "v", "cache", "block_table", "positions", "req", "cos_sin", "q", "q_out", "status"}, 5};
     return guarded([&] {
         PyObject* a[10];
         sig.parse(args, nargs, kwnames, a);
-        const moe_kv_cache* c = cache_of(a[2]);
-        const at::Tensor& kt = tensor(a[0], "k");
-        if (kt.dim() != 3) refuse("k: expected [T, heads, D]");
-        const int T = size32(kt.size(0), "k"), D = c->head_dim;
-        const Heads k = heads(a[0], "k", T, c->heads, D), v = heads(a[1], "v", T, c->heads, D);
-        if (k.code != v.code) refuse("k and v must have one dtype");
-        Heads q = {nullptr, 0, 0, 0}, o = {nullptr, 0, 0, 0};
-        int hq = 0;
-        if (given(a[7]) != given(a[8])) refuse("q and q_out go together");
-        if (given(a[7])) {
-            const at::Tensor& qt = tensor(a[7], "q");
-            if (qt.dim() != 3) refuse("q: expected [T, q_heads, D]");
-            hq = size32(qt.size(1), "q");
-            q = heads(a[7], "q", T, hq, D);
-            o = heads(a[8], "q_out", T, hq, D);
-            if (q.code != k.code || o.code != k.code) refuse("q, q_out and k must have one dtype");
-        }
-        const float* cs = nullptr;
-        int max_pos = 0, rot = 0;
-        if (given(a[6])) {
-            const at::Tensor& t = tensor(a[6], "cos_sin");
-            if (t.dim() != 2) refuse("cos_sin: expected [positions, rot]");
-            max_pos = size32(t.size(0), "cos_sin");
-            rot = size32(t.size(1), "cos_sin");
-            cs = static_cast<const float*>(exactly(a[6], "cos_sin", at::kFloat, {max_pos, rot}));
-        }
-        const Table t = table(a[3]);
-        auto* pos = static_cast<const int32_t*>(exactly(a[4], "positions", at::kInt, {T}));
-        auto* req = static_cast<const int32_t*>(exactly(a[5], "req", at::kInt, {T}));
-        auto* st = static_cast<int32_t*>(exactly(a[9], "status", at::kInt, {1}));
+        const AppendCall p(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9]);
         return done("moe_kv_append",
-                    g_append(k.p, k.outer, k.inner, v.p, v.outer, v.inner, k.code, T, c, t.p, t.ld, t.R, t.pages, pos, req,
-                             cs, rot, max_pos, q.p, q.outer, q.inner, o.p, o.outer, o.inner, hq, st, stream()));
+                    g_append(p.k.p, p.k.outer, p.k.inner, p.v.p, p.v.outer, p.v.inner, p.k.code, p.T, p.c, p.t.p, p.t.ld, p.t.R,
+                             p.t.pages, p.pos, p.req, p.cs, p.rot, p.max_pos, p.q.p, p.q.outer, p.q.inner, p.o.p, p.o.outer,
+                             p.o.inner, p.hq, p.st, stream()));
+    });
+}
+
+// A vector [n] of F32 or BF16; None is nullptr.
+void* weight(PyObject* o, const char* name, int n, int& code) {
+    if (!given(o)) return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    code = code_of(t, name);
+    return exactly(o, name, t.scalar_type(), {n});
+}
+
+PyObject* py_qk_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    static Signature<15> sig = {"moe_qk_norm_append",
+                                {"q", "k", "v", "q_weight", "k_weight", "eps", "cache", "block_table", "positions", "q_out",
+                                 "req", "cos_sin", "axis_positions", "axis", "status"}, 10};
+    return guarded([&] {
+        PyObject* a[15];
+        sig.parse(args, nargs, kwnames, a);
+        const AppendCall p(a[1], a[2], a[6], a[7], a[8], a[10], a[11], a[0], a[9], a[14]);
+        int qw_code = -1, kw_code = -1;
+        const void* qw = weight(a[3], "q_weight", p.c->head_dim, qw_code);
+        const void* kw = weight(a[4], "k_weight", p.c->head_dim, kw_code);
+        if (qw && kw && qw_code != kw_code) refuse("q_weight and k_weight must have one dtype");
+        const int32_t* places = nullptr;
+        const uint8_t* axis = nullptr;
+        int axes = 0;
+        if (given(a[12]) != given(a[13])) refuse("axis_positions and axis go together");
+        if (given(a[12])) {
+            const at::Tensor& t = tensor(a[12], "axis_positions");
+            if (t.dim() != 2) refuse("axis_positions: expected [axes, T]");
+            axes = size32(t.size(0), "axis_positions");
+            places = static_cast<const int32_t*>(exactly(a[12], "axis_positions", at::kInt, {axes, p.T}));
+            if (!PyBytes_Check(a[13]) || PyBytes_GET_SIZE(a[13]) != p.rot / 2) refuse("axis: expected bytes, one per pair of a row of cos_sin");
+            if (axes < 1) refuse("axis_positions: no axes");
+            axis = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[13]));
+        }
+        return done("moe_qk_norm_append",
+                    g_qk_append(p.k.p, p.k.outer, p.k.inner, p.v.p, p.v.outer, p.v.inner, p.k.code, p.T, p.c, p.t.p, p.t.ld, p.t.R,
+                                p.t.pages, p.pos, p.req, p.cs, p.rot, p.max_pos, p.q.p, p.q.outer, p.q.inner, p.o.p, p.o.outer,
+                                p.o.inner, p.hq, qw, kw, qw ? qw_code : kw_code, (float)number(a[5], 0.0), places, axes, axis,
+                                p.st, stream()));
     });
 }
 
@@ -357,16 +418,25 @@ PyObject* py_lora(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
     });
 }
 
-// bind(rmsnorm, kv_append, attn_decode, lora_project, on_error, cache type): addresses of the library's
-// functions, what raises for an error code, and the class of caches.
+// bind(addresses, on_error, cache type): the library's functions in the order of kMethods, what raises for
+// an error code, and the class of caches.
 PyObject* py_bind(PyObject*, PyObject* args) {
-    unsigned long long f[4];
-    PyObject *on_error, *cache_type;
-    if (!PyArg_ParseTuple(args, "KKKKOO!", &f[0], &f[1], &f[2], &f[3], &on_error, &PyType_Type, &cache_type)) return nullptr;
+    PyObject *addresses, *on_error, *cache_type;
+    if (!PyArg_ParseTuple(args, "O!OO!", &PyTuple_Type, &addresses, &on_error, &PyType_Type, &cache_type)) return nullptr;
+    void* f[kFunctions];
+    if (PyTuple_GET_SIZE(addresses) != kFunctions) {
+        PyErr_SetString(PyExc_ValueError, "bind: an address for each function");
+        return nullptr;
+    }
+    for (int i = 0; i < kFunctions; ++i) {
+        f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addresses, i));
+        if (!f[i] && PyErr_Occurred()) return nullptr;
+    }
     g_rmsnorm = reinterpret_cast<decltype(g_rmsnorm)>(f[0]);
     g_append = reinterpret_cast<decltype(g_append)>(f[1]);
     g_attn = reinterpret_cast<decltype(g_attn)>(f[2]);
     g_lora = reinterpret_cast<decltype(g_lora)>(f[3]);
+    g_qk_append = reinterpret_cast<decltype(g_qk_append)>(f[4]);
     Py_INCREF(on_error);
     Py_XSETREF(g_on_error, on_error);
     Py_INCREF(cache_type);
@@ -380,6 +450,7 @@ PyMethodDef kMethods[] = {
     {"moe_kv_append", FAST(py_append), "moe_kv_append of include/moe_block.h"},
     {"moe_attn_decode", FAST(py_attn), "moe_attn_decode of include/moe_block.h"},
     {"moe_lora_project", FAST(py_lora), "moe_lora_project of include/moe_block.h"},
+    {"moe_qk_norm_append", FAST(py_qk_append), "moe_qk_norm_append of include/moe_block.h"},
     {"bind", py_bind, METH_VARARGS, "addresses of the library's functions, and what they need of Python"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_block_bind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -109,3 +109,27 @@ def lora_project(x, w, lora=None, adapter=None, x_scale=None, w_scale=None):
                 y[t] += s[i] * (B[i] @ (A[i] @ x[t]))
                 size[t] += s[i].abs() * (B[i].abs() @ (A[i].abs() @ x[t].abs()))
     return y, size
+
+
+def qk_norm(x, weight, eps):
+    """Each head of x [T, heads, D] over the root of its mean square plus eps, times weight [D]."""
+    x = f64(x)
+    y = x / torch.sqrt((x * x).mean(dim=2, keepdim=True) + eps)
+    return y if weight is None else y * f64(weight)
+
+
+def rotate_axes(v, positions, cos_sin, axis_positions, axis):
+    """``rotate`` with the row of pair i at axis_positions[axis[i]]; tokens of a negative position, or with
+    one of these outside cos_sin, stay."""
+    v = f64(v).clone()
+    half = cos_sin.shape[1] // 2
+    for t, p in enumerate(positions.tolist()):
+        at = [int(axis_positions[axis[i], t]) for i in range(half)]
+        if p < 0 or any(a < 0 or a >= cos_sin.shape[0] for a in at):
+            continue
+        pair = torch.arange(half)
+        c, s = f64(cos_sin[at, pair]), f64(cos_sin[at, half + pair])
+        a, b = v[t, :, :half].clone(), v[t, :, half:2 * half].clone()
+        v[t, :, :half] = a * c - b * s
+        v[t, :, half:2 * half] = b * c + a * s
+    return v
