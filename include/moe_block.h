@@ -179,6 +179,87 @@ int moe_attn_decode(const void* q, int q_dtype, int64_t q_batch_stride, int64_t 
                     int64_t out_head_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* Attention over selected pages                                             */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * A long request's new token attends to the pages that can matter to it:
+ *   moe_page_bounds(cache)               of the pages that tokens were appended to
+ *   s = moe_page_scores(q, bounds)
+ *   tables, lens = moe_page_select(s)    per request and key-value head
+ *   a = moe_attn_pages(q, tables, lens)
+ * In all of them request b has n = seq_lens[b] tokens (none where n <= 0; no more
+ * than its max_pages entries of the block table have room for) in
+ * ceil(n / page_size) pages, block_table int32[B, max_pages] with row stride
+ * table_ld, B >= 0; status is int32[1] or NULL and receives MOE_ERR_DEVICE for a
+ * length beyond the table or a page outside the cache, and is left alone
+ * otherwise.
+ */
+
+/*
+ * For every page with tokens from first[b] (0 where first is NULL or negative) to n - 1,
+ * each key-value head h and each of the D channels:
+ *   bounds[page, h, 0, d] = least, bounds[page, h, 1, d] = greatest
+ * of the keys of all its tokens below n.  Exact; -0 and 0 are alike.
+ *   bounds      [num_pages, heads, 2, D] packed, of the cache's type (E4M3: codes, of
+ *               the cache's scales), 16-byte aligned
+ *   first       int32[B] or NULL
+ * A NaN key makes the least or the greatest of its channel NaN, or both.  Pages outside
+ * the cache are skipped (status).  Bounds of other pages are left alone.  A
+ * page of several requests gets the bounds of one of them.
+ */
+int moe_page_bounds(const moe_kv_cache* cache, void* bounds, const int32_t* block_table, int64_t table_ld,
+                    int max_pages, int B, const int32_t* seq_lens, const int32_t* first, int32_t* status,
+                    void* stream);
+
+/*
+ * scores[b, g, j] = sum over the query heads h of key-value head g and d of
+ *   max(q[b, h, d] lo[d], q[b, h, d] hi[d]),  lo, hi = bounds of page j of request b
+ * (times the cache's scales): no key of the page has a greater sum of q . k over
+ * these heads.  Computed as
+ *   sum_d (sum_h min(q, 0)) lo[d] + (sum_h max(q, 0)) hi[d],
+ * so an infinite bound may make a score NaN.  -inf for a page outside the cache (status).
+ *   q           [B, q_heads, D] F32 or BF16, strides as in moe_attn_decode
+ *   scores      float[B, heads, max_pages] packed; entries behind a request's
+ *               pages are left alone
+ * Of the cache only its type, sizes and k_scale are used.
+ */
+int moe_page_scores(const void* q, int q_dtype, int64_t q_batch_stride, int64_t q_head_stride, int B,
+                    int q_heads, const moe_kv_cache* cache, const void* bounds,
+                    const int32_t* block_table, int64_t table_ld, int max_pages, const int32_t* seq_lens,
+                    float* scores, int32_t* status, void* stream);
+
+/*
+ * The first `sinks` and the last `recent` pages of a request and those of the
+ * others with the greatest scores, `keep` in all or as many as it has; equal
+ * scores: the earlier page; NaN counts above all numbers.
+ *   tables[b, g, i] = block_table entry of the i-th page kept, in their order
+ *                     in the request; -1 behind the last one
+ *   lens[b, g]      = number of tokens in them
+ *   scores      float[B, heads, max_pages] packed
+ *   tables      int32[B, heads, keep] packed; lens int32[B, heads]
+ * Limits: page_size, keep >= 1; sinks, recent >= 0 with sinks + recent <= keep.
+ */
+int moe_page_select(const float* scores, int B, int heads, const int32_t* block_table, int64_t table_ld,
+                    int max_pages, const int32_t* seq_lens, int page_size, int keep, int sinks, int recent,
+                    int32_t* tables, int32_t* lens, void* stream);
+
+/*
+ * moe_attn_decode (without a window) over a table of pages and a length for each
+ * key-value head: the query heads of head g of request b attend to the first
+ * lens[b, g] slots of the pages tables[b, g, :], all but the last of them full.
+ * A page that a table lists twice counts twice.
+ *   tables      int32[B, heads, max_pages] packed; lens int32[B, heads]
+ * Workspace, status and all else are those of moe_attn_decode; one workspace
+ * serves calls of both.
+ */
+int moe_attn_pages(const void* q, int q_dtype, int64_t q_batch_stride, int64_t q_head_stride, int B,
+                   int q_heads, const moe_kv_cache* cache, const int32_t* tables, int max_pages,
+                   const int32_t* lens, float scale, float softcap, void* out, int out_dtype,
+                   int64_t out_batch_stride, int64_t out_head_stride, float* lse, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Shared projection with low-rank adapters                                  */
 /* ------------------------------------------------------------------------- */
 

@@ -108,6 +108,11 @@ _SIGS = {
     "moe_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "moe_attn_decode": (_I, [_P, _I, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _I64, _I, _P, _F, _I, _F, _P,
                              _I, _I64, _I64, _P, _P, _SZ, _P]),
+    "moe_page_bounds": (_I, [C.POINTER(KvCacheArgs), _P, _P, _I64, _I, _I, _P, _P, _P, _P]),
+    "moe_page_scores": (_I, [_P, _I, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _P, _I64, _I, _P, _P, _P, _P]),
+    "moe_page_select": (_I, [_P, _I, _I, _P, _I64, _I, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_attn_pages": (_I, [_P, _I, _I64, _I64, _I, _I, C.POINTER(KvCacheArgs), _P, _I, _P, _F, _F, _P, _I, _I64, _I64,
+                            _P, _P, _SZ, _P]),
     "moe_lora_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_lora_project": (_I, [_P, _I, _I64, _P, _I, _I, _P, _I, _I64, _P, _I, _P, _P, _P, _I, _I, _P, _P, _I, _I64,
                               _P, _SZ, _P]),
@@ -470,7 +475,8 @@ def _load_block():
     spec = importlib.util.spec_from_file_location("_block_bind", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
-    names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project", "moe_qk_norm_append")
+    names = ("moe_rmsnorm", "moe_kv_append", "moe_attn_decode", "moe_lora_project", "moe_qk_norm_append",
+             "moe_page_bounds", "moe_page_scores", "moe_page_select", "moe_attn_pages")
     mod.bind(tuple(C.cast(getattr(lib(), n), C.c_void_p).value for n in names), _check, KvCache)
     _block = mod
     return mod
@@ -565,6 +571,37 @@ def moe_attn_decode(q, cache: KvCache, block_table, seq_lens, scale: float, out,
     ``block_table`` int32 [B, pages], ``seq_lens`` int32 [B] (the new token
     included), ``lse`` float32 [B, q_heads] or None."""
     (_block or _load_block()).moe_attn_decode(q, cache, block_table, seq_lens, scale, out, ws, window, softcap, lse)
+
+
+def new_page_bounds(cache: KvCache) -> torch.Tensor:
+    """Allocate (torch) the bounds of a cache's pages, [pages, heads, 2, D] of its type; moe_page_bounds
+    writes those of the pages in use."""
+    k = cache.tensors[0]
+    return torch.empty((k.shape[0], cache.heads, 2, cache.head_dim), dtype=k.dtype, device=k.device)
+
+
+def moe_page_bounds(cache: KvCache, bounds, block_table, seq_lens, first=None, status=None):
+    """Per channel the least and greatest key of every page with tokens from ``first`` (int32 [B], the positions
+    just appended; None: all) to ``seq_lens`` - 1, into ``bounds`` (see new_page_bounds)."""
+    (_block or _load_block()).moe_page_bounds(cache, bounds, block_table, seq_lens, first, status)
+
+
+def moe_page_scores(q, cache: KvCache, bounds, block_table, seq_lens, scores, status=None):
+    """What the queries of a key-value head can score in a page, at most: q [B, q_heads, D], ``scores``
+    float32 [B, heads, pages] (entries behind a request's pages are left alone)."""
+    (_block or _load_block()).moe_page_scores(q, cache, bounds, block_table, seq_lens, scores, status)
+
+
+def moe_page_select(scores, block_table, seq_lens, page_size: int, tables, lens, sinks: int = 0, recent: int = 1):
+    """The first ``sinks``, the last ``recent`` and the best other pages of each request and key-value head, into
+    ``tables`` int32 [B, heads, pages to keep] (-1 behind the last) and ``lens`` int32 [B, heads] (their tokens)."""
+    (_block or _load_block()).moe_page_select(scores, block_table, seq_lens, page_size, tables, lens, sinks, recent)
+
+
+def moe_attn_pages(q, cache: KvCache, tables, lens, scale: float, out, ws, softcap: float = 0.0, lse=None):
+    """``moe_attn_decode`` over a table of pages and a length for each key-value head: ``tables`` int32
+    [B, heads, pages], ``lens`` int32 [B, heads]; workspaces are those of new_attn_workspace."""
+    (_block or _load_block()).moe_attn_pages(q, cache, tables, lens, scale, out, ws, softcap, lse)
 
 
 def moe_lora_workspace_bytes(T: int, d: int, r: int) -> int:

@@ -55,6 +55,38 @@ struct QkAppendArgs : AppendArgs {
 };
 cudaError_t launch_qk_norm_append(const QkAppendArgs& a, cudaStream_t s);
 
+// What the calls on pages have in common: the requests' tokens and their table.
+struct PageArgs {
+    const int32_t* table;
+    long long table_ld;
+    int B, max_pages, page_size;
+    const int32_t* seq_lens;
+    int32_t* status;
+};
+struct BoundsArgs : PageArgs {
+    moe_kv_cache c;
+    void* bounds;
+    const int32_t* first;      // null: from the first token on
+};
+struct ScoresArgs : PageArgs {
+    moe_kv_cache c;
+    const void* q;
+    long long q_bs, q_hs;
+    int q_dt, group;           // group = q_heads / c.heads
+    const void* bounds;
+    float* scores;
+};
+struct SelectArgs : PageArgs {
+    const float* scores;
+    int heads, keep, sinks, recent;
+    int cached;                // scores that shared memory holds (set by the launcher)
+    int32_t* tables;
+    int32_t* lens;
+};
+cudaError_t launch_page_bounds(const BoundsArgs& a, cudaStream_t s);
+cudaError_t launch_page_scores(const ScoresArgs& a, cudaStream_t s);
+cudaError_t launch_page_select(const SelectArgs& a, cudaStream_t s);
+
 struct AttnArgs {
     const void* q;
     void* out;
@@ -78,6 +110,8 @@ struct AttnArgs {
 size_t attn_workspace_bytes(int B, int q_heads, int heads, int head_dim, size_t* done_off, size_t* group_off,
                             size_t* parts_off);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
+// B requests and heads, each with a table and a length of its own.
+cudaError_t launch_attn_pages(const AttnArgs& a, cudaStream_t s);
 
 struct LoraArgs {
     const void* x;

@@ -84,6 +84,55 @@ int append_args(moe::AppendArgs& a, const char* who, const void* k, int64_t k_to
     return MOE_OK;
 }
 
+// The arguments of an attention, checked; a table and a length per request.
+int attn_args(moe::AttnArgs& a, const char* who, const void* q, int q_dtype, int64_t q_batch_stride, int64_t q_head_stride,
+              int B, int q_heads, const moe_kv_cache* cache, const int32_t* block_table, int64_t table_ld, int max_pages,
+              const int32_t* seq_lens, float scale, int window, float softcap, void* out, int out_dtype,
+              int64_t out_batch_stride, int64_t out_head_stride, float* lse, void* ws, size_t ws_bytes) {
+    int rc = check_cache(cache, who);
+    if (rc) return rc;
+    if (!is_act(q_dtype) || !is_act(out_dtype))
+        return api_fail(MOE_ERR_UNSUPPORTED, "%s: dtypes q %d, out %d", who, q_dtype, out_dtype);
+    if (B < 0 || q_heads < 1 || q_heads % cache->heads != 0)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: need B >= 0 and q_heads a multiple of the cache's %d heads (B=%d q_heads=%d)",
+                        who, cache->heads, B, q_heads);
+    if (max_pages < 0 || table_ld < max_pages || window < 0 || !(softcap >= 0.0f) || std::isinf(softcap) || !std::isfinite(scale))
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: need max_pages >= 0, table_ld >= max_pages, window >= 0, a finite softcap >= 0 and scale",
+                        who);
+    if (B == 0) return MOE_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || (q_batch_stride | q_head_stride | out_batch_stride | out_head_stride) % 8 != 0)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: q or out null or unaligned, or a stride no multiple of 8", who);
+    if ((!block_table && max_pages > 0) || !seq_lens) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+    size_t done_off, group_off, parts_off;
+    const size_t need = moe::attn_workspace_bytes(B, q_heads, cache->heads, cache->head_dim, &done_off, &group_off, &parts_off);
+    if (!ws || !aligned16(ws)) return api_fail(MOE_ERR_INVALID_ARG, "%s: workspace null or unaligned", who);
+    if (ws_bytes < need) return api_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu required", who, ws_bytes, need);
+    a.q = q; a.out = out; a.lse = lse;
+    a.q_bs = q_batch_stride; a.q_hs = q_head_stride; a.o_bs = out_batch_stride; a.o_hs = out_head_stride;
+    a.q_dt = q_dtype; a.o_dt = out_dtype; a.B = B; a.q_heads = q_heads; a.group = q_heads / cache->heads;
+    a.c = *cache;
+    a.table = block_table; a.table_ld = table_ld; a.max_pages = max_pages; a.seq_lens = seq_lens;
+    a.scale = scale; a.softcap = softcap; a.window = window;
+    a.status = static_cast<int32_t*>(ws);
+    a.done = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + done_off);
+    a.group_done = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + group_off);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + parts_off);
+    return MOE_OK;
+}
+
+// The requests' lengths and table, checked.
+int page_args(moe::PageArgs& a, const char* who, const int32_t* block_table, int64_t table_ld, int max_pages, int B,
+              const int32_t* seq_lens, int page_size, int32_t* status) {
+    if (B < 0 || max_pages < 0 || table_ld < max_pages)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: need B, max_pages >= 0 and table_ld >= max_pages (%d, %d, %lld)", who, B, max_pages,
+                        (long long)table_ld);
+    if (B == 0) return MOE_OK;
+    if ((!block_table && max_pages > 0) || !seq_lens) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+    a.table = block_table; a.table_ld = table_ld; a.max_pages = max_pages; a.B = B; a.seq_lens = seq_lens;
+    a.page_size = page_size; a.status = status;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -183,36 +232,79 @@ int moe_attn_decode(const void* q, int q_dtype, int64_t q_batch_stride, int64_t 
                     float softcap, void* out, int out_dtype, int64_t out_batch_stride,
                     int64_t out_head_stride, float* lse, void* ws, size_t ws_bytes, void* stream) {
     const char* who = "moe_attn_decode";
+    moe::AttnArgs a = {};
+    const int rc = attn_args(a, who, q, q_dtype, q_batch_stride, q_head_stride, B, q_heads, cache, block_table, table_ld,
+                             max_pages, seq_lens, scale, window, softcap, out, out_dtype, out_batch_stride,
+                             out_head_stride, lse, ws, ws_bytes);
+    if (rc || B == 0) return rc;
+    return launched(moe::launch_attn_decode(a, as_stream(stream)), who);
+}
+
+int moe_attn_pages(const void* q, int q_dtype, int64_t q_batch_stride, int64_t q_head_stride, int B,
+                   int q_heads, const moe_kv_cache* cache, const int32_t* tables, int max_pages,
+                   const int32_t* lens, float scale, float softcap, void* out, int out_dtype,
+                   int64_t out_batch_stride, int64_t out_head_stride, float* lse, void* ws,
+                   size_t ws_bytes, void* stream) {
+    const char* who = "moe_attn_pages";
+    moe::AttnArgs a = {};
+    const int rc = attn_args(a, who, q, q_dtype, q_batch_stride, q_head_stride, B, q_heads, cache, tables, max_pages,
+                             max_pages, lens, scale, 0, softcap, out, out_dtype, out_batch_stride, out_head_stride, lse,
+                             ws, ws_bytes);
+    if (rc || B == 0) return rc;
+    if ((long long)B * cache->heads > INT_MAX)
+        return api_fail(MOE_ERR_UNSUPPORTED, "%s: B=%d requests of %d heads exceed 2^31 tables", who, B, cache->heads);
+    a.B = B * cache->heads;
+    return launched(moe::launch_attn_pages(a, as_stream(stream)), who);
+}
+
+int moe_page_bounds(const moe_kv_cache* cache, void* bounds, const int32_t* block_table, int64_t table_ld,
+                    int max_pages, int B, const int32_t* seq_lens, const int32_t* first, int32_t* status,
+                    void* stream) {
+    const char* who = "moe_page_bounds";
+    moe::BoundsArgs a = {};
+    int rc = check_cache(cache, who);
+    if (rc || (rc = page_args(a, who, block_table, table_ld, max_pages, B, seq_lens, cache->page_size, status)) || B == 0) return rc;
+    if (!bounds || !aligned16(bounds)) return api_fail(MOE_ERR_INVALID_ARG, "%s: bounds null or unaligned", who);
+    a.c = *cache; a.bounds = bounds; a.first = first;
+    return launched(moe::launch_page_bounds(a, as_stream(stream)), who);
+}
+
+int moe_page_scores(const void* q, int q_dtype, int64_t q_batch_stride, int64_t q_head_stride, int B,
+                    int q_heads, const moe_kv_cache* cache, const void* bounds,
+                    const int32_t* block_table, int64_t table_ld, int max_pages, const int32_t* seq_lens,
+                    float* scores, int32_t* status, void* stream) {
+    const char* who = "moe_page_scores";
+    moe::ScoresArgs a = {};
     int rc = check_cache(cache, who);
     if (rc) return rc;
-    if (!is_act(q_dtype) || !is_act(out_dtype))
-        return api_fail(MOE_ERR_UNSUPPORTED, "%s: dtypes q %d, out %d", who, q_dtype, out_dtype);
-    if (B < 0 || q_heads < 1 || q_heads % cache->heads != 0)
-        return api_fail(MOE_ERR_INVALID_ARG, "%s: need B >= 0 and q_heads a multiple of the cache's %d heads (B=%d q_heads=%d)",
-                        who, cache->heads, B, q_heads);
-    if (max_pages < 0 || table_ld < max_pages || window < 0 || !(softcap >= 0.0f) || std::isinf(softcap) || !std::isfinite(scale))
-        return api_fail(MOE_ERR_INVALID_ARG, "%s: need max_pages >= 0, table_ld >= max_pages, window >= 0, a finite softcap >= 0 and scale",
-                        who);
-    if (B == 0) return MOE_OK;
-    if (!q || !out || !aligned16(q) || !aligned16(out) || (q_batch_stride | q_head_stride | out_batch_stride | out_head_stride) % 8 != 0)
-        return api_fail(MOE_ERR_INVALID_ARG, "%s: q or out null or unaligned, or a stride no multiple of 8", who);
-    if (!block_table || !seq_lens) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
-    size_t done_off, group_off, parts_off;
-    const size_t need = moe::attn_workspace_bytes(B, q_heads, cache->heads, cache->head_dim, &done_off, &group_off, &parts_off);
-    if (!ws || !aligned16(ws)) return api_fail(MOE_ERR_INVALID_ARG, "%s: workspace null or unaligned", who);
-    if (ws_bytes < need) return api_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu required", who, ws_bytes, need);
-    moe::AttnArgs a = {};
-    a.q = q; a.out = out; a.lse = lse;
-    a.q_bs = q_batch_stride; a.q_hs = q_head_stride; a.o_bs = out_batch_stride; a.o_hs = out_head_stride;
-    a.q_dt = q_dtype; a.o_dt = out_dtype; a.B = B; a.q_heads = q_heads; a.group = q_heads / cache->heads;
-    a.c = *cache;
-    a.table = block_table; a.table_ld = table_ld; a.max_pages = max_pages; a.seq_lens = seq_lens;
-    a.scale = scale; a.softcap = softcap; a.window = window;
-    a.status = static_cast<int32_t*>(ws);
-    a.done = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + done_off);
-    a.group_done = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + group_off);
-    a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + parts_off);
-    return launched(moe::launch_attn_decode(a, as_stream(stream)), who);
+    if (!is_act(q_dtype)) return api_fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d of q", who, q_dtype);
+    if (q_heads < 1 || q_heads % cache->heads != 0)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: need q_heads a multiple of the cache's %d heads (q_heads=%d)", who, cache->heads, q_heads);
+    if ((rc = page_args(a, who, block_table, table_ld, max_pages, B, seq_lens, cache->page_size, status)) || B == 0) return rc;
+    if (!q || !aligned16(q) || (q_batch_stride | q_head_stride) % 8 != 0)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: q null or unaligned, or a stride no multiple of 8", who);
+    if (!bounds || !aligned16(bounds)) return api_fail(MOE_ERR_INVALID_ARG, "%s: bounds null or unaligned", who);
+    if (!scores && max_pages > 0) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+    a.c = *cache; a.q = q; a.q_bs = q_batch_stride; a.q_hs = q_head_stride; a.q_dt = q_dtype;
+    a.group = q_heads / cache->heads; a.bounds = bounds; a.scores = scores;
+    return launched(moe::launch_page_scores(a, as_stream(stream)), who);
+}
+
+int moe_page_select(const float* scores, int B, int heads, const int32_t* block_table, int64_t table_ld,
+                    int max_pages, const int32_t* seq_lens, int page_size, int keep, int sinks, int recent,
+                    int32_t* tables, int32_t* lens, void* stream) {
+    const char* who = "moe_page_select";
+    if (heads < 1 || page_size < 1 || keep < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
+        return api_fail(MOE_ERR_INVALID_ARG, "%s: need heads, page_size, keep >= 1 and sinks, recent >= 0, at most keep together (%d, %d, %d, %d, %d)",
+                        who, heads, page_size, keep, sinks, recent);
+    moe::SelectArgs a = {};
+    int rc = page_args(a, who, block_table, table_ld, max_pages, B, seq_lens, page_size, nullptr);
+    if (rc || B == 0) return rc;
+    if ((long long)B * heads > INT_MAX)
+        return api_fail(MOE_ERR_UNSUPPORTED, "%s: B=%d requests of %d heads exceed 2^31 tables", who, B, heads);
+    if ((!scores && max_pages > 0) || !tables || !lens) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+    a.scores = scores; a.heads = heads; a.keep = keep; a.sinks = sinks; a.recent = recent; a.tables = tables; a.lens = lens;
+    return launched(moe::launch_page_select(a, as_stream(stream)), who);
 }
 
 size_t moe_lora_workspace_bytes(int T, int d, int r) {

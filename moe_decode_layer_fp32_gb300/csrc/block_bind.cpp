@@ -21,7 +21,11 @@ decltype(&moe_kv_append) g_append = nullptr;
 decltype(&moe_qk_norm_append) g_qk_append = nullptr;
 decltype(&moe_attn_decode) g_attn = nullptr;
 decltype(&moe_lora_project) g_lora = nullptr;
-constexpr int kFunctions = 5;
+decltype(&moe_page_bounds) g_bounds = nullptr;
+decltype(&moe_page_scores) g_scores = nullptr;
+decltype(&moe_page_select) g_select = nullptr;
+decltype(&moe_attn_pages) g_attn_pages = nullptr;
+constexpr int kFunctions = 9;
 PyObject* g_on_error = nullptr;      // (name, code) -> raises
 PyTypeObject* g_cache_type = nullptr;
 PyObject* g_address = nullptr;       // "address"
@@ -383,6 +387,98 @@ PyObject* py_attn(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
     });
 }
 
+// [B, heads, n] int32, contiguous.
+const int32_t* tables_of(PyObject* o, int B, int heads, int& n) {
+    const at::Tensor& t = tensor(o, "tables");
+    if (t.dim() != 3) refuse("tables: expected [requests, heads, pages]");
+    n = size32(t.size(2), "tables");
+    return static_cast<const int32_t*>(exactly(o, "tables", at::kInt, {B, heads, n}));
+}
+
+PyObject* py_attn_pages(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    static Signature<9> sig = {"moe_attn_pages", {"q", "cache", "tables", "lens", "scale", "out", "ws", "softcap", "lse"}, 7};
+    return guarded([&] {
+        PyObject* a[9];
+        sig.parse(args, nargs, kwnames, a);
+        const moe_kv_cache* c = cache_of(a[1]);
+        const at::Tensor& qt = tensor(a[0], "q");
+        if (qt.dim() != 3) refuse("q: expected [B, q_heads, D]");
+        const int B = size32(qt.size(0), "q"), hq = size32(qt.size(1), "q"), D = c->head_dim;
+        const Heads q = heads(a[0], "q", B, hq, D), o = heads(a[5], "out", B, hq, D);
+        int n;
+        const int32_t* tables = tables_of(a[2], B, c->heads, n);
+        auto* lens = static_cast<const int32_t*>(exactly(a[3], "lens", at::kInt, {B, c->heads}));
+        auto* lse = static_cast<float*>(exactly(a[8], "lse", at::kFloat, {B, hq}));
+        const Workspace ws = workspace(a[6]);
+        return done("moe_attn_pages",
+                    g_attn_pages(q.p, q.code, q.outer, q.inner, B, hq, c, tables, n, lens, (float)number(a[4], 0.0),
+                                 (float)number(a[7], 0.0), o.p, o.code, o.outer, o.inner, lse, ws.p, ws.bytes, stream()));
+    });
+}
+
+// [num_pages, heads, 2, D] of the cache's type, contiguous.
+void* bounds_of(PyObject* o, const moe_kv_cache* c) {
+    const at::ScalarType type = c->dtype == MOE_DTYPE_FP8_E4M3 ? at::kFloat8_e4m3fn : at::kBFloat16;
+    if (!given(o)) refuse("bounds: expected a tensor");
+    return exactly(o, "bounds", type, {c->num_pages, c->heads, 2, c->head_dim});
+}
+
+PyObject* py_page_bounds(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    static Signature<6> sig = {"moe_page_bounds", {"cache", "bounds", "block_table", "seq_lens", "first", "status"}, 4};
+    return guarded([&] {
+        PyObject* a[6];
+        sig.parse(args, nargs, kwnames, a);
+        const moe_kv_cache* c = cache_of(a[0]);
+        void* bounds = bounds_of(a[1], c);
+        const Table t = table(a[2]);
+        auto* lens = static_cast<const int32_t*>(exactly(a[3], "seq_lens", at::kInt, {t.R}));
+        auto* first = static_cast<const int32_t*>(exactly(a[4], "first", at::kInt, {t.R}));
+        auto* st = static_cast<int32_t*>(exactly(a[5], "status", at::kInt, {1}));
+        return done("moe_page_bounds", g_bounds(c, bounds, t.p, t.ld, t.pages, t.R, lens, first, st, stream()));
+    });
+}
+
+PyObject* py_page_scores(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    static Signature<7> sig = {"moe_page_scores", {"q", "cache", "bounds", "block_table", "seq_lens", "scores", "status"}, 6};
+    return guarded([&] {
+        PyObject* a[7];
+        sig.parse(args, nargs, kwnames, a);
+        const moe_kv_cache* c = cache_of(a[1]);
+        const at::Tensor& qt = tensor(a[0], "q");
+        if (qt.dim() != 3) refuse("q: expected [B, q_heads, D]");
+        const int B = size32(qt.size(0), "q"), hq = size32(qt.size(1), "q");
+        const Heads q = heads(a[0], "q", B, hq, c->head_dim);
+        void* bounds = bounds_of(a[2], c);
+        const Table t = table(a[3]);
+        if (t.R != B) refuse("block_table must have a row per request");
+        auto* lens = static_cast<const int32_t*>(exactly(a[4], "seq_lens", at::kInt, {B}));
+        auto* scores = static_cast<float*>(exactly(a[5], "scores", at::kFloat, {B, c->heads, t.pages}));
+        auto* st = static_cast<int32_t*>(exactly(a[6], "status", at::kInt, {1}));
+        return done("moe_page_scores",
+                    g_scores(q.p, q.code, q.outer, q.inner, B, hq, c, bounds, t.p, t.ld, t.pages, lens, scores, st, stream()));
+    });
+}
+
+PyObject* py_page_select(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    static Signature<8> sig = {"moe_page_select",
+                               {"scores", "block_table", "seq_lens", "page_size", "tables", "lens", "sinks", "recent"}, 6};
+    return guarded([&] {
+        PyObject* a[8];
+        sig.parse(args, nargs, kwnames, a);
+        const Table t = table(a[1]);
+        const at::Tensor& st = tensor(a[0], "scores");
+        if (st.dim() != 3) refuse("scores: expected [B, heads, pages]");
+        const int heads = size32(st.size(1), "scores");
+        auto* scores = static_cast<const float*>(exactly(a[0], "scores", at::kFloat, {t.R, heads, t.pages}));
+        auto* seq = static_cast<const int32_t*>(exactly(a[2], "seq_lens", at::kInt, {t.R}));
+        int keep;
+        auto* tables = const_cast<int32_t*>(tables_of(a[4], t.R, heads, keep));
+        auto* lens = static_cast<int32_t*>(exactly(a[5], "lens", at::kInt, {t.R, heads}));
+        return done("moe_page_select", g_select(scores, t.R, heads, t.p, t.ld, t.pages, seq, integer(a[3], 0), keep,
+                                                integer(a[6], 0), integer(a[7], 0), tables, lens, stream()));
+    });
+}
+
 PyObject* py_lora(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
     static Signature<8> sig = {"moe_lora_project", {"x", "w", "y", "ws", "lora", "adapter", "x_scale", "w_scale"}, 4};
     return guarded([&] {
@@ -437,6 +533,10 @@ PyObject* py_bind(PyObject*, PyObject* args) {
     g_attn = reinterpret_cast<decltype(g_attn)>(f[2]);
     g_lora = reinterpret_cast<decltype(g_lora)>(f[3]);
     g_qk_append = reinterpret_cast<decltype(g_qk_append)>(f[4]);
+    g_bounds = reinterpret_cast<decltype(g_bounds)>(f[5]);
+    g_scores = reinterpret_cast<decltype(g_scores)>(f[6]);
+    g_select = reinterpret_cast<decltype(g_select)>(f[7]);
+    g_attn_pages = reinterpret_cast<decltype(g_attn_pages)>(f[8]);
     Py_INCREF(on_error);
     Py_XSETREF(g_on_error, on_error);
     Py_INCREF(cache_type);
@@ -451,6 +551,10 @@ PyMethodDef kMethods[] = {
     {"moe_attn_decode", FAST(py_attn), "moe_attn_decode of include/moe_block.h"},
     {"moe_lora_project", FAST(py_lora), "moe_lora_project of include/moe_block.h"},
     {"moe_qk_norm_append", FAST(py_qk_append), "moe_qk_norm_append of include/moe_block.h"},
+    {"moe_page_bounds", FAST(py_page_bounds), "moe_page_bounds of include/moe_block.h"},
+    {"moe_page_scores", FAST(py_page_scores), "moe_page_scores of include/moe_block.h"},
+    {"moe_page_select", FAST(py_page_select), "moe_page_select of include/moe_block.h"},
+    {"moe_attn_pages", FAST(py_attn_pages), "moe_attn_pages of include/moe_block.h"},
     {"bind", py_bind, METH_VARARGS, "addresses of the library's functions, and what they need of Python"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_block_bind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -133,3 +133,34 @@ def rotate_axes(v, positions, cos_sin, axis_positions, axis):
         v[t, :, :half] = a * c - b * s
         v[t, :, half:2 * half] = b * c + a * s
     return v
+
+
+def page_bounds(rows, page_size, first, n):
+    """{column: (lo, hi)} of the pages with tokens first .. n - 1; rows [n, heads, D] are the keys of tokens 0 .. n - 1."""
+    out = {}
+    for col in range(max(first, 0) // page_size, -(-n // page_size)) if first < n else ():
+        r = rows[col * page_size:min(n, (col + 1) * page_size)]
+        out[col] = r.min(0).values, r.max(0).values
+    return out
+
+
+def page_scores(q, lo, hi):
+    """(scores, size) [heads, pages] of one request: q [hq, D]; lo, hi [pages, heads, D].  ``size`` is the sum
+    of the absolute values of what is added up."""
+    q, lo, hi = f64(q), f64(lo), f64(hi)
+    pages, heads, D = lo.shape
+    s, size = torch.zeros(heads, pages, dtype=torch.float64), torch.zeros(heads, pages, dtype=torch.float64)
+    for h in range(q.shape[0]):
+        g = h // (q.shape[0] // heads)
+        best = torch.maximum(q[h] * lo[:, g], q[h] * hi[:, g])
+        s[g] += best.sum(1)
+        size[g] += best.abs().sum(1)
+    return s, size
+
+
+def page_select(scores, pages, keep, sinks, recent):
+    """Columns kept of one request's ``pages`` by one head's scores (a list), in order."""
+    must = {j for j in range(pages) if j < sinks or j >= pages - recent}
+    rank = sorted((j for j in range(pages) if j not in must),
+                  key=lambda j: (0 if math.isnan(scores[j]) else 1, 0.0 if math.isnan(scores[j]) else -scores[j], j))
+    return sorted(must | set(rank[:max(0, keep - len(must))]))
