@@ -2,6 +2,7 @@
 // of a page (bounds), from them a bound on what a page can score (scores), and the best pages (select).
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include <math_constants.h>
 
@@ -163,123 +164,282 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsBlocks) page_bounds_ker
 //
 // sum over the heads h of a group of sum_d max(q_hd lo_d, q_hd hi_d) is one product of length 2 D,
 //   sum_d (sum_h min(q_hd, 0)) lo_d + (sum_h max(q_hd, 0)) hi_d,
-// as lo <= hi: two additions and multiplications per value read, and memory bounds it.  Units are
-// (request, key-value head, page); a warp takes a run of them, the sums of q in its registers, L lanes to a
-// page's 2 D values and 8 pages under way per lane.
-constexpr int kScoreThreads = 256;
-constexpr int kScorePages = 8;              // of a lane at a time
+// as lo <= hi: an addition and a multiplication per value read, and memory bounds it if the instructions
+// per value are few.  So the tensor cores multiply: 8 pages are the columns of an MMA, and its rows the sums of q as
+// three terms of bf16 (of f16 next to E4M3 bounds, which it holds: the E4M3 form of the instruction converts both
+// operands each time, 12 conversions where 4 do), 24 bits of them and more.
+// A lane reads 16 bytes of its page at a time, in any order of d, as a dot product does not mind it.
+// Every warp works alone on a run of batches of one or several heads, with the rows of the next batches on their way
+// into shared memory, a lane's pieces into places of its own; where a head begins the warp forms its terms of q
+// meanwhile.
+constexpr int kScoreThreads = 128;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreBlocks = 3;             // per SM
+constexpr int kScoreSetup = 1;              // what the terms of q cost, in batches
 
-template <bool F8, int L, int VL>
-__global__ void __launch_bounds__(kScoreThreads, 2) page_scores_kernel(const __grid_constant__ ScoresArgs a) {
-    constexpr int E = F8 ? 16 : 8, kWarps = kScoreThreads / 32, kSide = 32 / L, kBatch = kScorePages * kSide;
+// 4 JC pieces of 16 bytes: a page's 2 D values, rounded up.  U: 8 U pages are a batch.
+template <bool F8, int JC>
+struct Scores {
+    static constexpr int E = F8 ? 16 : 8, MC = E / 4;        // values of a piece, and its MMAs
+    static constexpr int U = JC >= 8 ? 1 : 2;
+    static constexpr int kBatch = 8 * U;
+    static constexpr int kValues = 4 * JC * E;
+    static constexpr int V = kValues > 256 ? kValues / 32 : 8;   // of a lane, in the terms of q
+    // A fragments of q: for each MMA the words of three terms, 4 lanes, 2 words
+    static constexpr int kWords = JC * MC * 24;
+    static constexpr int kStage = U * JC * 512;              // a warp's
+    static constexpr int kStages = 3;
+    static constexpr int kWarpBytes = kStages * kStage + kWords * 4;
+    static constexpr int kSmem = kScoreWarps * kWarpBytes;
+    static constexpr int kBlocksPerSm = JC >= 16 ? 2 : F8 && JC >= 8 ? 3 : kScoreBlocks;
+    static_assert(kBatch <= 32, "a lane's page");
+    static_assert(kBlocksPerSm * (kSmem + 1280) <= 228 * 1024, "blocks that run at once");
+};
+
+// max(x, 0) of two bf16 and of an fp32; NaN stays NaN.
+__device__ __forceinline__ uint32_t relu_bf16x2(uint32_t x) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0u));
+    return r;
+}
+__device__ __forceinline__ float relu_f32(float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(0.0f));
+    return r;
+}
+
+template <bool F8, int JC>
+__global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm)) page_scores_kernel(const __grid_constant__ ScoresArgs a) {
+    using K = Scores<F8, JC>;
+    constexpr int E = K::E, U = K::U, kBatch = K::kBatch, V = K::V;
+    extern __shared__ __align__(16) char smem[];
     __shared__ LineShared<kScoreThreads> sh;
+    const int heads = a.c.heads, D = a.c.head_dim, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pieces = 2 * D / E;
+    char* ring = smem + warp * K::kWarpBytes;
+    uint32_t* frag = reinterpret_cast<uint32_t*>(ring + K::kStages * K::kStage);
     pdl_allow_dependents();
     pdl_wait_primary();
     report_lengths(a);
-    const int heads = a.c.heads, D = a.c.head_dim, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int side = lane / L, at0 = lane % L, vecs = 2 * D / E;
     auto pages = [&](int b) { return pages_of(tokens_of(a, b), a.page_size); };
-    auto count = [&](int b) { return (long long)pages(b) * heads; };
+    auto batches = [&](int np) { return np > 0 ? (np - 1) / kBatch + 1 : 0; };
+    // a head's batches, and what its queries cost before the first one
+    auto count = [&](int b) {
+        const int nb = batches(pages(b));
+        return nb > 0 ? (long long)(nb + kScoreSetup) * heads : 0;
+    };
     long long total;
-    Stretch s = line_share<kScoreThreads>(a.B, count, [&](long long t) { return (t + kWarps * kBatch - 1) / (kWarps * kBatch); }, sh, total);
-    // the warp's part, in whole batches
-    const long long per = ((s.n + kWarps - 1) / kWarps + kBatch - 1) / kBatch * kBatch, whole = s.n;
-    s.skip(min(warp * per, whole), count);
-    s.n = min(per, whole - warp * per);
-    while (s.n > 0) {
-        const int b = s.b, np = pages(b), g = (int)div_u(s.at, np);
-        int col = (int)(s.at - (long long)g * np);
-        const int end = (int)min((long long)np, col + s.n);
-        // the sums of q that go with the lane's values
-        float q[VL][E];
-        const float ks = a.c.k_scale ? a.c.k_scale[g] : 1.0f;
+    // a batch to each warp at least
+    Stretch s = line_share<kScoreThreads>(a.B, count, [&](long long t) { return (t + kScoreWarps - 1) / kScoreWarps; }, sh, total);
+    // the warp's part
+    const long long from_unit = s.n * warp / kScoreWarps, to_unit = s.n * (warp + 1) / kScoreWarps;
+    s.skip(from_unit, count);
+    struct Walk {
+        int b, g, np, nb;
+        int n, last;              // the head's batches of the run
+        long long left;           // units of the run behind this head
+    };
+    auto take = [&](Walk& w, int r) {
+        const int units = (int)min((long long)(w.nb + kScoreSetup - r), w.left);
+        w.left -= units;
+        w.n = max(r - kScoreSetup, 0);
+        w.last = max(r + units - kScoreSetup, 0);
+    };
+    // to the run's next head with batches
+    auto next_head = [&](Walk& w) {
+        do {
+            if (w.left <= 0) return false;
+            if (++w.g == heads) {
+                w.g = 0;
+                do w.np = pages(++w.b);
+                while (w.np == 0);
+                w.nb = batches(w.np);
+            }
+            take(w, 0);
+        } while (w.n >= w.last);
+        return true;
+    };
+    Walk here = {s.b, 0, 0, 0, 0, 0, to_unit - from_unit};
+    if (here.left <= 0) return;
+    here.np = pages(here.b);
+    here.nb = batches(here.np);
+    here.g = (int)div_u(s.at, here.nb + kScoreSetup);
+    take(here, (int)(s.at - (long long)here.g * (here.nb + kScoreSetup)));
+    if (here.n >= here.last && !next_head(here)) return;
+    // ---- the copies, K::kStages - 1 batches ahead
+    Walk ahead = here;
+    bool more = true;
+    int stage_in = 0;
+    const uint32_t place = smem_u32(ring) + lane * 16;
+    const long long page_bytes = (long long)heads * pieces * 16;
+    auto ask = [&]() {
+        const int col = ahead.n * kBatch + lane;
+        return lane < kBatch && col < ahead.np ? max(a.table[ahead.b * a.table_ld + col], -1) : INT_MIN;
+    };
+    int id_next = ask(), ids[K::kStages];          // pages of the batches under way, a lane each (INT_MIN: none, -1: no such)
+    auto feed = [&](int& id) {
+        id = INT_MIN;
+        if (!more) return;
+        id = id_next;
+        const int g = ahead.g;
+        if (++ahead.n >= ahead.last) more = next_head(ahead);
+        if (more) id_next = ask();
+        if (id != INT_MIN && (id < 0 || id >= a.c.num_pages)) {
+            if (a.status) set_status(a.status, MOE_ERR_DEVICE);
+            id = -1;
+        }
+        __syncwarp();
 #pragma unroll
-        for (int v = 0; v < VL; ++v) {
-            const int vec = at0 + v * L, d = vec * E;
-            const bool low = d < D;
+        for (int u = 0; u < U; ++u) {
+            // a page that is not there has another's values, and pieces behind the last one its first: they
+            // meet terms of 0, or nobody looks at the sum
+            const int page = max(__shfl_sync(0xffffffffu, id, u * 8 + lane / 4), 0);
+            const char* from = static_cast<const char*>(a.bounds) + page * page_bytes + (g * pieces + lane % 4) * 16;
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[v][e] = 0.0f;
-            for (int h = 0; vec < vecs && h < a.group; ++h) {
-                const long long i = b * a.q_bs + (g * a.group + h) * a.q_hs + (low ? d : d - D);
+            for (int j = 0; j < JC; ++j)
+                cp_async16_to(place + stage_in * K::kStage + (u * JC + j) * 512, from + (4 * j + lane % 4 < pieces ? 64 * j : 0));
+        }
+        stage_in = stage_in + 1 == K::kStages ? 0 : stage_in + 1;
+    };
 #pragma unroll
-                for (int j = 0; j < E; j += 8) {
-                    float f[8];
-                    load8_f32(a.q, a.q_dt, i + j, f);
-                    // NaN goes into both
+    for (int i = 0; i < K::kStages - 1; ++i) {
+        feed(ids[i]);
+        cp_async_commit();
+    }
+    // ---- the products
+    // the rows of terms; those behind the last have it again, and count for nothing
+    const uint32_t* mine = frag + min(lane / 4, 2) * 8 + lane % 4 * 2;
+    const float part = lane < 12 ? 1.0f : 0.0f;
+    int stage = 0;
+    do {
+        // the sums of q: V of the 2 D values to a lane, eight query heads' loads together (the type is asked outside the
+        // loop); the lower side's with its sign turned
+        float q[V] = {};
+        auto add = [&](auto dt) {
+            constexpr bool BF = decltype(dt)::value == MOE_DTYPE_BF16;
+            constexpr int N = BF ? 1 : 2;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) q[v][j + e] += (low ? f[e] > 0.0f : f[e] < 0.0f) ? 0.0f : f[e];
+            for (int v = 0; v < V; v += 8) {
+                const int d = lane * V + v;
+                const uint32_t turn = d < D ? BF ? 0x80008000u : 0x80000000u : 0u;
+                const char* from = static_cast<const char*>(a.q) + (here.b * a.q_bs + here.g * a.group * a.q_hs + (d < D ? d : d - D)) * (2 * N);
+                for (int h0 = 0; d < 2 * D && h0 < a.group; h0 += 8) {
+                    uint4 w[8][N];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+#pragma unroll
+                        for (int c = 0; c < N; ++c)
+                            w[k][c] = h0 + k < a.group ? reinterpret_cast<const uint4*>(from + (h0 + k) * a.q_hs * (2 * N))[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+#pragma unroll
+                        for (int c = 0; c < N; ++c) {
+                            const uint32_t x[4] = {w[k][c].x ^ turn, w[k][c].y ^ turn, w[k][c].z ^ turn, w[k][c].w ^ turn};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (BF) {
+                                    const uint32_t y = relu_bf16x2(x[i]);
+                                    q[v + 2 * i] += __uint_as_float(y << 16);
+                                    q[v + 2 * i + 1] += __uint_as_float(y & 0xffff0000u);
+                                } else {
+                                    q[v + c * 4 + i] += relu_f32(__uint_as_float(x[i]));
+                                }
+                            }
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[v + e] = d < D ? -q[v + e] : q[v + e];
+            }
+        };
+        if (a.q_dt == MOE_DTYPE_BF16) add(std::integral_constant<int, MOE_DTYPE_BF16>());
+        else add(std::integral_constant<int, MOE_DTYPE_F32>());
+        float back = a.c.k_scale ? a.c.k_scale[here.g] : 1.0f;
+        if constexpr (F8) {
+            // a power of two brings the greatest between 2^14 and 2^15: f16 holds it, and 2^-38 of it
+            float most = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) most = fmaxf(most, fabsf(q[e]));
+            __syncwarp();
+            const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23, up = min(268 - e, 253u);
+            back *= __uint_as_float((254 - up) << 23);
+#pragma unroll
+            for (int v = 0; v < V; ++v) q[v] *= __uint_as_float(up << 23);
+        }
+        __syncwarp();       // the terms of the head before have been read
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const int at = lane * V + v, piece = at / E;
+            if (at >= K::kValues) break;
+            uint32_t* to = frag + (piece / 4 * K::MC + at % E / 4) * 24 + piece % 4 * 2 + at % 4 / 2;
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                if constexpr (F8) {
+                    const uint32_t w = pack_f16x2(q[v], q[v + 1]);
+                    const float2 have = unpack_f16x2(w);
+                    to[t * 8] = w;
+                    q[v] -= have.x;
+                    q[v + 1] -= have.y;
+                } else {
+                    to[t * 8] = pack_hi(q[v], q[v + 1]);
+                    q[v] -= bf16_trunc(q[v]);
+                    q[v + 1] -= bf16_trunc(q[v + 1]);
                 }
             }
         }
-        const int32_t* row = a.table + b * a.table_ld;
-        float* out = a.scores + ((long long)b * heads + g) * a.max_pages;
-        auto ids = [&](int c) { return lane < kBatch && c + lane < end ? max(row[c + lane], -1) : INT_MIN; };
-        int id = ids(col);
-        s.skip(end - col, count);
-        for (; col < end; col += kBatch) {
-            const int next = ids(col + kBatch);
-            if (id != INT_MIN && (id < 0 || id >= a.c.num_pages)) {
-                if (a.status) set_status(a.status, MOE_ERR_DEVICE);
-                id = -1;
-            }
-            __syncwarp();
-            uint4 w[kScorePages][VL];
+        __syncwarp();
+        float* out = a.scores + ((long long)here.b * heads + here.g) * a.max_pages;
+        for (; here.n < here.last; ++here.n) {
+            cp_async_wait<K::kStages - 2>();
+            const int had = ids[0];
 #pragma unroll
-            for (int u = 0; u < kScorePages; ++u) {
-                const int page = __shfl_sync(0xffffffffu, id, u * kSide + side);
-                const char* from = static_cast<const char*>(a.bounds) + ((long long)page * heads + g) * vecs * 16;
+            for (int i = 0; i + 2 < K::kStages; ++i) ids[i] = ids[i + 1];
+            feed(ids[K::kStages - 2]);
+            cp_async_commit();
+            const char* rows = ring + stage * K::kStage + lane * 16;
+            stage = stage + 1 == K::kStages ? 0 : stage + 1;
+            float c[2][U][4] = {};          // two chains of additions
 #pragma unroll
-                for (int v = 0; v < VL; ++v) {
-                    const int vec = at0 + v * L;
-                    w[u][v] = page >= 0 && vec < vecs ? reinterpret_cast<const uint4*>(from)[vec] : make_uint4(0, 0, 0, 0);
-                }
-            }
-            float sum[kScorePages];
+            for (int j = 0; j < JC; ++j) {
+                uint4 y[U];
 #pragma unroll
-            for (int u = 0; u < kScorePages; ++u) {
-                sum[u] = 0.0f;
+                for (int u = 0; u < U; ++u) y[u] = *reinterpret_cast<const uint4*>(rows + (u * JC + j) * 512);
 #pragma unroll
-                for (int v = 0; v < VL; ++v) {
-                    if constexpr (F8) {
-                        const uint32_t x[4] = {w[u][v].x, w[u][v].y, w[u][v].z, w[u][v].w};
+                for (int i = 0; i < K::MC; ++i) {
+                    const uint2 f = *reinterpret_cast<const uint2*>(mine + (j * K::MC + i) * 24);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 l = unpack_e4m3x2<false>(x[i]), h = unpack_e4m3x2<true>(x[i]);
-                            sum[u] = fmaf(q[v][4 * i], l.x, sum[u]);
-                            sum[u] = fmaf(q[v][4 * i + 1], l.y, sum[u]);
-                            sum[u] = fmaf(q[v][4 * i + 2], h.x, sum[u]);
-                            sum[u] = fmaf(q[v][4 * i + 3], h.y, sum[u]);
-                        }
-                    } else {
-                        float f[8];
-                        unpack_bf16x8(w[u][v], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) sum[u] = fmaf(q[v][e], f[e], sum[u]);
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t x[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+                        if constexpr (F8) mma_f16(c[i % 2][u], f.x, 0u, f.y, 0u, e4m3x2_to_f16x2<false>(x[i]), e4m3x2_to_f16x2<true>(x[i]));
+                        else mma_bf16(c[i % 2][u], f.x, 0u, f.y, 0u, x[2 * i], x[2 * i + 1]);
                     }
                 }
             }
-            // Sums over the L lanes of a page: at the three widest steps a lane keeps half of its pages and
-            // hands on the others, then all lanes of a page add up.
-            int mine = 0;
+            // The rows of terms are 4 lanes apart, and a lane has two pages of each 8: halves of what there is change
+            // hands while there are halves, then all add up.
+            float v[2 * U];
 #pragma unroll
-            for (int n = kScorePages / 2, o = L / 2; n > 0; n /= 2, o /= 2) {
-                const bool up = lane & o;
-                mine += up ? n : 0;
+            for (int i = 0; i < 2 * U; ++i) v[i] = (c[0][i / 2][i % 2] + c[1][i / 2][i % 2]) * part;
+            int which = 0;
 #pragma unroll
-                for (int u = 0; u < kScorePages / 2; ++u) {
-                    if (u >= n) continue;
-                    const float give = up ? sum[u] : sum[u + n], keep = up ? sum[u + n] : sum[u];
-                    sum[u] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            for (int k = U, w = 16; w >= 4; k /= 2, w /= 2) {
+                const bool up = lane & w;
+                if (k > 0) {
+                    which += up ? k : 0;
+#pragma unroll
+                    for (int i = 0; i < k; ++i) {
+                        const float give = up ? v[i] : v[i + k], stay = up ? v[i + k] : v[i];
+                        v[i] = stay + __shfl_xor_sync(0xffffffffu, give, w);
+                    }
+                } else {
+                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
                 }
             }
-            float total_q = sum[0];
-#pragma unroll
-            for (int o = L / 16; o > 0; o /= 2) total_q += __shfl_xor_sync(0xffffffffu, total_q, o);
-            const int at = mine * kSide + side, known = __shfl_sync(0xffffffffu, id, at);
-            if (lane % (L / 8) == 0 && known != INT_MIN) out[col + at] = known < 0 ? -CUDART_INF_F : total_q * ks;
-            id = next;
+            const int at = which / 2 * 8 + lane % 4 * 2 + which % 2, known = __shfl_sync(0xffffffffu, had, at);
+            constexpr int kCopies = U >= 4 ? 0 : U == 2 ? 4 : 12;     // bits of the lanes that have the same
+            if ((lane & kCopies) == 0 && known != INT_MIN) out[here.n * kBatch + at] = known < 0 ? -CUDART_INF_F : v[0] * back;
         }
-    }
+    } while (next_head(here));
+    cp_async_wait<0>();
 }
 
 // ---- select -------------------------------------------------------------------
@@ -407,9 +567,14 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
     }
 }
 
-template <bool F8, int L, int VL>
+template <bool F8, int JC>
 cudaError_t launch_scores_as(const ScoresArgs& a, cudaStream_t s) {
-    return launch_pdl(page_scores_kernel<F8, L, VL>, dim3((unsigned)(2 * device_sm_count())), dim3(kScoreThreads), 0, s, a);
+    using K = Scores<F8, JC>;
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(page_scores_kernel<F8, JC>), K::kSmem, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(page_scores_kernel<F8, JC>, dim3((unsigned)(K::kBlocksPerSm * device_sm_count())), dim3(kScoreThreads),
+                      K::kSmem, s, a);
 }
 
 }  // namespace
@@ -422,10 +587,10 @@ cudaError_t launch_page_bounds(const BoundsArgs& a, cudaStream_t s) {
 cudaError_t launch_page_scores(const ScoresArgs& a, cudaStream_t s) {
     const int D = a.c.head_dim;
     if (a.c.dtype == MOE_DTYPE_FP8_E4M3)
-        return D <= 64 ? launch_scores_as<true, 8, 1>(a, s) : D <= 128 ? launch_scores_as<true, 16, 1>(a, s) : launch_scores_as<true, 32, 1>(a, s);
-    return D <= 32 ? launch_scores_as<false, 8, 1>(a, s)
-           : D <= 64 ? launch_scores_as<false, 16, 1>(a, s)
-           : D <= 128 ? launch_scores_as<false, 32, 1>(a, s) : launch_scores_as<false, 32, 2>(a, s);
+        return D <= 64 ? launch_scores_as<true, 2>(a, s) : D <= 128 ? launch_scores_as<true, 4>(a, s) : launch_scores_as<true, 8>(a, s);
+    return D <= 32 ? launch_scores_as<false, 2>(a, s)
+           : D <= 64 ? launch_scores_as<false, 4>(a, s)
+           : D <= 128 ? launch_scores_as<false, 8>(a, s) : launch_scores_as<false, 16>(a, s);
 }
 
 cudaError_t launch_page_select(const SelectArgs& args, cudaStream_t s) {
