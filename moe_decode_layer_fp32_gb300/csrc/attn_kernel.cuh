@@ -123,12 +123,11 @@ struct Attn {
     static constexpr uint32_t kAllKeys = KT == 32 ? 0xffffffffu : (1u << (KT % 32)) - 1u;
     static constexpr int kChunks = kPitch / 16;                      // 16-byte chunks of a row
     static constexpr int kRowsPerIter = 32 / kChunks;
-    // bf16 queries over an E4M3 cache: q is two E4M3 terms (4 bits each, its 8) and the codes of K go
-    // into the MMA as they are
-    static constexpr bool kQ8 = F8 && !EX;
-    static constexpr int kQTerms = EX ? (F8 ? 2 : 3) : kQ8 ? 2 : 1;
+    // bf16 queries over an E4M3 cache: one f16 term has their 8 bits (down to 2^-22 of a row's greatest, and 2^-33
+    // of it below that)
+    static constexpr int kQTerms = EX ? (F8 ? 2 : 3) : 1;
     static constexpr int kPTerms = EX && !F8 ? 3 : 2;
-    static constexpr int kSteps = kQ8 ? DP / 32 : DP / 16;           // MMAs of q . k along d
+    static constexpr int kSteps = DP / 16;           // MMAs of q . k along d
     static constexpr int kVElems = F8 ? (DP >= 128 ? 16 : 8) : 8;    // columns a thread takes of a V row at once
     static constexpr int kWindows = DP / (8 * kVElems);
     static constexpr int kAccs = DP / 8;                             // n8 tiles of o
@@ -181,7 +180,7 @@ struct Attn {
     // The cursor's key-value head, its rows of that head's group, and its request.
     __device__ static __forceinline__ int head_of(const AttnArgs& a, const Cursor& c, int nsub) {
         if constexpr (HEADS) return (int)((uint32_t)c.b % (uint32_t)a.c.heads);
-        return nsub == 1 ? c.unit : c.unit / nsub;
+        return c.unit / nsub;
     }
     __device__ static __forceinline__ int sub_of(const Cursor& c, int nsub) { return HEADS ? c.unit : c.unit % nsub; }
     __device__ static __forceinline__ int request_of(const AttnArgs& a, int b) {
@@ -229,7 +228,7 @@ struct Attn {
     // mask of the keys that count.  The rows of the others become zeros.
     __device__ static __forceinline__ uint32_t issue(const AttnArgs& a, const Cursor& c, int2 place, int nsub, int lane,
                                                      const Lane& ln, uint32_t stage) {
-        const int g = head_of(a, c, nsub);
+        const int g = !HEADS && nsub == 1 ? c.unit : head_of(a, c, nsub);
         const uint32_t mask = __ballot_sync(0xffffffffu, place.x >= 0);
         if (mask == 0u) return 0u;   // nobody reads the stage
         // offsets in 16-byte steps: 32 bits of them unless a cache tensor passes 64 GB
@@ -335,27 +334,12 @@ struct Attn {
                     for (int i = 0; i < E; ++i) f[j][i] *= up;
             }
             st.qf[rr] = a.scale * (ks * back);   // in this order: a small scale of k goes with a large q
-            if constexpr (kQ8) {
-                // E4M3 has no infinity: a head with one gets NaN
+            // a head with an infinity gets NaN over an E4M3 cache, whatever the codes beside it are
+            if constexpr (F8 && !EX) {
                 if (mx == CUDART_INF_F) st.qf[rr] = CUDART_NAN_F;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float* u = &f[s / 2][(s % 2) * 8 + h * 4];
-                            const uint32_t w = pack_e4m3x4(u[0], u[1], u[2], u[3]);
-                            const float2 lo = unpack_e4m3x2<false>(w), hi = unpack_e4m3x2<true>(w);
-                            u[0] = (u[0] - lo.x) * 16.0f;
-                            u[1] = (u[1] - lo.y) * 16.0f;
-                            u[2] = (u[2] - hi.x) * 16.0f;
-                            u[3] = (u[3] - hi.y) * 16.0f;
-                            st.q[t][rr][s][h] = w;
-                        }
             }
 #pragma unroll
-            for (int t = 0; t < (kQ8 ? 0 : kQTerms); ++t)
+            for (int t = 0; t < kQTerms; ++t)
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
                     const int j = s / (E / 4) % J, i = (s % (E / 4)) * 4;
@@ -400,22 +384,6 @@ struct Attn {
                 // row 8 nt + lane / 4, chunk 4 j + lane % 4
                 const uint4 k4 = lds128(stage + ln.k[j & 1] + nt * 8 * kPitch + (j >> 1) * 128);
                 const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-                if constexpr (kQ8) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t(&q0)[2] = st.q[0][0][j * 2 + i];
-                        const uint32_t(&q1)[2] = st.q[1][0][j * 2 + i];
-                        if constexpr (ROWS == 16) {
-                            const uint32_t(&r0)[2] = st.q[0][1][j * 2 + i];
-                            const uint32_t(&r1)[2] = st.q[1][1][j * 2 + i];
-                            mma_e4m3(c, q0[0], r0[0], q0[1], r0[1], w[2 * i], w[2 * i + 1]);
-                            mma_e4m3(c2, q1[0], r1[0], q1[1], r1[1], w[2 * i], w[2 * i + 1]);
-                        } else {
-                            mma_e4m3(c, q0[0], q1[0], q0[1], q1[1], w[2 * i], w[2 * i + 1]);
-                        }
-                    }
-                    continue;
-                }
                 constexpr int SJ = F8 ? 4 : 2;
 #pragma unroll
                 for (int i = 0; i < SJ; ++i) {
@@ -447,10 +415,7 @@ struct Attn {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 s[nt][0][e] = c[e];
-                if constexpr (kQ8) {
-                    s[nt][0][e] = fmaf(ROWS == 16 ? c2[e] : c[2 + e], 0.0625f, c[e]);
-                    if constexpr (ROWS == 16) s[nt][1][e] = fmaf(c2[2 + e], 0.0625f, c[2 + e]);
-                } else if constexpr (ROWS == 16) s[nt][1][e] = c[2 + e];
+                if constexpr (ROWS == 16) s[nt][1][e] = c[2 + e];
                 // an infinite first term stands: the others' products with it may be NaN
                 else if (kQTerms > 1 && fabsf(c[e]) < CUDART_INF_F) s[nt][0][e] = c[e] + (c[2 + e] + c2[e]);
             }
