@@ -116,19 +116,19 @@ __device__ __forceinline__ void cp_async8(void* dst_smem, const void* src) {
 // Vectors of VEC elements.  A unit is a token and a slice of its heads, nq of q's and nkv of k's and v's to a
 // thread at most; a block takes units blockIdx.x, + gridDim.x, ..., with the next one's rows on their way into
 // shared memory (every thread's own vectors into places of its own) while it works on the current one's.
-template <bool BF, int VEC>
-__global__ void __launch_bounds__(kAppendThreads) qk_append_kernel(const __grid_constant__ QkAppendArgs a, int slices, int nq, int nkv) {
+template <bool BF, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS) qk_append_kernel(const __grid_constant__ QkAppendArgs a, int slices, int nq, int nkv) {
     constexpr int WB = VEC * (BF ? 2 : 4), N = VEC / 2;       // bytes of a vector, its pairs of neighbours
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, D = a.c.head_dim, kvh = a.c.heads, P = a.c.page_size, n = nq + nkv, half = a.rot / 2;
-    const int items = items_of(D, a.rot, VEC), span = span_of(items), lanes = kAppendThreads / span, hl = tid / span;
+    const int items = items_of(D, a.rot, VEC), span = span_of(items), lanes = THREADS / span, hl = tid / span;
     const bool on = tid - hl * span < items;                  // has an item
-    float* turns = reinterpret_cast<float*>(smem + 4 * n * kAppendThreads * WB);   // [2][rot], behind the rows
+    float* turns = reinterpret_cast<float*>(smem + 4 * n * THREADS * WB);   // [2][rot], behind the rows
     float* weights = turns + 2 * a.rot;                       // [2][D] of q and k
     float* inv = weights + 2 * D;                             // [2 kvh] 1 / scale of E4M3 rows
     Item<VEC> it;
     it.place(on ? tid - hl * span : 0, D, half);
-    auto place = [&](int buf, int s, int k) { return smem + (((buf * n + s) * 2 + k) * kAppendThreads + tid) * WB; };
+    auto place = [&](int buf, int s, int k) { return smem + (((buf * n + s) * 2 + k) * THREADS + tid) * WB; };
     // vectors that the thread does not have are zeros: they add nothing to a sum
     for (int i = 0; i < 2 * n; ++i)
         for (int k = 0; k < 2; ++k)
@@ -136,16 +136,17 @@ __global__ void __launch_bounds__(kAppendThreads) qk_append_kernel(const __grid_
                 for (int w = 0; w < WB; w += 8) *reinterpret_cast<uint2*>(place(0, i, k) + w) = make_uint2(0, 0);
     pdl_allow_dependents();
     pdl_wait_primary();
-    for (int i = tid; i < 2 * D; i += kAppendThreads) weights[i] = weight_at(i < D ? a.q_weight : a.k_weight, a.w_dt, i < D ? i : i - D);
-    for (int i = tid; i < 2 * kvh; i += kAppendThreads) {
+    for (int i = tid; i < 2 * D; i += THREADS) weights[i] = weight_at(i < D ? a.q_weight : a.k_weight, a.w_dt, i < D ? i : i - D);
+    for (int i = tid; i < 2 * kvh; i += THREADS) {
         const float* scale = i < kvh ? a.c.k_scale : a.c.v_scale;
         inv[i] = scale ? 1.0f / scale[i < kvh ? i : i - kvh] : 1.0f;
     }
     const bool with_axes = a.axes > 0;
-    int axis[2] = {0, 0};      // of the words tid, + 128 of a row of cos, sin
+    constexpr int W = 256 / THREADS;
+    int axis[W] = {};          // of the words tid, + THREADS, ... of a row of cos, sin
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int w = tid + j * kAppendThreads;
+    for (int j = 0; j < W; ++j) {
+        const int w = tid + j * THREADS;
         if (w < a.rot) axis[j] = a.axis[w < half ? w : w - half];
     }
     const int last = last_of(a);
@@ -161,43 +162,43 @@ __global__ void __launch_bounds__(kAppendThreads) qk_append_kernel(const __grid_
         if constexpr (WB == 32) cp_async16(dst + 16, src + 16);
     };
     // whether a row of cos, sin that the token needs is not there (with axes, seen by some of the threads)
-    auto fetch = [&](int buf, int t, int slice, int pos, const int (&at)[2]) {
+    auto fetch = [&](int buf, int t, int slice, int pos, const int (&at)[W]) {
         bool bad = false;
         const int q1 = on ? min(a.q_heads, first_q(slice) + nq * lanes) : 0, kv1 = on && pos >= 0 ? min(2 * kvh, first_kv(slice) + nkv * lanes) : 0;
         char* to = place(buf, 0, 0);
-        for (int h = first_q(slice); h < q1; h += lanes, to += 2 * kAppendThreads * WB) {
+        for (int h = first_q(slice); h < q1; h += lanes, to += 2 * THREADS * WB) {
             const long long o = t * a.q_ts + h * a.q_hs;
             copy(to, a.q, o + it.i0);
-            if (it.two) copy(to + kAppendThreads * WB, a.q, o + it.i1);
+            if (it.two) copy(to + THREADS * WB, a.q, o + it.i1);
         }
         to = place(buf, nq, 0);
-        for (int h = first_kv(slice); h < kv1; h += lanes, to += 2 * kAppendThreads * WB) {
+        for (int h = first_kv(slice); h < kv1; h += lanes, to += 2 * THREADS * WB) {
             const bool k = h < kvh;
             const void* p = k ? a.k : a.v;
             const long long o = k ? t * a.k_ts + h * a.k_hs : t * a.v_ts + (h - kvh) * a.v_hs;
             copy(to, p, o + it.i0);
-            if (it.two) copy(to + kAppendThreads * WB, p, o + it.i1);
+            if (it.two) copy(to + THREADS * WB, p, o + it.i1);
         }
         if (with_axes) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int w = tid + j * kAppendThreads;
+            for (int j = 0; j < W; ++j) {
+                const int w = tid + j * THREADS;
                 if (w >= a.rot || pos < 0) continue;
                 if (at[j] < 0 || at[j] >= a.max_pos) bad = true;
                 else cp_async4(turns + buf * a.rot + w, a.cos_sin + (long long)at[j] * a.rot + w);
             }
         } else if (pos >= 0 && pos < a.max_pos) {
-            for (int w = tid * 4; w < a.rot; w += kAppendThreads * 4)
+            for (int w = tid * 4; w < a.rot; w += THREADS * 4)
                 cp_async16(turns + buf * a.rot + w, a.cos_sin + (long long)pos * a.rot + w);
         }
         cp_async_commit();
         return bad;
     };
     // the axes' positions of the thread's words
-    auto places = [&](int t, int (&at)[2]) {
+    auto places = [&](int t, int (&at)[W]) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (with_axes && t < a.T && tid + j * kAppendThreads < a.rot) at[j] = a.axis_positions[(long long)axis[j] * a.T + t];
+        for (int j = 0; j < W; ++j)
+            if (with_axes && t < a.T && tid + j * THREADS < a.rot) at[j] = a.axis_positions[(long long)axis[j] * a.T + t];
     };
     // this unit, the next and the one after it
     const int dt = gridDim.x / slices, ds = gridDim.x % slices;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kAppendThreads) qk_append_kernel(const __grid_
     advance(t1, slice1);
     int t2 = t1, slice2 = slice1;
     // what is loaded in one turn of the loop is looked at in the next
-    int pos = position(t), pos1 = position(t1), req1 = request(t1), entry = page_of(a, request(t), pos, last), at[2], at1[2];
+    int pos = position(t), pos1 = position(t1), req1 = request(t1), entry = page_of(a, request(t), pos, last), at[W], at1[W];
     places(t, at);
     places(t1, at1);
     bool bad = fetch(0, t, slice, pos, at);
@@ -238,25 +239,32 @@ __global__ void __launch_bounds__(kAppendThreads) qk_append_kernel(const __grid_
         auto factors = [&](const float* w) {
             const float* row = turns + buf * a.rot + it.i0;
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                xx[e] = *reinterpret_cast<const float2*>(w + it.i0 + 2 * e);
-                yy[e] = it.two ? *reinterpret_cast<const float2*>(w + it.i1 + 2 * e) : make_float2(0.0f, 0.0f);
+            for (int e = 0; e < N; e += 2) {
+                const float4 u = *reinterpret_cast<const float4*>(w + it.i0 + 2 * e);
+                const float4 v = *reinterpret_cast<const float4*>(w + (it.two ? it.i1 : it.i0) + 2 * e);
+                xx[e] = make_float2(u.x, u.y);
+                xx[e + 1] = make_float2(u.z, u.w);
+                yy[e] = make_float2(v.x, v.y);
+                yy[e + 1] = make_float2(v.z, v.w);
             }
             if (turn) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float2 c = *reinterpret_cast<const float2*>(row + 2 * e), s = *reinterpret_cast<const float2*>(row + half + 2 * e);
-                    xy[e] = fmul2(xx[e], s);
-                    yx[e] = fmul2(yy[e], make_float2(-s.x, -s.y));
-                    xx[e] = fmul2(xx[e], c);
-                    yy[e] = fmul2(yy[e], c);
+                for (int e = 0; e < N; e += 2) {
+                    const float4 c = *reinterpret_cast<const float4*>(row + 2 * e), s = *reinterpret_cast<const float4*>(row + half + 2 * e);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 cc = k ? make_float2(c.z, c.w) : make_float2(c.x, c.y), ss = k ? make_float2(s.z, s.w) : make_float2(s.x, s.y);
+                        xy[e + k] = fmul2(xx[e + k], ss);
+                        yx[e + k] = fmul2(yy[e + k], make_float2(-ss.x, -ss.y));
+                        xx[e + k] = fmul2(xx[e + k], cc);
+                        yy[e + k] = fmul2(yy[e + k], cc);
+                    }
                 }
             }
         };
-        float2 x[N], y[N];
-        auto get = [&](const char* from) {
+        auto get = [&](const char* from, float2 (&x)[N], float2 (&y)[N]) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k, from += kAppendThreads * WB) {
+            for (int k = 0; k < 2; ++k, from += THREADS * WB) {
                 float2(&f)[N] = k ? y : x;
                 if constexpr (BF && VEC == 8) {
                     unpack_bf16x8_f2(*reinterpret_cast<const uint4*>(from), f);
@@ -274,51 +282,77 @@ __global__ void __launch_bounds__(kAppendThreads) qk_append_kernel(const __grid_
                 }
             }
         };
-        auto norm = [&]() {
-            float2 sum = fmul2(x[0], x[0]);
+        // H heads at once, so that one's shuffles and conversions wait beside the other's
+        auto norm = [&](auto& x, auto& y) {
+            constexpr int H = sizeof(x) / sizeof(float2[N]);
+            float all[H];
 #pragma unroll
-            for (int e = 1; e < N; ++e) sum = ffma2(x[e], x[e], sum);
+            for (int h = 0; h < H; ++h) {
+                float2 sum = fmul2(x[h][0], x[h][0]);
 #pragma unroll
-            for (int e = 0; e < N; ++e) sum = ffma2(y[e], y[e], sum);
-            float all = sum.x + sum.y;
-            for (int o = span / 2; o > 0; o >>= 1) all += __shfl_xor_sync(group, all, o);
-            const float r = inv_sqrt(fmaf(all, inv_d, a.eps));
-            const float2 rr = make_float2(r, r);
+                for (int e = 1; e < N; ++e) sum = ffma2(x[h][e], x[h][e], sum);
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float2 f = x[e], g = y[e];
-                x[e] = fmul2(f, xx[e]);
-                y[e] = fmul2(g, yy[e]);
-                if (turn) {
-                    x[e] = ffma2(g, yx[e], x[e]);
-                    y[e] = ffma2(f, xy[e], y[e]);
+                for (int e = 0; e < N; ++e) sum = ffma2(y[h][e], y[h][e], sum);
+                all[h] = sum.x + sum.y;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2)
+                if (o < span) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h) all[h] += __shfl_xor_sync(group, all[h], o);
                 }
-                x[e] = fmul2(x[e], rr);
-                y[e] = fmul2(y[e], rr);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float r = inv_sqrt(fmaf(all[h], inv_d, a.eps));
+                const float2 rr = make_float2(r, r);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float2 f = x[h][e], g = y[h][e];
+                    x[h][e] = fmul2(f, xx[e]);
+                    y[h][e] = fmul2(g, yy[e]);
+                    if (turn) {
+                        x[h][e] = ffma2(g, yx[e], x[h][e]);
+                        y[h][e] = ffma2(f, xy[e], y[h][e]);
+                    }
+                    x[h][e] = fmul2(x[h][e], rr);
+                    y[h][e] = fmul2(y[h][e], rr);
+                }
             }
         };
-        auto put = [&](void* p, int type, long long d, float scale) {
+        auto put = [&](void* p, int type, long long d, const float2 (&x)[N], const float2 (&y)[N], float scale) {
             if (!on) return;
             store_vec<VEC>(p, type, d + it.i0, reinterpret_cast<const float(&)[VEC]>(x), scale);
             if (it.two) store_vec<VEC>(p, type, d + it.i1, reinterpret_cast<const float(&)[VEC]>(y), scale);
         };
         const int q1 = min(a.q_heads, first_q(slice) + nq * lanes), kv1 = page >= 0 ? min(2 * kvh, first_kv(slice) + nkv * lanes) : 0;
+        constexpr int kPass = 2 * THREADS * WB, kType = BF ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
         const char* from = place(buf, 0, 0);
         factors(weights);
-        for (int h = first_q(slice); h < q1; h += lanes, from += 2 * kAppendThreads * WB) {
-            get(from);
-            norm();
-            put(a.q_out, BF ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, t * a.o_ts + h * a.o_hs, 1.0f);
+        int h = first_q(slice);
+        for (; h + lanes < q1; h += 2 * lanes, from += 2 * kPass) {
+            float2 x[2][N], y[2][N];
+            get(from, x[0], y[0]);
+            get(from + kPass, x[1], y[1]);
+            norm(x, y);
+            put(a.q_out, kType, t * a.o_ts + h * a.o_hs, x[0], y[0], 1.0f);
+            put(a.q_out, kType, t * a.o_ts + (h + lanes) * a.o_hs, x[1], y[1], 1.0f);
+        }
+        if (h < q1) {
+            float2 x[1][N], y[1][N];
+            get(from, x[0], y[0]);
+            norm(x, y);
+            put(a.q_out, kType, t * a.o_ts + h * a.o_hs, x[0], y[0], 1.0f);
         }
         from = place(buf, nq, 0);
         const int slot = pos - pos / P * P;
         const long long krow = (long long)page * a.c.k_page_stride + slot * a.c.k_slot_stride, vrow = page * a.c.v_page_stride + slot * a.c.v_slot_stride;
         if (first_kv(slice) < min(kv1, kvh)) factors(weights + D);
-        for (int h = first_kv(slice); h < kv1; h += lanes, from += 2 * kAppendThreads * WB) {
+        for (int h = first_kv(slice); h < kv1; h += lanes, from += kPass) {
             const bool k = h < kvh;
-            get(from);
-            if (k) norm();
-            put(k ? a.c.k : a.c.v, a.c.dtype, k ? krow + h * a.c.k_head_stride : vrow + (h - kvh) * a.c.v_head_stride, inv[h]);
+            float2 x[1][N], y[1][N];
+            get(from, x[0], y[0]);
+            if (k) norm(x, y);
+            put(k ? a.c.k : a.c.v, a.c.dtype, k ? krow + h * a.c.k_head_stride : vrow + (h - kvh) * a.c.v_head_stride, x[0], y[0], inv[h]);
         }
         t = t1;
         slice = slice1;
@@ -331,9 +365,9 @@ __global__ void __launch_bounds__(kAppendThreads) qk_append_kernel(const __grid_
     }
 }
 
-template <bool BF, int VEC>
-cudaError_t launch(const QkAppendArgs& a, cudaStream_t s) {
-    const int sms = device_sm_count(), lanes = kAppendThreads / span_of(items_of(a.c.head_dim, a.rot, VEC));
+template <bool BF, int VEC, int THREADS>
+cudaError_t launch_as(const QkAppendArgs& a, cudaStream_t s) {
+    const int sms = device_sm_count(), lanes = THREADS / span_of(items_of(a.c.head_dim, a.rot, VEC));
     const int most_q = (a.q_heads + lanes - 1) / lanes, most_kv = (2 * a.c.heads + lanes - 1) / lanes;
     // Few tokens: slices of the heads, until the blocks fill the GPU or a thread has one head.
     int slices = std::max(1, std::min(std::max(most_q, most_kv), 8 * sms / a.T)), nq, nkv;
@@ -341,17 +375,25 @@ cudaError_t launch(const QkAppendArgs& a, cudaStream_t s) {
     for (;; ++slices) {      // whole tokens where two units of them fit in shared memory
         nq = (most_q + slices - 1) / slices;
         nkv = (most_kv + slices - 1) / slices;
-        smem = (size_t)4 * (nq + nkv) * kAppendThreads * VEC * (BF ? 2 : 4) + (2 * a.rot + 2 * a.c.head_dim + 2 * a.c.heads) * 4;
+        smem = (size_t)4 * (nq + nkv) * THREADS * VEC * (BF ? 2 : 4) + (2 * a.rot + 2 * a.c.head_dim + 2 * a.c.heads) * 4;
         if (smem <= (size_t)kAppendSmem || nq + nkv <= 2) break;
     }
-    auto kern = qk_append_kernel<BF, VEC>;
+    auto kern = qk_append_kernel<BF, VEC, THREADS>;
     static std::atomic<uint64_t> done, blocks;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kAppendSmem, done);
     int per_sm = 0;
-    if (e == cudaSuccess) e = blocks_per_sm(reinterpret_cast<const void*>(kern), kAppendThreads, smem, blocks, &per_sm);
+    if (e == cudaSuccess) e = blocks_per_sm(reinterpret_cast<const void*>(kern), THREADS, smem, blocks, &per_sm);
     if (e != cudaSuccess) return e;
     const int grid = std::min(a.T * slices, per_sm * sms);
-    return launch_pdl(kern, dim3((unsigned)grid), dim3(kAppendThreads), smem, s, a, slices, nq, nkv);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(THREADS), smem, s, a, slices, nq, nkv);
+}
+
+// Blocks of 64 threads where 128 would take all heads of q in one turn: half the instructions that every warp spends on
+// a token as such.
+template <bool BF, int VEC>
+cudaError_t launch(const QkAppendArgs& a, cudaStream_t s) {
+    const bool narrow = a.q_heads * span_of(items_of(a.c.head_dim, a.rot, VEC)) <= 128;
+    return narrow ? launch_as<BF, VEC, 64>(a, s) : launch_as<BF, VEC, 128>(a, s);
 }
 
 }  // namespace
