@@ -79,7 +79,6 @@ struct ScoresArgs : PageArgs {
 struct SelectArgs : PageArgs {
     const float* scores;
     int heads, keep, sinks, recent;
-    int cached;                // scores that shared memory holds (set by the launcher)
     int32_t* tables;
     int32_t* lens;
 };

@@ -445,24 +445,26 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
 // ---- select -------------------------------------------------------------------
 //
 // One block per (request, key-value head).  Scores become whole numbers of the same order, forced pages the
-// greatest; the `keep`-th greatest is found digit by digit (8 bits each, from the highest bit in which two of
-// them differ), and the pages above it, with the first ones equal to it, are written in order.
-constexpr int kSelectThreads = 256;
-constexpr int kSelectKeys = 8192;           // kept in shared memory; the others are read again
+// greatest.  The last one wanted of the others lies among fewer and fewer keys: those that agree with it in a digit
+// (8 bits each, from the highest bit in which two of them differ), until they are few enough to be compared with one
+// another.  The pages above it, with the first ones equal to it, are written in order.  Trips to memory, barriers and
+// chains of instructions bound it: a thread has up to 8 keys in registers from one trip, a warp consecutive ones.
+// (Keys in shared memory and four digits: 8.5 instead of 5.6 us for 4 heads of 2048 pages, 17 instead of 13.4 for
+// 1024 heads of up to as many.)
+constexpr int kSelectItems = 8;             // keys of a thread; more pages go in turns, read again each time
+constexpr int kSelectRank = 128;            // keys that are compared with one another
 
+// Keys of no page, and of a forced one.
+constexpr uint32_t kNone = 0u, kForced = 0xffffffffu;
 // Scores in ascending order; NaN above all, -0 like 0.
-__device__ __forceinline__ uint32_t key_of(float s) {
-    if (s != s) return 0xfffffffeu;
-    const uint32_t u = __float_as_uint(s + 0.0f);
-    return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
-}
+__device__ __forceinline__ uint32_t key_of(float s) { return s != s ? kForced - 1 : ordered_key(s); }
 
-__global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __grid_constant__ SelectArgs a) {
-    constexpr int kWarps = kSelectThreads / 32;
-    extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ uint32_t hist[256], found[2];
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(const __grid_constant__ SelectArgs a) {
+    constexpr int kWarps = THREADS / 32, kTurn = THREADS * kSelectItems;
+    __shared__ __align__(16) uint32_t list[kSelectRank];
+    __shared__ uint32_t hist[256], found[4];
     __shared__ uint32_t ends[2][kWarps];
-    __shared__ long long wsum[kWarps];
     pdl_allow_dependents();
     pdl_wait_primary();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, unit = blockIdx.x, b = unit / a.heads, keep = a.keep;
@@ -470,101 +472,188 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
     const float* scores = a.scores + (long long)unit * a.max_pages;
     const int32_t* row = a.table + b * a.table_ld;
     int32_t* out = a.tables + (long long)unit * keep;
-    if (tid == 0) {
-        // whole pages but for the last one, if that is among them
-        a.lens[unit] = pages <= keep ? n : kept * a.page_size;
-    }
-    for (int i = kept + tid; i < keep; i += kSelectThreads) out[i] = -1;
+    // whole pages but for the last one, if that is among them
+    if (tid == 0) a.lens[unit] = pages <= keep ? n : kept * a.page_size;
+    for (int i = kept + tid; i < keep; i += THREADS) out[i] = -1;
     if (pages <= keep) {
-        for (int i = tid; i < pages; i += kSelectThreads) out[i] = row[i];
+        for (int i = tid; i < pages; i += THREADS) out[i] = row[i];
         return;
     }
-    auto key_at = [&](int i) {
-        return i < a.sinks || i >= pages - a.recent ? 0xffffffffu : key_of(scores[i]);
+    // A turn's pages from `base` on, equally many of them in a row to each warp: item j of the thread is page first + 32 j.
+    uint32_t k[kSelectItems];
+    int first = 0, items = 0;
+    auto load = [&](int base) {
+        items = (min(pages - base, kTurn) + THREADS - 1) / THREADS;
+        first = base + warp * 32 * items + lane;
+        const int end = min(pages, base + kTurn);
+        float f[kSelectItems];
+#pragma unroll
+        for (int j = 0; j < kSelectItems; ++j) f[j] = j < items && first + 32 * j < end ? scores[first + 32 * j] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kSelectItems; ++j) {
+            const int i = first + 32 * j;
+            k[j] = j >= items || i >= end ? kNone : i < a.sinks || i >= pages - a.recent ? kForced : key_of(f[j]);
+        }
     };
-    uint32_t low = 0xffffffffu, high = 0u;
-    for (int i = tid; i < pages; i += kSelectThreads) {
-        const uint32_t k = key_at(i);
-        if (i < a.cached) keys[i] = k;
-        low = min(low, k);
-        high = max(high, k);
-    }
+    const bool turns = pages > kTurn;
+    // f() for every turn, with its keys
+    auto each = [&](auto f) {
+        for (int base = 0; base < pages; base += kTurn) {
+            if (turns) load(base);
+            f();
+        }
+    };
+    if (!turns) load(0);
+    uint32_t low = kForced, high = 0u;      // of the others
+    each([&] {
+#pragma unroll
+        for (int j = 0; j < kSelectItems; ++j)
+            if (k[j] != kNone && k[j] != kForced) {
+                low = min(low, k[j]);
+                high = max(high, k[j]);
+            }
+    });
+    __syncwarp();
     low = __reduce_min_sync(0xffffffffu, low);
     high = __reduce_max_sync(0xffffffffu, high);
     if (lane == 0) {
         ends[0][warp] = low;
         ends[1][warp] = high;
     }
+    if (tid < 256) hist[tid] = 0;
+    if (tid == 0) found[3] = 0;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         low = min(low, ends[0][w]);
         high = max(high, ends[1][w]);
     }
-    auto key = [&](int i) { return i < a.cached ? keys[i] : key_at(i); };
-    // The keys in question agree with `value` above bit `bits`; `need` of the greatest of them are wanted.
-    int bits = 32 - __clz(low ^ high);
-    uint32_t value = bits == 32 ? 0u : high >> bits << bits, need = keep;
-    while (bits > 0) {
+    // The `candidates` keys in question agree with `value` from bit `bits` on; `need` of the greatest of them are wanted.
+    const int must = a.sinks + a.recent;
+    int bits = must < keep ? 32 - __clz(low ^ high) : 0;
+    uint32_t value = must == keep ? kForced - 1 : bits == 32 ? 0u : high >> bits << bits, need = keep - must, candidates = pages - must;
+    auto in_question = [&](uint32_t key) { return key != kNone && key != kForced && (bits == 32 || (key ^ value) >> bits == 0); };
+    while (bits > 0 && candidates > kSelectRank) {
         const int take = min(bits, 8), shift = bits - take;
-        hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < pages; i += kSelectThreads) {
-            const uint32_t k = key(i);
-            if (bits == 32 || (k ^ value) >> bits == 0) atomicAdd(hist + (k >> shift & ((1u << take) - 1u)), 1u);
-        }
-        __syncthreads();
-        // keys of this digit or a greater one, thread 0 at the greatest digit
-        const uint32_t mine = hist[255 - tid];
-        uint32_t incl = mine;
+        each([&] {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        if (lane == 31) ends[0][warp] = incl;
+            for (int j = 0; j < kSelectItems; ++j)
+                if (in_question(k[j])) atomicAdd(hist + (k[j] >> shift & ((1u << take) - 1u)), 1u);
+        });
         __syncthreads();
+        // one warp looks for the digit, 8 to a lane, the greatest ones in lane 0
+        if (warp == 0) {
+            uint32_t h[8], mine = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (w < warp) incl += ends[0][w];
-        if (incl >= need && incl - mine < need) {
-            found[0] = 255 - tid;
-            found[1] = incl - mine;
+            for (int i = 0; i < 8; ++i) {
+                h[i] = hist[255 - 8 * lane - i];
+                hist[255 - 8 * lane - i] = 0;
+                mine += h[i];
+            }
+            uint32_t above = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, above, o);
+                if (lane >= o) above += u;
+            }
+            above -= mine;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (above < need && above + h[i] >= need) {
+                    found[0] = 255 - 8 * lane - i;
+                    found[1] = above;
+                    found[2] = h[i];
+                }
+                above += h[i];
+            }
         }
         __syncthreads();
         value |= found[0] << shift;
         need -= found[1];
+        candidates = found[2];
         bits = shift;
     }
-    // `need` pages of key `value`, the first ones, and all above; a thread has a run of an odd
-    // number of pages (bank conflicts), and writes behind what the threads before it do
-    const int run = (pages + kSelectThreads - 1) / kSelectThreads | 1, i0 = min(tid * run, pages), i1 = min(i0 + run, pages);
-    long long mine = 0;                     // pages above, and in the upper half pages equal
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = key(i);
-        mine += k > value ? 1ll : k == value ? 1ll << 32 : 0ll;
-    }
-    long long incl = mine;
+    if (bits > 0) {
+        each([&] {
+            uint32_t in[kSelectItems], all = 0, at = 0;
+            __syncwarp();
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
+            for (int j = 0; j < kSelectItems; ++j) {
+                in[j] = __ballot_sync(0xffffffffu, in_question(k[j]));
+                all += __popc(in[j]);
+            }
+            if (lane == 0 && all) at = atomicAdd(found + 3, all);
+            at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        if (w < warp) incl += wsum[w];
-    uint32_t above = (uint32_t)(incl - mine), equal = (uint32_t)((incl - mine) >> 32);
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = key(i);
-        if (k > value || (k == value && equal < need)) {
-            out[above + min(equal, need)] = row[i];
-            if (i == pages - 1) a.lens[unit] = n - (pages - keep) * a.page_size;
+            for (int j = 0; j < kSelectItems; ++j) {
+                if (in[j] >> lane & 1u) list[at + __popc(in[j] & ((1u << lane) - 1u))] = k[j];
+                at += __popc(in[j]);
+            }
+        });
+        __syncthreads();
+        if (warp * 32 < (int)candidates) {
+            const uint32_t mine = tid < (int)candidates ? list[tid] : kNone;
+            uint32_t greater = 0, equal = 0;
+            for (uint32_t i = 0; i < candidates; i += 4) {
+                const uint4 o = *reinterpret_cast<const uint4*>(list + i);
+                const uint32_t other[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    greater += i + e < candidates && other[e] > mine;
+                    equal += i + e < candidates && other[e] == mine;
+                }
+            }
+            if (tid < (int)candidates && greater < need && greater + equal >= need) {
+                found[0] = mine;           // the same for all that are equal
+                found[1] = greater;
+            }
         }
-        above += k > value;
-        equal += k == value;
+        __syncthreads();
+        value = found[0];
+        need -= found[1];
     }
+    // `need` pages of key `value`, the first ones, and all above: a warp writes behind what the warps before it do
+    uint32_t above = 0, equal = 0;          // in the turns before
+    each([&] {
+        int32_t entry[kSelectItems];
+        uint32_t more[kSelectItems], same[kSelectItems], n_more = 0, n_same = 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kSelectItems; ++j) {
+            entry[j] = k[j] >= value && k[j] != kNone ? row[first + 32 * j] : 0;
+            more[j] = __ballot_sync(0xffffffffu, k[j] > value);
+            same[j] = __ballot_sync(0xffffffffu, k[j] == value);
+            n_more += __popc(more[j]);
+            n_same += __popc(same[j]);
+        }
+        if (turns) __syncthreads();         // the counts before have been read
+        if (lane == 0) {
+            ends[0][warp] = n_more;
+            ends[1][warp] = n_same;
+        }
+        __syncthreads();
+        uint32_t up = above, eq = equal;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            above += ends[0][w];
+            equal += ends[1][w];
+            if (w < warp) {
+                up += ends[0][w];
+                eq += ends[1][w];
+            }
+        }
+        const uint32_t before = (1u << lane) - 1u;
+#pragma unroll
+        for (int j = 0; j < kSelectItems; ++j) {
+            const uint32_t e = eq + __popc(same[j] & before);
+            if ((more[j] >> lane & 1u) || ((same[j] >> lane & 1u) && e < need)) {
+                out[up + __popc(more[j] & before) + min(e, need)] = entry[j];
+                if (first + 32 * j == pages - 1) a.lens[unit] = n - (pages - keep) * a.page_size;
+            }
+            up += __popc(more[j]);
+            eq += __popc(same[j]);
+        }
+    });
 }
 
 template <bool F8, int JC>
@@ -593,10 +682,17 @@ cudaError_t launch_page_scores(const ScoresArgs& a, cudaStream_t s) {
            : D <= 128 ? launch_scores_as<false, 8>(a, s) : launch_scores_as<false, 16>(a, s);
 }
 
-cudaError_t launch_page_select(const SelectArgs& args, cudaStream_t s) {
-    SelectArgs a = args;
-    a.cached = std::min(a.max_pages, kSelectKeys);
-    return launch_pdl(page_select_kernel, dim3((unsigned)(a.B * a.heads)), dim3(kSelectThreads), (size_t)a.cached * 4, s, a);
+cudaError_t launch_page_select(const SelectArgs& a, cudaStream_t s) {
+    const int blocks = a.B * a.heads;
+    // More than 2048 pages: blocks that have them all in a turn (or many of them), but no more threads than the SMs hold at
+    // once.  4 heads of 8192 pages 20.5, 14.5 and 10.4 us with 256, 512 and 1024 threads, 256 heads of 4096 18.7, 9.9
+    // and 18.6, 1024 heads of up to 2048 13.4, 22.3 with 256 and 512.
+    const int sms = device_sm_count();
+    if (a.max_pages > 512 * kSelectItems && blocks <= sms)
+        return launch_pdl(page_select_kernel<1024>, dim3((unsigned)blocks), dim3(1024), 0, s, a);
+    if (a.max_pages > 256 * kSelectItems && blocks <= 2 * sms)
+        return launch_pdl(page_select_kernel<512>, dim3((unsigned)blocks), dim3(512), 0, s, a);
+    return launch_pdl(page_select_kernel<256>, dim3((unsigned)blocks), dim3(256), 0, s, a);
 }
 
 }  // namespace moe
