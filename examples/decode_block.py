@@ -12,7 +12,16 @@
 block before this one adds to it, and ``y`` what the next one will.  All
 buffers are the block's own, so that a step can be captured in a CUDA graph.
 
-    python examples/decode_block.py [--requests 16] [--context 2048] [--steps 32] [--cache e4m3]
+With ``keep`` pages the heads of q and k are normed, and attention reads that many pages of a
+request per key-value head, those that its query can score highest in:
+
+    norm and rotate q, k; k, v into the cache    moe_qk_norm_append
+    bounds of the page just written to           moe_page_bounds
+    what q can score in each page                moe_page_scores
+    the first, the last two and the best ones    moe_page_select
+    a    = attention of q over these             moe_attn_pages
+
+    python examples/decode_block.py [--requests 16] [--context 2048] [--steps 32] [--cache e4m3] [--keep 32]
 
 runs the block of the 2048-wide DeaMoE layer on random weights, captured once
 and replayed, and prints the time of a step.
@@ -36,11 +45,11 @@ EPS = 1e-5
 
 class DecodeBlock:
     """Weights, cache, workspaces and buffers of one block for ``requests``
-    requests of up to ``max_len`` tokens."""
+    requests of up to ``max_len`` tokens; ``keep``: pages that attention reads (0: all)."""
 
     def __init__(self, shape: synth.LayerShape, requests: int, max_len: int, heads: int, kv_heads: int,
                  head_dim: int, page: int = 16, adapters: int = 4, rank: int = 16, cache: str = "bf16",
-                 seed: int = 0, device="cuda"):
+                 seed: int = 0, device="cuda", keep: int = 0):
         self.shape, self.heads, self.kv_heads, self.head_dim = shape, heads, kv_heads, head_dim
         T, d, D = requests, shape.d, head_dim
         wide = (heads + 2 * kv_heads) * D
@@ -84,6 +93,17 @@ class DecodeBlock:
         self.o, self.h2, self.y = (buffer(T, d, dtype=torch.float32) for _ in range(3))
         self.topk_idx = buffer(T, shape.k, dtype=torch.int32)
         self.topk_w = buffer(T, shape.k, dtype=torch.float32)
+        self.keep, self.page = keep, page
+        if keep:
+            self.q_norm, self.k_norm = normal(D, std=0.1) + 1, normal(D, std=0.1) + 1
+            self.bounds = B.new_page_bounds(self.cache)
+            self.scores = buffer(T, kv_heads, per, dtype=torch.float32)
+            self.tables, self.lens = buffer(T, kv_heads, keep, dtype=torch.int32), buffer(T, kv_heads, dtype=torch.int32)
+
+    def prompt(self, seq_lens):
+        """The first ``seq_lens`` (int32 [T]) tokens of each request have been written to the cache."""
+        if self.keep:
+            B.moe_page_bounds(self.cache, self.bounds, self.block_table, seq_lens)
 
     def step(self, delta, x, positions, seq_lens, adapter):
         """One new token per request: ``delta`` and ``x`` float32 [T, d] (x is
@@ -94,8 +114,17 @@ class DecodeBlock:
         B.moe_lora_project(self.h1, self.w_qkv, self.qkv, self.ws_qkv, lora=self.lora_qkv, adapter=adapter)
         heads = self.qkv.view(-1, H + 2 * KV, D)
         q, k, v = heads[:, :H], heads[:, H:H + KV], heads[:, H + KV:]
-        B.moe_kv_append(k, v, self.cache, self.block_table, positions, cos_sin=self.cos_sin, q=q, q_out=q)
-        B.moe_attn_decode(q, self.cache, self.block_table, seq_lens, D ** -0.5, self.attn, self.ws_attn)
+        if self.keep:
+            B.moe_qk_norm_append(q, k, v, self.q_norm, self.k_norm, EPS, self.cache, self.block_table, positions, q,
+                                 cos_sin=self.cos_sin)
+            B.moe_page_bounds(self.cache, self.bounds, self.block_table, seq_lens, first=positions)
+            B.moe_page_scores(q, self.cache, self.bounds, self.block_table, seq_lens, self.scores)
+            B.moe_page_select(self.scores, self.block_table, seq_lens, self.page, self.tables, self.lens,
+                              sinks=min(1, self.keep - 1), recent=min(2, self.keep))
+            B.moe_attn_pages(q, self.cache, self.tables, self.lens, D ** -0.5, self.attn, self.ws_attn)
+        else:
+            B.moe_kv_append(k, v, self.cache, self.block_table, positions, cos_sin=self.cos_sin, q=q, q_out=q)
+            B.moe_attn_decode(q, self.cache, self.block_table, seq_lens, D ** -0.5, self.attn, self.ws_attn)
         B.moe_lora_project(self.attn.view(-1, H * D), self.w_o, self.o, self.ws_o, lora=self.lora_o, adapter=adapter)
         B.moe_rmsnorm(self.o, self.norm2, EPS, self.h2, residual=x, residual_out=x)
         s, L = self.shape, self.layer
@@ -121,13 +150,16 @@ def main():
     ap.add_argument("--context", type=int, default=2048, help="tokens already in each request's cache")
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--cache", choices=("bf16", "e4m3"), default="bf16")
+    ap.add_argument("--keep", type=int, default=0, help="pages that attention reads of a request (0: all)")
     a = ap.parse_args()
     T, shape = a.requests, synth.DEAMOE_7B
-    block = DecodeBlock(shape, T, a.context + a.steps + 8, heads=16, kv_heads=4, head_dim=128, cache=a.cache)
+    block = DecodeBlock(shape, T, a.context + a.steps + 8, heads=16, kv_heads=4, head_dim=128, cache=a.cache,
+                        keep=a.keep)
     x, delta = torch.zeros(T, shape.d, device="cuda"), synth.hidden(T, shape.d, 1, "cuda")
     positions = torch.full((T,), a.context, dtype=torch.int32, device="cuda")
     seq_lens = positions + 1
     adapter = torch.tensor([t % 5 - 1 for t in range(T)], dtype=torch.int32, device="cuda")
+    block.prompt(positions)
     block.step(delta, x, positions, seq_lens, adapter)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -149,7 +181,8 @@ def main():
     if status:
         raise SystemExit(f"device status {status}")
     us = first.elapsed_time(last) * 1e3 / max(1, a.steps - 2)
-    print(f"{T} requests of {a.context} tokens, {a.cache} cache: {us:.1f} us a block step "
+    kept = f", {a.keep} pages of each" if a.keep else ""
+    print(f"{T} requests of {a.context} tokens, {a.cache} cache{kept}: {us:.1f} us a block step "
           f"({us / T:.2f} us a token), |y| = {block.y.norm().item():.4g}")
 
 

@@ -33,7 +33,7 @@ __device__ __forceinline__ void report_lengths(const PageArgs& a) {
 // threads share the rows of a unit and meet in shared memory.
 constexpr int kBoundsThreads = 256;
 constexpr int kBoundsParts = 8;
-constexpr int kBoundsBlocks = 4;            // per SM
+constexpr int kBoundsBlocks = 3;            // per SM
 constexpr int kBoundsAhead = 8;             // rows in flight per thread
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
@@ -191,7 +191,7 @@ struct Scores {
     static constexpr int kStages = 3;
     static constexpr int kWarpBytes = kStages * kStage + kWords * 4;
     static constexpr int kSmem = kScoreWarps * kWarpBytes;
-    static constexpr int kBlocksPerSm = JC >= 16 ? 2 : F8 && JC >= 8 ? 3 : kScoreBlocks;
+    static constexpr int kBlocksPerSm = JC <= 2 ? 4 : JC >= 16 ? 2 : F8 && JC >= 8 ? 3 : kScoreBlocks;
     static_assert(kBatch <= 32, "a lane's page");
     static_assert(kBlocksPerSm * (kSmem + 1280) <= 228 * 1024, "blocks that run at once");
 };
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
     Walk ahead = here;
     bool more = true;
     int stage_in = 0;
-    const uint32_t place = smem_u32(ring) + lane * 16;
+    const uint32_t place = smem_u32(ring);
     const long long page_bytes = (long long)heads * pieces * 16;
     auto ask = [&]() {
         const int col = ahead.n * kBatch + lane;
@@ -290,14 +290,13 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
         }
         __syncwarp();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            // a page that is not there has another's values, and pieces behind the last one its first: they
-            // meet terms of 0, or nobody looks at the sum
-            const int page = max(__shfl_sync(0xffffffffu, id, u * 8 + lane / 4), 0);
-            const char* from = static_cast<const char*>(a.bounds) + page * page_bytes + (g * pieces + lane % 4) * 16;
-#pragma unroll
-            for (int j = 0; j < JC; ++j)
-                cp_async16_to(place + stage_in * K::kStage + (u * JC + j) * 512, from + (4 * j + lane % 4 < pieces ? 64 * j : 0));
+        for (int i = 0; i < U * JC; ++i) {
+            // a page that is not there has another's values, and pieces behind the last one that: they meet
+            // terms of 0, or nobody looks at the sum
+            const int at = (i * 32 + lane) / (4 * JC), piece = (i * 32 + lane) % (4 * JC);
+            const int page = max(__shfl_sync(0xffffffffu, id, at), 0);
+            const char* from = static_cast<const char*>(a.bounds) + page * page_bytes + ((long long)g * pieces + min(piece, pieces - 1)) * 16;
+            cp_async16_to(place + stage_in * K::kStage + (at * 4 * JC + (piece ^ (at & 1) << 2)) * 16, from);
         }
         stage_in = stage_in + 1 == K::kStages ? 0 : stage_in + 1;
     };
@@ -390,19 +389,21 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
         float* out = a.scores + ((long long)here.b * heads + here.g) * a.max_pages;
         for (; here.n < here.last; ++here.n) {
             cp_async_wait<K::kStages - 2>();
+            __syncwarp();          // all lanes' pieces are there, and the stage before has been read
             const int had = ids[0];
 #pragma unroll
             for (int i = 0; i + 2 < K::kStages; ++i) ids[i] = ids[i + 1];
             feed(ids[K::kStages - 2]);
             cp_async_commit();
-            const char* rows = ring + stage * K::kStage + lane * 16;
+            const char* rows = ring + stage * K::kStage + lane / 4 * JC * 64 + lane % 4 * 16;
+            const int odd = lane / 4 % 2 * 64;
             stage = stage + 1 == K::kStages ? 0 : stage + 1;
             float c[2][U][4] = {};          // two chains of additions
 #pragma unroll
             for (int j = 0; j < JC; ++j) {
                 uint4 y[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) y[u] = *reinterpret_cast<const uint4*>(rows + (u * JC + j) * 512);
+                for (int u = 0; u < U; ++u) y[u] = *reinterpret_cast<const uint4*>(rows + u * JC * 512 + j * 64 + (j % 2 ? -odd : odd));
 #pragma unroll
                 for (int i = 0; i < K::MC; ++i) {
                     const uint2 f = *reinterpret_cast<const uint2*>(mine + (j * K::MC + i) * 24);

@@ -7,11 +7,16 @@ side, so that those absolute values are the terms' own (where lo <= 0 <= hi; els
 taken apart).  Attention: see test_gpu_block.py.
 """
 
+import importlib.util
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
+from moe_decode_layer_fp32_gb300 import synth
 from oracle import block_oracle as O
 from tests.helpers import ensure_built
 from tests.test_gpu_block import BF, DT, U, assert_within, cos_sin_table, gen, make_cache, normal, raw
@@ -587,3 +592,121 @@ def test_a_step_on_another_stream_and_in_graphs(B):
         for graph in graphs:
             graph.replay()
         check()
+
+
+# ------------------------------------------------------------------ far and odd places
+
+
+def test_far_pages(B):
+    """Pages whose offset passes 2^32 elements: append, bounds and attention."""
+    D, page = 64, 16
+    stride = 1 << 28
+    buf = torch.zeros((17 * stride + page * D,), dtype=torch.uint8, device="cuda")
+    k = buf.view(torch.float8_e4m3fn).as_strided((18, page, 1, D), (stride, D, D, 1))
+    s = torch.ones(1, device="cuda")
+    cache = B.KvCache(k, k, s, s)
+    g = gen(20)
+    rows, table, req = normal(g, 2, 1, D), torch.tensor([[17]], **INT), torch.zeros(2, **INT)
+    B.moe_qk_norm_append(None, rows, rows, None, None, 1e-6, cache, table, torch.tensor([0, 1], **INT), None, req=req)
+    got = O.f64(buf[17 * stride:17 * stride + 2 * D].view(torch.float8_e4m3fn)).view(2, 1, D)
+    assert (got != 0).any()
+    bounds = B.new_page_bounds(cache)
+    B.moe_page_bounds(cache, bounds, table, torch.tensor([2], **INT))
+    assert torch.equal(O.f64(bounds[17]), torch.stack([got.min(0).values, got.max(0).values], 1))
+    q, o = normal(g, 1, 1, D), torch.empty(1, 1, D, device="cuda")
+    B.moe_attn_pages(q, cache, table.view(1, 1, 1), torch.tensor([[2]], **INT), 0.125, o, B.new_attn_workspace(1, 1, 1, D))
+    want, _ = O.decode_attention(q[0], (got, got), 0.125)
+    assert_within(o[0], want, 4e-4, "far page")
+
+
+def test_far_bounds(B):
+    """Bounds of 2^22 pages and more, beyond 2^32 bytes; the cache is a view of one page."""
+    pages, hkv, D = (1 << 22) + 8, 4, 128
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    g = gen(21)
+    k = normal(g, 1, 16, hkv, D, dtype=torch.bfloat16).expand(pages, 16, hkv, D)
+    cache = B.KvCache(k, k)
+    bounds = B.new_page_bounds(cache)
+    table = torch.tensor([[pages - 1, 3, pages - 8]], **INT)
+    seq = torch.tensor([40], **INT)
+    B.moe_page_bounds(cache, bounds, table, seq)
+    assert torch.equal(bounds[pages - 1, :, 0], k[0].amin(0)) and torch.equal(bounds[pages - 8, :, 1], k[0, :8].amax(0))
+    q, scores = normal(g, 1, 8, D), torch.zeros(1, hkv, 3, device="cuda")
+    B.moe_page_scores(q, cache, bounds, table, seq, scores)
+    at = torch.tensor([pages - 1, 3, pages - 8], device="cuda")
+    want, size = O.page_scores(q[0], bounds[at, :, 0], bounds[at, :, 1])
+    assert_within(scores[0], want, 30 * U * size + 1e-4, "far bounds")
+
+
+def test_scores_lengths_near_the_limit_of_int(B):
+    """2^31 - 1 tokens in two pages of 2^30 slots, of a cache that is a view of one row."""
+    k = normal(gen(22), 1, 1, 2, 64, dtype=torch.bfloat16).expand(3, 2**30, 2, 64)
+    cache = B.KvCache(k, k)
+    bounds = torch.stack([k[:, 0], k[:, 0]], 2).contiguous()
+    q, scores = normal(gen(23), 1, 2, 64), torch.zeros(1, 2, 2, device="cuda")
+    B.moe_page_scores(q, cache, bounds, torch.tensor([[2, 0]], **INT), torch.tensor([2**31 - 1], **INT), scores)
+    want = (O.f64(q[0]) * O.f64(k[0, 0])).sum(1)
+    assert_within(scores[0, :, 0], want, 1e-4, "first page")
+    assert_within(scores[0, :, 1], want, 1e-4, "second page")
+
+
+# ------------------------------------------------------------------------- example
+
+
+@pytest.fixture(scope="module")
+def example(B):
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_block.py")
+    spec = importlib.util.spec_from_file_location("decode_block_pages", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_example_block_with_selected_pages(B, example, cache):
+    """Eager steps and replays of a captured one give the same bits; with every page kept, attention is that over
+    the whole cache."""
+    T, runs = 3, []
+    for captured, keep in ((False, 3), (True, 3), (False, 10)):
+        blk = example.DecodeBlock(synth.TINY_VANILLA, T, 80, 4, 2, 64, page=8, adapters=2, rank=8, cache=cache, seed=5, keep=keep)
+        x, delta = torch.zeros(T, 256, device="cuda"), synth.hidden(T, 256, 2, "cuda")
+        positions = torch.tensor([0, 9, 60], **INT)
+        seq, adapter = positions + 1, torch.tensor([1, -1, 0], **INT)
+        g = gen(1)
+        for c in blk.cache.tensors[:2]:
+            c.copy_(normal(g, *c.shape, std=0.5).to(c.dtype))
+        blk.prompt(positions)
+
+        def one():
+            blk.step(delta, x, positions, seq, adapter)
+            positions.add_(1)
+            seq.add_(1)
+
+        step = one
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                one()
+            step = graph.replay
+        for i in range(5):
+            step()
+        torch.cuda.synchronize()
+        assert blk.status() == 0
+        runs.append((blk.attn.clone(), blk.tables.clone(), blk.lens.clone()))
+        if keep == 10:
+            q = blk.qkv.view(T, -1, 64)[:, :4]
+            out = torch.empty_like(blk.attn)
+            B.moe_attn_decode(q, blk.cache, blk.block_table, seq - 1, 64 ** -0.5, out, B.new_attn_workspace(T, 4, 2, 64))
+            top = O.f64(blk.cache.tensors[1]).abs().max().item() * (8 / 448 if cache == "e4m3" else 1.0)
+            assert_within(blk.attn, O.f64(out), 1e-4 * top + 2.02 * BF * O.f64(out).abs(), "all pages")
+    for a, b in zip(runs[0], runs[1]):
+        assert torch.equal(a, b)
+
+
+def test_example_runs(B):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "decode_block.py"), "--requests", "3", "--context", "500",
+                        "--steps", "4", "--keep", "8"], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert "8 pages of each" in r.stdout
