@@ -165,9 +165,9 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsBlocks) page_bounds_ker
 // sum over the heads h of a group of sum_d max(q_hd lo_d, q_hd hi_d) is one product of length 2 D,
 //   sum_d (sum_h min(q_hd, 0)) lo_d + (sum_h max(q_hd, 0)) hi_d,
 // as lo <= hi: an addition and a multiplication per value read, and memory bounds it if the instructions
-// per value are few.  So the tensor cores multiply: 8 pages are the columns of an MMA, and its rows the sums of q as
-// three terms of bf16 (of f16 next to E4M3 bounds, which it holds: the E4M3 form of the instruction converts both
-// operands each time, 12 conversions where 4 do), 24 bits of them and more.
+// per value are few.  So the tensor cores multiply: 8 or 16 pages are the rows of an MMA, and its columns the sums of q
+// as three terms of bf16 (of f16 next to E4M3 bounds, which it holds: the E4M3 form of mma.sync is two f16 ones and
+// conversions of both operands), 24 bits of them and more.
 // A lane reads 16 bytes of its page at a time, in any order of d, as a dot product does not mind it.
 // Every warp works alone on a run of batches of one or several heads, with the rows of the next batches on their way
 // into shared memory, a lane's pieces into places of its own; where a head begins the warp forms its terms of q
@@ -185,7 +185,7 @@ struct Scores {
     static constexpr int kBatch = 8 * U;
     static constexpr int kValues = 4 * JC * E;
     static constexpr int V = kValues > 256 ? kValues / 32 : 8;   // of a lane, in the terms of q
-    // A fragments of q: for each MMA the words of three terms, 4 lanes, 2 words
+    // B fragments of q: for each MMA the words of three terms, 4 lanes, 2 words
     static constexpr int kWords = JC * MC * 24;
     static constexpr int kStage = U * JC * 512;              // a warp's
     static constexpr int kStages = 3;
@@ -306,9 +306,8 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
         cp_async_commit();
     }
     // ---- the products
-    // the rows of terms; those behind the last have it again, and count for nothing
+    // the columns of terms; those behind the last have it again, and count for nothing
     const uint32_t* mine = frag + min(lane / 4, 2) * 8 + lane % 4 * 2;
-    const float part = lane < 12 ? 1.0f : 0.0f;
     int stage = 0;
     do {
         // the sums of q: V of the 2 D values to a lane, eight query heads' loads together (the type is asked outside the
@@ -398,46 +397,31 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
             const char* rows = ring + stage * K::kStage + lane / 4 * JC * 64 + lane % 4 * 16;
             const int odd = lane / 4 % 2 * 64;
             stage = stage + 1 == K::kStages ? 0 : stage + 1;
-            float c[2][U][4] = {};          // two chains of additions
+            float c[2][4] = {};            // two chains of additions
 #pragma unroll
             for (int j = 0; j < JC; ++j) {
-                uint4 y[U];
+                uint4 y[2] = {};
 #pragma unroll
                 for (int u = 0; u < U; ++u) y[u] = *reinterpret_cast<const uint4*>(rows + u * JC * 512 + j * 64 + (j % 2 ? -odd : odd));
+                const uint32_t x0[4] = {y[0].x, y[0].y, y[0].z, y[0].w}, x1[4] = {y[1].x, y[1].y, y[1].z, y[1].w};
 #pragma unroll
                 for (int i = 0; i < K::MC; ++i) {
                     const uint2 f = *reinterpret_cast<const uint2*>(mine + (j * K::MC + i) * 24);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const uint32_t x[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
-                        if constexpr (F8) mma_f16(c[i % 2][u], f.x, 0u, f.y, 0u, e4m3x2_to_f16x2<false>(x[i]), e4m3x2_to_f16x2<true>(x[i]));
-                        else mma_bf16(c[i % 2][u], f.x, 0u, f.y, 0u, x[2 * i], x[2 * i + 1]);
-                    }
+                    if constexpr (F8)
+                        mma_f16(c[i % 2], e4m3x2_to_f16x2<false>(x0[i]), U > 1 ? e4m3x2_to_f16x2<false>(x1[i]) : 0u,
+                                e4m3x2_to_f16x2<true>(x0[i]), U > 1 ? e4m3x2_to_f16x2<true>(x1[i]) : 0u, f.x, f.y);
+                    else
+                        mma_bf16(c[i % 2], x0[2 * i], x1[2 * i], x0[2 * i + 1], x1[2 * i + 1], f.x, f.y);
                 }
             }
-            // The rows of terms are 4 lanes apart, and a lane has two pages of each 8: halves of what there is change
-            // hands while there are halves, then all add up.
-            float v[2 * U];
+            // lane 4 p has page p's (and 8 + p's) sums of the first two terms, its neighbour that of the third
 #pragma unroll
-            for (int i = 0; i < 2 * U; ++i) v[i] = (c[0][i / 2][i % 2] + c[1][i / 2][i % 2]) * part;
-            int which = 0;
-#pragma unroll
-            for (int k = U, w = 16; w >= 4; k /= 2, w /= 2) {
-                const bool up = lane & w;
-                if (k > 0) {
-                    which += up ? k : 0;
-#pragma unroll
-                    for (int i = 0; i < k; ++i) {
-                        const float give = up ? v[i] : v[i + k], stay = up ? v[i + k] : v[i];
-                        v[i] = stay + __shfl_xor_sync(0xffffffffu, give, w);
-                    }
-                } else {
-                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
-                }
+            for (int u = 0; u < U; ++u) {
+                const float first = c[0][2 * u] + c[1][2 * u], second = c[0][2 * u + 1] + c[1][2 * u + 1];
+                const float found = first + (second + __shfl_down_sync(0xffffffffu, first, 1));
+                const int at = u * 8 + lane / 4, known = __shfl_sync(0xffffffffu, had, at);
+                if (lane % 4 == 0 && known != INT_MIN) out[here.n * kBatch + at] = known < 0 ? -CUDART_INF_F : found * back;
             }
-            const int at = which / 2 * 8 + lane % 4 * 2 + which % 2, known = __shfl_sync(0xffffffffu, had, at);
-            constexpr int kCopies = U >= 4 ? 0 : U == 2 ? 4 : 12;     // bits of the lanes that have the same
-            if ((lane & kCopies) == 0 && known != INT_MIN) out[here.n * kBatch + at] = known < 0 ? -CUDART_INF_F : v[0] * back;
         }
     } while (next_head(here));
     cp_async_wait<0>();
