@@ -19,20 +19,27 @@
 // With up to 8 heads the other 8 rows hold the second term of each value: q (when
 // fp32) and the weights p enter as sums of two or three terms of the cache's
 // 16-bit type (f16 for E4M3, which holds its values), which keeps them to 16 bits and
-// more at no cost in MMAs; bf16 queries over an E4M3 cache as two E4M3 terms.
+// more at no cost in MMAs; bf16 queries are one term.
+//
+// The same kernel takes a table of pages and a length per key-value head (HEADS): a (request, head) is then
+// what a request is here.
 //
 // Measured: 1 x 131071 keys of 8 heads of 128, bf16 (537 MB) 87 us, 6.1 TB/s; 128
-// requests of 1 to 4096 keys, bf16 137 us, 6.3 TB/s, and E4M3 95 us, 4.6 TB/s: there the
-// chains of dependent instructions bound it, about 750 for a warp's 32 keys, which a scheduler's two
-// warps (255 registers each) issue at 0.35 a clock (105 us with a mask or shift more per conversion).
+// requests of 1 to 4096 keys, bf16 137 us, 6.3 TB/s, and E4M3 89 us, 4.9 TB/s: there the
+// chains of dependent instructions bound it, several hundred for a warp's 32 keys, which a scheduler's two
+// warps (255 registers each) issue at 0.35 a clock (E4M3 queries for E4M3 MMAs, which convert both operands
+// themselves, 95 us; 10 us more with a mask or shift more per conversion).
 // Two CTAs per SM with a ring of three stages beat three with two (64 x 2048 keys: bf16 91 and 98 us,
-// E4M3 58 and 66) and tiles of 16 keys (E4M3 69).
+// E4M3 58 and 66) and tiles of 16 keys (E4M3 69).  Offsets of a page's rows counted up instead of handed from lane
+// to lane, where the page holds all keys of a warp: E4M3 56 us instead of 58, but bf16 91 instead of 89.
+// 128 x 8 heads with up to 64 pages of 64 keys each (821 MB, E4M3) 156 us, 5.3 TB/s; 16 x 8 heads with 64 pages of 32
+// (117 MB, bf16) 30 us.
 //
 // Beyond 128 columns o, the scores and q do not fit the registers (124 to 960 bytes of spills) and a bf16
 // cache leaves one CTA to an SM: 64 x 2048 keys of 4 heads of 256, 16 query heads, bf16 102 us (77 % of
-// the cache's bytes at the copy rate), fp32 q 264, over E4M3 90 and 73.  More than 8 query heads of a key-value head
+// the cache's bytes at the copy rate), fp32 q 264, over E4M3 69 and 73.  More than 8 query heads of a key-value head
 // are one unit of 16 rows up to 128 columns without extra terms; otherwise every 8 of them are a unit of
-// their own and read the keys again: 64 / 4 heads of 128, bf16 54 us, fp32 q 92, over E4M3 49 and 59.
+// their own and read the keys again: 64 / 4 heads of 128, bf16 54 us, fp32 q 92, over E4M3 42 and 59.
 #pragma once
 
 #include <algorithm>

@@ -31,6 +31,10 @@ __device__ __forceinline__ void report_lengths(const PageArgs& a) {
 // few trips to it for the pages of a few new tokens.  A unit is 16 bytes of a head's row and all rows of a
 // page, so that a thread needs nothing of another; where there are fewer units than threads, up to 8
 // threads share the rows of a unit and meet in shared memory.
+//
+// Measured: 7 x 16383 tokens of 8 heads of 128 in pages of 64 (242 MB in bf16) 41 us, 6.0 TB/s, and E4M3 23, 5.3;
+// 33 requests with a new token each 4.4. With 16 or 4 rows in flight and 2 or 6 blocks per SM 40 and 45 us (E4M3 26 and
+// 32), 4 blocks 41 (E4M3 26); without sharing, 128 new tokens of one head 9.2 instead of 5.2.
 constexpr int kBoundsThreads = 256;
 constexpr int kBoundsParts = 8;
 constexpr int kBoundsBlocks = 3;            // per SM
@@ -170,8 +174,15 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsBlocks) page_bounds_ker
 // conversions of both operands), 24 bits of them and more.
 // A lane reads 16 bytes of its page at a time, in any order of d, as a dot product does not mind it.
 // Every warp works alone on a run of batches of one or several heads, with the rows of the next batches on their way
-// into shared memory, a lane's pieces into places of its own; where a head begins the warp forms its terms of q
-// meanwhile.
+// into shared memory; where a head begins the warp forms its terms of q meanwhile.
+//
+// Measured, 128 requests of 0 to 32768 tokens in pages of 32, 56 / 8 heads of 128: E4M3 (112 MB) 31.5 us, bf16 (221 MB) 47; a
+// request of 2048 pages, 16 / 4 heads 5.5. About 7 us of that are launch, lengths, shares, page numbers and first
+// rows, the rest streams at 5.2 to 5.6 TB/s; 4 blocks per SM or other numbers of stages change nothing. Ruled out: a
+// page's values to 16 lanes with fp32 multiply-adds 59 us (E4M3); the terms formed by a block instead of a warp 38 to 48;
+// all heads of a page in one block 46 to 57; a bulk copy per page 30 with 8-bit MMAs, as fast as these copies then, but
+// issued one lane after another; pieces copied in the order in which they are read (64 bytes a page and instruction) 5 %
+// slower.
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kScoreBlocks = 3;             // per SM
