@@ -445,9 +445,10 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
 // (8 bits each, from the highest bit in which two of them differ), until they are few enough to be compared with one
 // another.  The pages above it, with the first ones equal to it, are written in order.  Trips to memory, barriers and
 // chains of instructions bound it: a thread has up to 8 keys in registers from one trip, a warp consecutive ones.
-// (Keys in shared memory and four digits: 8.5 instead of 5.6 us for 4 heads of 2048 pages, 17 instead of 13.4 for
+// (Keys in shared memory and four digits: 8.5 instead of 5.6 us for 4 heads of 2048 pages, 17 instead of 12.1 for
 // 1024 heads of up to as many.)
 constexpr int kSelectItems = 8;             // keys of a thread; more pages go in turns, read again each time
+constexpr int kSelectGroup = 2;             // and those that are gone through without a branch
 constexpr int kSelectRank = 128;            // keys that are compared with one another
 
 // Keys of no page, and of a forced one.
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
         for (int j = 0; j < kSelectItems; ++j) f[j] = j < items && first + 32 * j < end ? scores[first + 32 * j] : 0.0f;
 #pragma unroll
         for (int j = 0; j < kSelectItems; ++j) {
+            if (j % kSelectGroup == 0 && j >= items) break;
             const int i = first + 32 * j;
             k[j] = j >= items || i >= end ? kNone : i < a.sinks || i >= pages - a.recent ? kForced : key_of(f[j]);
         }
@@ -503,11 +505,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
     uint32_t low = kForced, high = 0u;      // of the others
     each([&] {
 #pragma unroll
-        for (int j = 0; j < kSelectItems; ++j)
-            if (k[j] != kNone && k[j] != kForced) {
-                low = min(low, k[j]);
-                high = max(high, k[j]);
-            }
+        for (int j = 0; j < kSelectItems; ++j) {
+            if (j % kSelectGroup == 0 && j >= items) break;
+            if (k[j] == kNone || k[j] == kForced) continue;
+            low = min(low, k[j]);
+            high = max(high, k[j]);
+        }
     });
     __syncwarp();
     low = __reduce_min_sync(0xffffffffu, low);
@@ -533,8 +536,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
         const int take = min(bits, 8), shift = bits - take;
         each([&] {
 #pragma unroll
-            for (int j = 0; j < kSelectItems; ++j)
+            for (int j = 0; j < kSelectItems; ++j) {
+                if (j % kSelectGroup == 0 && j >= items) break;
                 if (in_question(k[j])) atomicAdd(hist + (k[j] >> shift & ((1u << take) - 1u)), 1u);
+            }
         });
         __syncthreads();
         // one warp looks for the digit, 8 to a lane, the greatest ones in lane 0
@@ -575,6 +580,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < kSelectItems; ++j) {
+                if (j % kSelectGroup == 0 && j >= items) break;
                 in[j] = __ballot_sync(0xffffffffu, in_question(k[j]));
                 all += __popc(in[j]);
             }
@@ -582,6 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
             at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
             for (int j = 0; j < kSelectItems; ++j) {
+                if (j % kSelectGroup == 0 && j >= items) break;
                 if (in[j] >> lane & 1u) list[at + __popc(in[j] & ((1u << lane) - 1u))] = k[j];
                 at += __popc(in[j]);
             }
@@ -616,6 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kSelectItems; ++j) {
+            if (j % kSelectGroup == 0 && j >= items) break;
             entry[j] = k[j] >= value && k[j] != kNone ? row[first + 32 * j] : 0;
             more[j] = __ballot_sync(0xffffffffu, k[j] > value);
             same[j] = __ballot_sync(0xffffffffu, k[j] == value);
@@ -641,6 +649,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
         const uint32_t before = (1u << lane) - 1u;
 #pragma unroll
         for (int j = 0; j < kSelectItems; ++j) {
+            if (j % kSelectGroup == 0 && j >= items) break;
             const uint32_t e = eq + __popc(same[j] & before);
             if ((more[j] >> lane & 1u) || ((same[j] >> lane & 1u) && e < need)) {
                 out[up + __popc(more[j] & before) + min(e, need)] = entry[j];
