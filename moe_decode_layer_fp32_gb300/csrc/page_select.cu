@@ -302,10 +302,12 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < U * JC; ++i) {
-            // a page that is not there has another's values, and pieces behind the last one that: they meet
-            // terms of 0, or nobody looks at the sum
+            // A page that is not there stays what the stage has (nobody looks at its sum; reads of some page instead
+            // of it, the same for all warps, took 13.4 us for 128 requests of one page, and 5.4 without). Pieces behind the
+            // last one are that one: they meet terms of 0.
             const int at = (i * 32 + lane) / (4 * JC), piece = (i * 32 + lane) % (4 * JC);
-            const int page = max(__shfl_sync(0xffffffffu, id, at), 0);
+            const int page = __shfl_sync(0xffffffffu, id, at);
+            if (page < 0) continue;
             const char* from = static_cast<const char*>(a.bounds) + page * page_bytes + ((long long)g * pieces + min(piece, pieces - 1)) * 16;
             cp_async16_to(place + stage_in * K::kStage + (at * 4 * JC + (piece ^ (at & 1) << 2)) * 16, from);
         }
