@@ -176,23 +176,22 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsBlocks) page_bounds_ker
 // Every warp works alone on a run of batches of one or several heads, with the rows of the next batches on their way
 // into shared memory; where a head begins the warp forms its terms of q meanwhile.
 //
-// Measured, 128 requests of 0 to 32768 tokens in pages of 32, 56 / 8 heads of 128: E4M3 (112 MB) 31.5 us, bf16 (221 MB) 47; a
-// request of 2048 pages, 16 / 4 heads 5.5. About 7 us of that are launch, lengths, shares, page numbers and first
-// rows, the rest streams at 5.2 to 5.6 TB/s; 4 blocks per SM or other numbers of stages change nothing. Ruled out: a
+// Measured, 128 requests of 0 to 32768 tokens in pages of 32, 56 / 8 heads of 128: E4M3 (112 MB) 26 us, bf16 (221 MB) 46; a
+// request of 2048 pages, 16 / 4 heads 5.4. About 5 us of that are launch, lengths, shares, page numbers and first
+// rows, the rest streams at 5.2 to 5.4 TB/s; other numbers of stages or blocks per SM change 3 %. Ruled out: a
 // page's values to 16 lanes with fp32 multiply-adds 59 us (E4M3); the terms formed by a block instead of a warp 38 to 48;
-// all heads of a page in one block 46 to 57; a bulk copy per page 30 with 8-bit MMAs, as fast as these copies then, but
-// issued one lane after another; pieces copied in the order in which they are read (64 bytes a page and instruction) 5 %
-// slower.
+// all heads of a page in one block 46 to 57; a bulk copy per page 30 when these copies took 32 (it is issued one lane after
+// another); pieces copied in the order in which they are read (64 bytes a page and instruction) 5 % slower; a page read in
+// the place of one that a batch does not have, the same for all warps, 31.5.
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreBlocks = 3;             // per SM
 constexpr int kScoreSetup = 1;              // what the terms of q cost, in batches
 
 // 4 JC pieces of 16 bytes: a page's 2 D values, rounded up.  U: 8 U pages are a batch.
 template <bool F8, int JC>
 struct Scores {
     static constexpr int E = F8 ? 16 : 8, MC = E / 4;        // values of a piece, and its MMAs
-    static constexpr int U = JC >= 8 ? 1 : 2;
+    static constexpr int U = JC >= 8 ? 1 : 8 / JC;
     static constexpr int kBatch = 8 * U;
     static constexpr int kValues = 4 * JC * E;
     static constexpr int V = kValues > 256 ? kValues / 32 : 8;   // of a lane, in the terms of q
@@ -202,7 +201,7 @@ struct Scores {
     static constexpr int kStages = 3;
     static constexpr int kWarpBytes = kStages * kStage + kWords * 4;
     static constexpr int kSmem = kScoreWarps * kWarpBytes;
-    static constexpr int kBlocksPerSm = JC <= 2 ? 4 : JC >= 16 ? 2 : F8 && JC >= 8 ? 3 : kScoreBlocks;
+    static constexpr int kBlocksPerSm = JC >= 16 ? 2 : JC >= 8 ? 3 : 4;
     static_assert(kBatch <= 32, "a lane's page");
     static_assert(kBlocksPerSm * (kSmem + 1280) <= 228 * 1024, "blocks that run at once");
 };
@@ -410,27 +409,34 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
             const char* rows = ring + stage * K::kStage + lane / 4 * JC * 64 + lane % 4 * 16;
             const int odd = lane / 4 % 2 * 64;
             stage = stage + 1 == K::kStages ? 0 : stage + 1;
-            float c[2][4] = {};            // two chains of additions
+            constexpr int G = (U + 1) / 2;          // 16 pages each
+            float c[G][2][4] = {};                  // two chains of additions
 #pragma unroll
             for (int j = 0; j < JC; ++j) {
-                uint4 y[2] = {};
+                uint4 y[2 * G] = {};
 #pragma unroll
                 for (int u = 0; u < U; ++u) y[u] = *reinterpret_cast<const uint4*>(rows + u * JC * 512 + j * 64 + (j % 2 ? -odd : odd));
-                const uint32_t x0[4] = {y[0].x, y[0].y, y[0].z, y[0].w}, x1[4] = {y[1].x, y[1].y, y[1].z, y[1].w};
 #pragma unroll
                 for (int i = 0; i < K::MC; ++i) {
                     const uint2 f = *reinterpret_cast<const uint2*>(mine + (j * K::MC + i) * 24);
-                    if constexpr (F8)
-                        mma_f16(c[i % 2], e4m3x2_to_f16x2<false>(x0[i]), U > 1 ? e4m3x2_to_f16x2<false>(x1[i]) : 0u,
-                                e4m3x2_to_f16x2<true>(x0[i]), U > 1 ? e4m3x2_to_f16x2<true>(x1[i]) : 0u, f.x, f.y);
-                    else
-                        mma_bf16(c[i % 2], x0[2 * i], x1[2 * i], x0[2 * i + 1], x1[2 * i + 1], f.x, f.y);
+#pragma unroll
+                    for (int k = 0; k < G; ++k) {
+                        const uint4 y0 = y[2 * k], y1 = y[2 * k + 1];
+                        const uint32_t x0[4] = {y0.x, y0.y, y0.z, y0.w}, x1[4] = {y1.x, y1.y, y1.z, y1.w};
+                        if constexpr (F8)
+                            mma_f16(c[k][i % 2], e4m3x2_to_f16x2<false>(x0[i]), U > 1 ? e4m3x2_to_f16x2<false>(x1[i]) : 0u,
+                                    e4m3x2_to_f16x2<true>(x0[i]), U > 1 ? e4m3x2_to_f16x2<true>(x1[i]) : 0u, f.x, f.y);
+                        else
+                            mma_bf16(c[k][i % 2], x0[2 * i], x1[2 * i], x0[2 * i + 1], x1[2 * i + 1], f.x, f.y);
+                    }
                 }
             }
             // lane 4 p has page p's (and 8 + p's) sums of the first two terms, its neighbour that of the third
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float first = c[0][2 * u] + c[1][2 * u], second = c[0][2 * u + 1] + c[1][2 * u + 1];
+                const float(&c0)[4] = c[u / 2][0];
+                const float(&c1)[4] = c[u / 2][1];
+                const float first = c0[u % 2 * 2] + c1[u % 2 * 2], second = c0[u % 2 * 2 + 1] + c1[u % 2 * 2 + 1];
                 const float found = first + (second + __shfl_down_sync(0xffffffffu, first, 1));
                 const int at = u * 8 + lane / 4, known = __shfl_sync(0xffffffffu, had, at);
                 if (lane % 4 == 0 && known != INT_MIN) out[here.n * kBatch + at] = known < 0 ? -CUDART_INF_F : found * back;
