@@ -161,8 +161,10 @@ __global__ void __launch_bounds__(THREADS) qk_append_kernel(const __grid_constan
     // the thread's heads of a slice: from here on, lanes apart
     auto first_q = [&](int slice) { return slice * nq * lanes + hl; };
     auto first_kv = [&](int slice) { return slice * nkv * lanes + hl; };
-    auto copy = [&](char* dst, const void* p, long long i) {
-        const char* src = static_cast<const char*>(p) + i * (BF ? 2 : 4);
+    constexpr int kSize = BF ? 2 : 4;
+    const long long q_step = lanes * a.q_hs * kSize, o_step = lanes * a.o_hs * kSize;     // bytes from a head of the thread to the next
+    const int apart = (it.i1 - it.i0) * kSize;
+    auto copy = [&](char* dst, const char* src) {
         if constexpr (WB == 8) cp_async8(dst, src);
         else cp_async16(dst, src);
         if constexpr (WB == 32) cp_async16(dst + 16, src + 16);
@@ -172,18 +174,17 @@ __global__ void __launch_bounds__(THREADS) qk_append_kernel(const __grid_constan
         bool bad = false;
         const int q1 = on ? min(a.q_heads, first_q(slice) + nq * lanes) : 0, kv1 = on && pos >= 0 ? min(2 * kvh, first_kv(slice) + nkv * lanes) : 0;
         char* to = place(buf, 0, 0);
-        for (int h = first_q(slice); h < q1; h += lanes, to += 2 * THREADS * WB) {
-            const long long o = t * a.q_ts + h * a.q_hs;
-            copy(to, a.q, o + it.i0);
-            if (it.two) copy(to + THREADS * WB, a.q, o + it.i1);
+        const char* src = static_cast<const char*>(a.q) + (t * a.q_ts + first_q(slice) * a.q_hs + it.i0) * kSize;
+        for (int h = first_q(slice); h < q1; h += lanes, to += 2 * THREADS * WB, src += q_step) {
+            copy(to, src);
+            if (it.two) copy(to + THREADS * WB, src + apart);
         }
         to = place(buf, nq, 0);
         for (int h = first_kv(slice); h < kv1; h += lanes, to += 2 * THREADS * WB) {
             const bool k = h < kvh;
-            const void* p = k ? a.k : a.v;
-            const long long o = k ? t * a.k_ts + h * a.k_hs : t * a.v_ts + (h - kvh) * a.v_hs;
-            copy(to, p, o + it.i0);
-            if (it.two) copy(to + THREADS * WB, p, o + it.i1);
+            src = static_cast<const char*>(k ? a.k : a.v) + ((k ? t * a.k_ts + h * a.k_hs : t * a.v_ts + (h - kvh) * a.v_hs) + it.i0) * kSize;
+            copy(to, src);
+            if (it.two) copy(to + THREADS * WB, src + apart);
         }
         if (with_axes) {
 #pragma unroll
@@ -335,19 +336,20 @@ __global__ void __launch_bounds__(THREADS) qk_append_kernel(const __grid_constan
         const char* from = place(buf, 0, 0);
         factors(weights);
         int h = first_q(slice);
-        for (; h + lanes < q1; h += 2 * lanes, from += 2 * kPass) {
+        char* to = static_cast<char*>(a.q_out) + (t * a.o_ts + h * a.o_hs) * kSize;
+        for (; h + lanes < q1; h += 2 * lanes, from += 2 * kPass, to += 2 * o_step) {
             float2 x[2][N], y[2][N];
             get(from, x[0], y[0]);
             get(from + kPass, x[1], y[1]);
             norm(x, y);
-            put(a.q_out, kType, t * a.o_ts + h * a.o_hs, x[0], y[0], 1.0f);
-            put(a.q_out, kType, t * a.o_ts + (h + lanes) * a.o_hs, x[1], y[1], 1.0f);
+            put(to, kType, 0, x[0], y[0], 1.0f);
+            put(to + o_step, kType, 0, x[1], y[1], 1.0f);
         }
         if (h < q1) {
             float2 x[1][N], y[1][N];
             get(from, x[0], y[0]);
             norm(x, y);
-            put(a.q_out, kType, t * a.o_ts + h * a.o_hs, x[0], y[0], 1.0f);
+            put(to, kType, 0, x[0], y[0], 1.0f);
         }
         from = place(buf, nq, 0);
         const int slot = pos - pos / P * P;
