@@ -218,7 +218,9 @@ int moe_page_bounds(const moe_kv_cache* cache, void* bounds, const int32_t* bloc
  * (times the cache's scales): no key of the page has a greater sum of q . k over
  * these heads.  Computed as
  *   sum_d (sum_h min(q, 0)) lo[d] + (sum_h max(q, 0)) hi[d],
- * so an infinite bound may make a score NaN.  -inf for a page outside the cache (status).
+ * so an infinite query or bound may make a score NaN.  Within fp32 accuracy; over an
+ * E4M3 cache a channel's sum of q below 2^-14 of the head's greatest is kept to 2^-38 of that, not to
+ * 24 bits of its own.  -inf for a page outside the cache (status).
  *   q           [B, q_heads, D] F32 or BF16, strides as in moe_attn_decode
  *   scores      float[B, heads, max_pages] packed; entries behind a request's
  *               pages are left alone

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
     here.g = (int)div_u(s.at, here.nb + kScoreSetup);
     take(here, (int)(s.at - (long long)here.g * (here.nb + kScoreSetup)));
     if (here.n >= here.last && !next_head(here)) return;
-    // ---- the copies, K::kStages - 1 batches ahead
+    // ---- the copies, kStages - 1 batches ahead
     Walk ahead = here;
     bool more = true;
     int stage_in = 0;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
         const int col = ahead.n * kBatch + lane;
         return lane < kBatch && col < ahead.np ? max(a.table[ahead.b * a.table_ld + col], -1) : INT_MIN;
     };
-    int id_next = ask(), ids[K::kStages];          // pages of the batches under way, a lane each (INT_MIN: none, -1: no such)
+    int id_next = ask(), ids[K::kStages - 1];      // pages of the batches under way, a lane each (INT_MIN: none, -1: no such)
     auto feed = [&](int& id) {
         id = INT_MIN;
         if (!more) return;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
         else add(std::integral_constant<int, MOE_DTYPE_F32>());
         float back = a.c.k_scale ? a.c.k_scale[here.g] : 1.0f;
         if constexpr (F8) {
-            // a power of two brings the greatest between 2^14 and 2^15: f16 holds it, and 2^-38 of it
+            // a power of two brings the greatest between 2^14 and 2^15: f16 holds it, and three terms 2^-38 of it
             float most = 0.0f;
 #pragma unroll
             for (int e = 0; e < V; ++e) most = fmaxf(most, fabsf(q[e]));

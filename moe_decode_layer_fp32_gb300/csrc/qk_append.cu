@@ -7,14 +7,15 @@
 // the tokens with the next one's rows on their way into shared memory.  The threads of a head are a power
 // of two, so that its sum of squares is a few shuffles.  The weights and cos, sin become one set of factors per
 // token and thread, so that a pair costs two multiplications and two multiply-adds, and one more of each
-// of its values with 1 / sqrt; two heads at a time hide one another's shuffles.  With several axes every element of cos, sin comes from the row of its pair's axis: single
-// words copied into one row, which is read like any other.
+// of its values with 1 / sqrt; two heads at a time hide one another's shuffles.  With several axes every element
+// of cos, sin comes from the row of its pair's axis: single words copied into one row, which is read like any other.
 //
 // Measured, 12345 tokens of 56 + 8 + 8 heads of 128, bf16 into E4M3, half of each head rotated by three axes (430 MB):
-// 79 us, 5.4 TB/s (with one axis 79; the append without norms 67); 54 M warp instructions at 0.57 a clock and
-// scheduler bound it. One head at a time 86 us, the append's kernel with plain multiplications 104; at 102 registers
-// instead of 128 (5 blocks per SM instead of 4) 89. 12345 tokens of 32 + 8 + 8 heads of 64 43 us (blocks of 128 threads 46),
-// of 80 with 40 rotated, in vectors of 4, 72 (an element at a time 240).
+// 77 us, 5.6 TB/s (with one axis 76; the append without norms 67). The instructions bound it, at 0.57 a clock and
+// scheduler. One head at a time 86 us, the append's kernel with plain multiplications 104; at 102 registers
+// instead of 117 (5 blocks per SM instead of 4) 89. 12345 tokens of 32 + 8 + 8 heads: of 64 34 us (blocks of 128 threads
+// 46 before, and 43 of 64), of 80 62 (5 of 8 threads have an item; 6 heads of 5 threads to a warp, with sums one
+// thread after another, 64), of 80 with 40 rotated, in vectors of 4, 67 (an element at a time 240).
 #include <algorithm>
 
 #include <math_constants.h>

@@ -594,6 +594,64 @@ def test_a_step_on_another_stream_and_in_graphs(B):
         check()
 
 
+def test_padding_in_a_step(B):
+    """A slot of the batch without a request: position -1, length 0; the others are as without it."""
+    c = chain(B, T=4, seed=7)
+    c["step"]()
+    torch.cuda.synchronize()
+    want = {n: c[n].clone() for n in ("out", "tables", "kept")}
+    c["pos"][1], c["seq"][1] = -1, 0
+    for n in want:
+        c[n].fill_(5)
+    c["step"]()
+    torch.cuda.synchronize()
+    assert (c["out"][1] == 0).all() and (c["tables"][1] == -1).all() and (c["kept"][1] == 0).all()
+    for n, t in want.items():
+        for b in (0, 2, 3):
+            assert torch.equal(c[n][b], t[b])
+    c["seq"][2], c["pos"][2] = -3, -1             # a negative length is none
+    c["step"]()
+    torch.cuda.synchronize()
+    assert (c["out"][2] == 0).all() and torch.equal(c["out"][3], want["out"][3])
+
+
+def test_steps_on_two_streams_at_once(B):
+    cs = [chain(B, seed=8), chain(B, "e4m3", T=9, seed=9, prompt=700)]
+    want = []
+    for c in cs:
+        c["step"]()
+        torch.cuda.synchronize()
+        want.append([c[n].clone() for n in ("q", "out", "tables", "kept")])
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                c["step"]()
+    torch.cuda.synchronize()
+    for c, w in zip(cs, want):
+        for n, t in zip(("q", "out", "tables", "kept"), w):
+            assert torch.equal(c[n], t), n
+
+
+def test_scores_of_infinite_values(B):
+    """An infinite query or bound makes its own head's or page's scores infinite or NaN, and no other."""
+    for dtype in ("bf16", "e4m3"):
+        g = gen(24)
+        k, v, ks, vs, cache = make_cache(B, g, 4, 16, 2, 64, dtype)
+        bounds = B.new_page_bounds(cache)
+        table, seq = torch.tensor([[0, 1, 2, 3]], **INT), torch.tensor([64], **INT)
+        B.moe_page_bounds(cache, bounds, table, seq)
+        q, scores = normal(g, 1, 4, 64), torch.zeros(1, 2, 4, device="cuda")
+        if dtype == "bf16":
+            bounds[2, 0, 1, 7] = math.inf
+        q[0, 3, 5] = -math.inf
+        B.moe_page_scores(q, cache, bounds, table, seq, scores)
+        assert not torch.isfinite(scores[0, 1]).any()
+        assert torch.isfinite(scores[0, 0]).tolist() == [True, True, dtype == "e4m3", True]
+
+
 # ------------------------------------------------------------------ far and odd places
 
 

@@ -145,7 +145,10 @@ def test_qk_append_heads(B, hq, hkv, T):
 
 def test_qk_append_strides_in_place_and_without_q(B):
     run(B, pad=8, seed=6)
-    run(B, pad=3, seed=6)                    # rows that are not 16 bytes apart
+    run(B, pad=4, seed=6)                    # rows that are not a multiple of 16 bytes apart, but of 8
+    run(B, shift=4, A=3, rot=64, seed=6)
+    run(B, pad=4, x="f32", D=80, rot=80, hq=9, seed=6)
+    run(B, pad=3, seed=6)                    # nor of 8
     run(B, shift=1, seed=7)                  # nor aligned
     run(B, shift=1, x="f32", A=2, seed=7)
     run(B, in_place=True, seed=8)
