@@ -205,8 +205,8 @@ int moe_attn_decode(const void* q, int q_dtype, int64_t q_batch_stride, int64_t 
  *               the cache's scales), 16-byte aligned
  *   first       int32[B] or NULL
  * A NaN key makes the least or the greatest of its channel NaN, or both.  Pages outside
- * the cache are skipped (status).  Bounds of other pages are left alone.  A
- * page of several requests gets the bounds of one of them.
+ * the cache are skipped (status).  Bounds of other pages are left alone.  The bounds of
+ * a page that several requests end in, with different numbers of its tokens, may mix theirs.
  */
 int moe_page_bounds(const moe_kv_cache* cache, void* bounds, const int32_t* block_table, int64_t table_ld,
                     int max_pages, int B, const int32_t* seq_lens, const int32_t* first, int32_t* status,
