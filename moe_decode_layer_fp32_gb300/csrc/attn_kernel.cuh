@@ -61,6 +61,9 @@ constexpr int kJoinGroup = 16;
 // for 128 ragged bf16 requests in order of length, 134, 92, 94, 98 for E4M3 with a cap, 10.2, 10.1, 10.8,
 // 12.0 for one request of 777 keys.
 constexpr int kTileCost = 2, kUnitCost = 3;
+// Units of so many tiles go to one CTA (HEADS): 4 heads of 2, 4, 5, 6 and 8 tiles of bf16 keys take 6.7, 8.5, 9.6, 10.5
+// and 12.2 us in one piece, and 13.2, 9.8, 9.8, 10.0 and 10.1 in parts that are joined.
+constexpr int kWholeTiles = 5;
 // The fast tanh is off by 2^-22 of the cap: up to 256, 2^-14 of a weight, where a bf16 output is rounded to
 // 2^-9.  Larger caps take the kernel of fp32 outputs, with tanhf (64 x 2048 keys, bf16 91 and 94 us, E4M3 60
 // and 60; with 16 heads to a key-value head, which that kernel takes in two parts, 96 and 181, 88 and 110).
@@ -98,8 +101,11 @@ struct Cursor {
 };
 // Of a unit of so many tiles.
 __device__ __forceinline__ int span_of(int tiles) { return tiles > 0 ? kTileCost * tiles + kUnitCost : 0; }
-// Tiles of the cursor's unit that begin before position p.
+// Tiles of the cursor's unit that begin before position p; a unit of up to `whole` tiles is not divided and has all of
+// them at its beginning.
+template <int whole>
 __device__ __forceinline__ int tiles_before(const Cursor& c, long long p) {
+    if (whole > 0 && c.tiles <= whole) return p > c.base ? c.tiles : 0;
     const long long n = p - c.base - kUnitCost;
     return n <= 0 ? 0 : (int)min((n + kTileCost - 1) / kTileCost, (long long)c.tiles);
 }
@@ -147,6 +153,7 @@ struct Attn {
     static constexpr uint32_t kLeast2 = 0x00800080u;
     static constexpr float kPShift = F8 ? 7.0f : 0.0f;
     static constexpr int kCtasPerSm = kTileBytes > 4096 ? 1 : 2;
+    static constexpr int kWhole = HEADS ? kWholeTiles : 0;
     static constexpr int kStages = 3;
     static constexpr size_t kRing = (size_t)kAttnWarps * kStages * 2 * kTileBytes;
     static constexpr int kQBytes = ROWS * DP * (EX ? 4 : 2);         // a unit's query rows
@@ -215,7 +222,7 @@ struct Attn {
                 set_request(a, c);
             } while (c.tiles == 0);
         }
-        c.last = tiles_before(c, end);
+        c.last = tiles_before<kWhole>(c, end);
     }
     // Page and slot of the key that lane `lane` looks after in the warp's tile; page -1: none.
     __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
@@ -837,8 +844,8 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
     K::set_request(a, c);
     c.unit = (int)div_u(start - sh.found_pre, span_of(c.tiles));
     c.base = sh.found_pre + (long long)c.unit * span_of(c.tiles);
-    c.tile = tiles_before(c, start);
-    c.last = tiles_before(c, end);
+    c.tile = tiles_before<K::kWhole>(c, start);
+    c.last = tiles_before<K::kWhole>(c, end);
     if (c.tile == c.tiles) {            // the part begins with the end of a unit
         --c.tile;
         K::advance(a, units, end, c);
@@ -905,8 +912,19 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
         if (!whole) {
             const int c_first = share.cta_of(seg.base + kUnitCost);
             const int c_last = share.cta_of(seg.base + kUnitCost + (long long)kTileCost * (seg.tiles - 1));
-            // the unit is the first one of CTA c_first unless that also has the last tile before it
-            const bool head = seg.base == 0 || share.start(c_first) > seg.base - kTileCost;
+            // the unit is the first one of CTA c_first unless that also has the last tile before it (all of the
+            // unit before it where that is not divided)
+            long long before = seg.base - kTileCost;       // where that begins
+            if (K::kWhole > 0 && seg.unit == 0 && seg.base > 0) {
+                Cursor p;
+                p.b = seg.b;
+                do {
+                    --p.b;
+                    K::set_request(a, p);
+                } while (p.tiles == 0);
+                if (p.tiles <= K::kWhole) before = seg.base - span_of(p.tiles);
+            }
+            const bool head = seg.base == 0 || share.start(c_first) > before;
             const int n = c_last - c_first + 1;
             auto part_at = [&](int i) { return part_of(c_first + i, i > 0 || head); };
             uint32_t* done = a.done + (long long)seg.b * units + seg.unit;
