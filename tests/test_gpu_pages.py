@@ -434,6 +434,49 @@ def test_attn_pages_long_and_many(B, counts, hq, hkv, dtype):
     pages_case(B, counts, hq, hkv, D=64, dtype=dtype, pages=200, seed=4)
 
 
+@pytest.mark.parametrize("dtype,q", [("bf16", "bf16"), ("e4m3", "bf16"), ("bf16", "f32")])
+def test_attn_pages_mixes_of_short_and_long(B, dtype, q):
+    """Lists that a CTA takes whole next to lists that several share, cut at many places: 30 mixes, each twice over one
+    workspace (the counters are zero again)."""
+    host = torch.Generator()
+    host.manual_seed(30)
+
+    def pick(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=host))
+
+    g = gen(30)
+    D, page, pages, hkv = 64, 16, 300, 2
+    k, v, ks, vs, cache = make_cache(B, g, pages, page, hkv, D, dtype)
+    kd, vd = ((O.f64(c) * (O.f64(s)[:, None] if s is not None else 1.0)).cuda() for c, s in ((k, ks), (v, vs)))
+    ws = B.new_attn_workspace(64, 8, hkv, D)
+    for i in range(30):
+        nb = pick(1, 60)
+        lens = torch.zeros(nb, hkv, dtype=torch.int32)
+        for b in range(nb):
+            for h in range(hkv):
+                kind = pick(0, 5)
+                lens[b, h] = 0 if kind == 0 else pick(1, 700) if kind < 4 else pick(700, 4000)
+        width = max(1, -(-int(lens.max()) // page))
+        tables = torch.randint(0, pages, (nb, hkv, width), generator=g, device="cuda", dtype=torch.int32)
+        lens = lens.cuda()
+        qt = normal(g, nb, 8, D, std=1.5, dtype=DT[q])
+        out = torch.full((nb, 8, D), 9.0, dtype=DT[q], device="cuda")
+        at = torch.arange(width * page, device="cuda")
+        want = torch.zeros(nb, hkv, 4, D, dtype=torch.float64, device="cuda")
+        for h in range(hkv):
+            rows = tables[:, h].long()[:, at // page]
+            s = torch.einsum("bgd,bld->bgl", qt.double().view(nb, hkv, 4, D)[:, h], kd[rows, at % page, h]) * 0.125
+            seen = (at < lens[:, h, None])[:, None]
+            s = torch.where(seen, s, -math.inf)
+            p = torch.nan_to_num(torch.softmax(s, -1))
+            want[:, h] = torch.einsum("bgl,bld->bgd", p, vd[rows, at % page, h])
+        for _ in range(2):
+            B.moe_attn_pages(qt, cache, tables, lens, 0.125, out, ws)
+            bound = 1e-4 * vd.abs().max().item() + (1.01 * BF * want.abs() if q == "bf16" else 0.0)
+            assert ((out.double().view_as(want) - want).abs() <= bound).all(), f"mix {i}"
+    assert B.moe_read_status(ws)[0] == 0
+
+
 def test_attn_pages_equal_calls_give_equal_bits(B):
     go, ot, lt = pages_case(B, [[5000, 700], [0, 3], [999, 4000]], 8, 2, q="f32", seed=5)
     first = ot.clone(), lt.clone()
