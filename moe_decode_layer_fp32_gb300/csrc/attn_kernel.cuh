@@ -792,11 +792,16 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
         }
         return incl;
     };
-    const int s0 = tid < a.B ? span_of(tiles_of(tid)) : 0;      // of the first block
+    // HEADS: there are many, and a thread has equally many in a row instead, so that one scan is enough
+    const int per = HEADS ? (a.B - 1) / kAttnThreads + 1 : 1;
+    const int s0 = !HEADS && tid < a.B ? span_of(tiles_of(tid)) : 0;      // of the first block
+    long long mine0 = s0;
+    if constexpr (HEADS)
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine0 += span_of(tiles_of(b));
     long long sum0, total;
-    const long long incl0 = scan((long long)s0 * units, sum0);
+    const long long incl0 = scan(mine0 * units, sum0);
     total = sum0;
-    if (a.B > kAttnThreads) {
+    if (!HEADS && a.B > kAttnThreads) {
         long long mine = 0;
         for (int b = kAttnThreads + tid; b < a.B; b += kAttnThreads) mine += span_of(tiles_of(b));
         long long rest;
@@ -823,9 +828,22 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
     const Share share(min((long long)gridDim.x, div_u(total, kTileCost + kUnitCost)), total);
     if (blockIdx.x >= share.ctas) return;
     const long long start = share.start(blockIdx.x), end = share.start(blockIdx.x + 1);
+    if constexpr (HEADS) {
+        long long pre = incl0 - mine0 * units;
+        if (start >= pre && start < incl0) {
+            int b = tid * per - 1;
+            long long next = pre;
+            do {
+                pre = next;
+                next += (long long)span_of(tiles_of(++b)) * units;
+            } while (start >= next);
+            sh.found_b = b;
+            sh.found_pre = pre;
+        }
+    }
     long long sum = 0, incl = incl0, all = sum0;
     int span = s0, b0 = 0;
-    while (true) {
+    while (!HEADS) {
         const long long pre = sum + incl - (long long)span * units;
         if (start >= pre && start < sum + incl) {
             sh.found_b = b0 + tid;
