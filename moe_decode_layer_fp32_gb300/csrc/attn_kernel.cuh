@@ -32,7 +32,7 @@
 // Two CTAs per SM with a ring of three stages beat three with two (64 x 2048 keys: bf16 91 and 98 us,
 // E4M3 58 and 66) and tiles of 16 keys (E4M3 69).  Offsets of a page's rows counted up instead of handed from lane
 // to lane, where the page holds all keys of a warp: E4M3 56 us instead of 58, but bf16 91 instead of 89.
-// 128 x 8 heads with up to 64 pages of 64 keys each (821 MB, E4M3) 156 us, 5.3 TB/s; 16 x 8 heads with 64 pages of 32
+// 128 x 8 heads with up to 64 pages of 64 keys each (821 MB, E4M3) 145 us, 5.7 TB/s; 16 x 8 heads with 64 pages of 32
 // (117 MB, bf16) 30 us.
 //
 // Beyond 128 columns o, the scores and q do not fit the registers (124 to 960 bytes of spills) and a bf16
@@ -60,7 +60,11 @@ constexpr int kJoinGroup = 16;
 // What a tile and the beginning and end of a unit cost.  Unit costs of 1, 3, 5 and 8: 204, 137, 136, 136 us
 // for 128 ragged bf16 requests in order of length, 134, 92, 94, 98 for E4M3 with a cap, 10.2, 10.1, 10.8,
 // 12.0 for one request of 777 keys.
-constexpr int kTileCost = 2, kUnitCost = 3;
+// HEADS: a unit has a length and a table row of its own; unit costs of 3, 5 and 6: 58, 52 and 51 us for 1024 ragged
+// lists of up to 1000 bf16 keys, 154, 145 and 146 for 1024 of up to 4096 over E4M3, 11, 11 and 12 for 256 of up to 250.
+constexpr int kTileCost = 2, kUnitCost = 3, kHeadsUnitCost = 5;
+// The least share of a CTA.  Of 3, 5 and 7: one request of 2048 keys takes 13.5, 13.4 and 14.3 us.
+constexpr int kLeastShare = 5;
 // Units of so many tiles go to one CTA (HEADS): 4 heads of 2, 4, 5, 6 and 8 tiles of bf16 keys take 6.7, 8.5, 9.6, 10.5
 // and 12.2 us in one piece, and 13.2, 9.8, 9.8, 10.0 and 10.1 in parts that are joined.
 constexpr int kWholeTiles = 5;
@@ -100,13 +104,14 @@ struct Cursor {
     long long base;                        // where the unit begins in the line of all units
 };
 // Of a unit of so many tiles.
-__device__ __forceinline__ int span_of(int tiles) { return tiles > 0 ? kTileCost * tiles + kUnitCost : 0; }
+template <int unit>
+__device__ __forceinline__ int span_of(int tiles) { return tiles > 0 ? kTileCost * tiles + unit : 0; }
 // Tiles of the cursor's unit that begin before position p; a unit of up to `whole` tiles is not divided and has all of
 // them at its beginning.
-template <int whole>
+template <int unit, int whole>
 __device__ __forceinline__ int tiles_before(const Cursor& c, long long p) {
     if (whole > 0 && c.tiles <= whole) return p > c.base ? c.tiles : 0;
-    const long long n = p - c.base - kUnitCost;
+    const long long n = p - c.base - unit;
     return n <= 0 ? 0 : (int)min((n + kTileCost - 1) / kTileCost, (long long)c.tiles);
 }
 // Whether the cursor's tile is one of the run.
@@ -153,7 +158,7 @@ struct Attn {
     static constexpr uint32_t kLeast2 = 0x00800080u;
     static constexpr float kPShift = F8 ? 7.0f : 0.0f;
     static constexpr int kCtasPerSm = kTileBytes > 4096 ? 1 : 2;
-    static constexpr int kWhole = HEADS ? kWholeTiles : 0;
+    static constexpr int kWhole = HEADS ? kWholeTiles : 0, kUnit = HEADS ? kHeadsUnitCost : kUnitCost;
     static constexpr int kStages = 3;
     static constexpr size_t kRing = (size_t)kAttnWarps * kStages * 2 * kTileBytes;
     static constexpr int kQBytes = ROWS * DP * (EX ? 4 : 2);         // a unit's query rows
@@ -211,7 +216,7 @@ struct Attn {
     // To the next tile; where none begins before `end`, to none of the run.
     __device__ static __forceinline__ void advance(const AttnArgs& a, int units, long long end, Cursor& c) {
         if (++c.tile < c.tiles) return;
-        c.base += span_of(c.tiles);
+        c.base += span_of<kUnit>(c.tiles);
         c.tile = 0;
         c.last = 0;
         if (c.base >= end) return;
@@ -222,7 +227,7 @@ struct Attn {
                 set_request(a, c);
             } while (c.tiles == 0);
         }
-        c.last = tiles_before<kWhole>(c, end);
+        c.last = tiles_before<kUnit, kWhole>(c, end);
     }
     // Page and slot of the key that lane `lane` looks after in the warp's tile; page -1: none.
     __device__ static __forceinline__ int2 place_of(const AttnArgs& a, const Cursor& c, int warp, int lane) {
@@ -764,7 +769,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
     pdl_allow_dependents();
     pdl_wait_primary();
 
-    // ---- the run of this CTA.  All units lie end to end, each with kUnitCost for its beginning and
+    // ---- the run of this CTA.  All units lie end to end, each with kUnit for its beginning and
     // end and kTileCost per tile; a CTA has the tiles that begin in its equal part of that.  The
     // part's first request is found with a scan of the requests in blocks of the CTA's threads.
     auto tiles_of = [&](int b) {
@@ -794,16 +799,16 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
     };
     // HEADS: there are many, and a thread has equally many in a row instead, so that one scan is enough
     const int per = HEADS ? (a.B - 1) / kAttnThreads + 1 : 1;
-    const int s0 = !HEADS && tid < a.B ? span_of(tiles_of(tid)) : 0;      // of the first block
+    const int s0 = !HEADS && tid < a.B ? span_of<K::kUnit>(tiles_of(tid)) : 0;      // of the first block
     long long mine0 = s0;
     if constexpr (HEADS)
-        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine0 += span_of(tiles_of(b));
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine0 += span_of<K::kUnit>(tiles_of(b));
     long long sum0, total;
     const long long incl0 = scan(mine0 * units, sum0);
     total = sum0;
     if (!HEADS && a.B > kAttnThreads) {
         long long mine = 0;
-        for (int b = kAttnThreads + tid; b < a.B; b += kAttnThreads) mine += span_of(tiles_of(b));
+        for (int b = kAttnThreads + tid; b < a.B; b += kAttnThreads) mine += span_of<K::kUnit>(tiles_of(b));
         long long rest;
         __syncthreads();
         scan(mine * units, rest);
@@ -824,8 +829,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
             K::finish(a, K::request_of(a, b), K::head_of(a, none, nsub), K::sub_of(none, nsub), row, c4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
         }
     }
-    // parts of at least a whole tile and unit
-    const Share share(min((long long)gridDim.x, div_u(total, kTileCost + kUnitCost)), total);
+    const Share share(min((long long)gridDim.x, div_u(total, kLeastShare)), total);
     if (blockIdx.x >= share.ctas) return;
     const long long start = share.start(blockIdx.x), end = share.start(blockIdx.x + 1);
     if constexpr (HEADS) {
@@ -835,7 +839,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
             long long next = pre;
             do {
                 pre = next;
-                next += (long long)span_of(tiles_of(++b)) * units;
+                next += (long long)span_of<K::kUnit>(tiles_of(++b)) * units;
             } while (start >= next);
             sh.found_b = b;
             sh.found_pre = pre;
@@ -852,7 +856,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
         sum += all;
         if (start < sum) break;      // the same for all threads
         b0 += kAttnThreads;
-        span = b0 + tid < a.B ? span_of(tiles_of(b0 + tid)) : 0;
+        span = b0 + tid < a.B ? span_of<K::kUnit>(tiles_of(b0 + tid)) : 0;
         __syncthreads();
         incl = scan((long long)span * units, all);
     }
@@ -860,10 +864,10 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
     Cursor c;
     c.b = sh.found_b;
     K::set_request(a, c);
-    c.unit = (int)div_u(start - sh.found_pre, span_of(c.tiles));
-    c.base = sh.found_pre + (long long)c.unit * span_of(c.tiles);
-    c.tile = tiles_before<K::kWhole>(c, start);
-    c.last = tiles_before<K::kWhole>(c, end);
+    c.unit = (int)div_u(start - sh.found_pre, span_of<K::kUnit>(c.tiles));
+    c.base = sh.found_pre + (long long)c.unit * span_of<K::kUnit>(c.tiles);
+    c.tile = tiles_before<K::kUnit, K::kWhole>(c, start);
+    c.last = tiles_before<K::kUnit, K::kWhole>(c, end);
     if (c.tile == c.tiles) {            // the part begins with the end of a unit
         --c.tile;
         K::advance(a, units, end, c);
@@ -928,8 +932,8 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
         constexpr int kStride = K::kStages * 2 * K::kTileBytes;
         K::merge(a, seg, nsub, st, lay, kStride, sh, whole ? nullptr : part_of(blockIdx.x, segment == 0));
         if (!whole) {
-            const int c_first = share.cta_of(seg.base + kUnitCost);
-            const int c_last = share.cta_of(seg.base + kUnitCost + (long long)kTileCost * (seg.tiles - 1));
+            const int c_first = share.cta_of(seg.base + K::kUnit);
+            const int c_last = share.cta_of(seg.base + K::kUnit + (long long)kTileCost * (seg.tiles - 1));
             // the unit is the first one of CTA c_first unless that also has the last tile before it (all of the
             // unit before it where that is not divided)
             long long before = seg.base - kTileCost;       // where that begins
@@ -940,7 +944,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn<DP, F8, ROWS, EX, HEADS>::k
                     --p.b;
                     K::set_request(a, p);
                 } while (p.tiles == 0);
-                if (p.tiles <= K::kWhole) before = seg.base - span_of(p.tiles);
+                if (p.tiles <= K::kWhole) before = seg.base - span_of<K::kUnit>(p.tiles);
             }
             const bool head = seg.base == 0 || share.start(c_first) > before;
             const int n = c_last - c_first + 1;
