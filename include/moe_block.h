@@ -193,7 +193,7 @@ int moe_attn_decode(const void* q, int q_dtype, int64_t q_batch_stride, int64_t 
  * ceil(n / page_size) pages, block_table int32[B, max_pages] with row stride
  * table_ld, B >= 0; status is int32[1] or NULL and receives MOE_ERR_DEVICE for a
  * length beyond the table or a page outside the cache, and is left alone
- * otherwise.
+ * otherwise.  Limits: B, max_pages and keep <= 2^30, and B * heads <= 2^30 tables.
  */
 
 /*

@@ -120,12 +120,25 @@ int attn_args(moe::AttnArgs& a, const char* who, const void* q, int q_dtype, int
     return MOE_OK;
 }
 
+// Requests, pages and tables of a call: half of the 2^31 that an index holds, so that a block's step beyond the last
+// one is an index too.
+constexpr int kMostPages = 1 << 30;
+
+// Tables of B requests of so many heads.
+int check_tables(const char* who, int B, int heads) {
+    if ((long long)B * heads <= kMostPages) return MOE_OK;
+    return api_fail(MOE_ERR_UNSUPPORTED, "%s: B=%d requests of %d heads exceed 2^30 tables (half of the 2^31 that an index holds)", who, B,
+                    heads);
+}
+
 // The requests' lengths and table, checked.
 int page_args(moe::PageArgs& a, const char* who, const int32_t* block_table, int64_t table_ld, int max_pages, int B,
               const int32_t* seq_lens, int page_size, int32_t* status) {
     if (B < 0 || max_pages < 0 || table_ld < max_pages)
         return api_fail(MOE_ERR_INVALID_ARG, "%s: need B, max_pages >= 0 and table_ld >= max_pages (%d, %d, %lld)", who, B, max_pages,
                         (long long)table_ld);
+    if (B > kMostPages || max_pages > kMostPages)
+        return api_fail(MOE_ERR_UNSUPPORTED, "%s: B=%d or max_pages=%d exceeds 2^30", who, B, max_pages);
     if (B == 0) return MOE_OK;
     if ((!block_table && max_pages > 0) || !seq_lens) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
     a.table = block_table; a.table_ld = table_ld; a.max_pages = max_pages; a.B = B; a.seq_lens = seq_lens;
@@ -251,8 +264,7 @@ int moe_attn_pages(const void* q, int q_dtype, int64_t q_batch_stride, int64_t q
                              max_pages, lens, scale, 0, softcap, out, out_dtype, out_batch_stride, out_head_stride, lse,
                              ws, ws_bytes);
     if (rc || B == 0) return rc;
-    if ((long long)B * cache->heads > INT_MAX)
-        return api_fail(MOE_ERR_UNSUPPORTED, "%s: B=%d requests of %d heads exceed 2^31 tables", who, B, cache->heads);
+    if (const int bad = check_tables(who, B, cache->heads)) return bad;
     a.B = B * cache->heads;
     return launched(moe::launch_attn_pages(a, as_stream(stream)), who);
 }
@@ -300,8 +312,8 @@ int moe_page_select(const float* scores, int B, int heads, const int32_t* block_
     moe::SelectArgs a = {};
     int rc = page_args(a, who, block_table, table_ld, max_pages, B, seq_lens, page_size, nullptr);
     if (rc || B == 0) return rc;
-    if ((long long)B * heads > INT_MAX)
-        return api_fail(MOE_ERR_UNSUPPORTED, "%s: B=%d requests of %d heads exceed 2^31 tables", who, B, heads);
+    if ((rc = check_tables(who, B, heads))) return rc;
+    if (keep > kMostPages) return api_fail(MOE_ERR_UNSUPPORTED, "%s: keep=%d exceeds 2^30", who, keep);
     if ((!scores && max_pages > 0) || !tables || !lens) return api_fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
     a.scores = scores; a.heads = heads; a.keep = keep; a.sinks = sinks; a.recent = recent; a.tables = tables; a.lens = lens;
     return launched(moe::launch_page_select(a, as_stream(stream)), who);

@@ -98,6 +98,26 @@ def test_attn_pages_refusals(B, over, code, text):
     assert text in B.lib().moe_last_error().decode()
 
 
+@pytest.mark.parametrize("over", [dict(B=2**30 + 1, heads=1), dict(pages=2**30 + 1, ld=2**31), dict(keep=2**30 + 1),
+                                  dict(B=2**28 + 1)])
+def test_select_more_than_an_index_steps_over(B, over):
+    assert _call(B.lib().moe_page_select, SELECT, over) == UNSUPPORTED
+    assert "2^30" in B.lib().moe_last_error().decode()
+
+
+@pytest.mark.parametrize("over", [dict(B=2**30 + 1), dict(pages=2**30 + 1, ld=2**31)])
+def test_bounds_and_scores_of_more_than_an_index_steps_over(B, over):
+    for fn, args in (("moe_page_bounds", BOUNDS), ("moe_page_scores", SCORES)):
+        assert _call(getattr(B.lib(), fn), dict(args, cache=_cache(B)), over) == UNSUPPORTED
+        assert "2^30" in B.lib().moe_last_error().decode()
+
+
+def test_attn_pages_of_more_tables_than_an_index_steps_over(B):
+    over = dict(B=2**28 + 1, ws_bytes=1 << 60)       # of 4 heads each
+    assert _call(B.lib().moe_attn_pages, dict(PAGES, cache=_cache(B)), over) == UNSUPPORTED
+    assert "2^30" in B.lib().moe_last_error().decode()
+
+
 def test_no_requests(B):
     """Nothing is launched, and pointers of an empty batch are not asked for."""
     L, none = B.lib(), dict(B=0, table=None, lens=None)
