@@ -205,6 +205,15 @@ def test_qk_append_many_tokens(B, T, hq, hkv, D, rot, x, A):
         assert_within(c, full, BF * full.abs() * 1.01 + 24 * U * mag * (full != 0), name)
 
 
+@pytest.mark.parametrize("T,hq,hkv,D,rot,x,A", [(700, 16, 4, 128, 128, "f32", 3), (650, 32, 8, 64, 64, "bf16", 0),
+                                                (1300, 5, 5, 16, 16, "f32", 2), (640, 6, 2, 80, 40, "bf16", 3)])
+def test_qk_append_few_heads_of_many_tokens(B, T, hq, hkv, D, rot, x, A):
+    """Heads of q that narrow blocks take, for just as many tokens as they need and more."""
+    test_qk_append_many_tokens(B, T, hq, hkv, D, rot, x, A)
+    run(B, T=T, R=200, hq=hq, hkv=hkv, D=D, rot=rot, x=x, A=A, dtype="e4m3", seed=T)
+    run(B, T=T, R=200, hq=hq, hkv=hkv, D=D, rot=rot, x=x, A=A, pad=4, seed=T)
+
+
 @pytest.mark.parametrize("bad", ["req", "table", "page_high", "page_negative", "position_cos", "axis_high", "axis_negative"])
 @pytest.mark.parametrize("rot", [128, 24])
 def test_qk_append_drops_tokens_without_a_slot(B, bad, rot):
