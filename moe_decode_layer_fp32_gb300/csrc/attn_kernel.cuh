@@ -32,7 +32,7 @@
 // Two CTAs per SM with a ring of three stages beat three with two (64 x 2048 keys: bf16 91 and 98 us,
 // E4M3 58 and 66) and tiles of 16 keys (E4M3 69).  Offsets of a page's rows counted up instead of handed from lane
 // to lane, where the page holds all keys of a warp: E4M3 56 us instead of 58, but bf16 91 instead of 89.
-// 128 x 8 heads with up to 64 pages of 64 keys each (821 MB, E4M3) 145 us, 5.7 TB/s; 16 x 8 heads with 64 pages of 32
+// 128 x 8 heads with up to 64 pages of 64 keys each (821 MB, E4M3) 145 to 150 us, 5.5 TB/s; 16 x 8 heads with 64 pages of 32
 // (117 MB, bf16) 30 us.
 //
 // Beyond 128 columns o, the scores and q do not fit the registers (124 to 960 bytes of spills) and a bf16
