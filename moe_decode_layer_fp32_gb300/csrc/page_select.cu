@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
     constexpr int kWarps = THREADS / 32, kTurn = THREADS * kSelectItems;
     __shared__ __align__(16) uint32_t list[kSelectRank];
     __shared__ uint32_t hist[256], found[4];
-    __shared__ uint32_t ends[2][kWarps];
+    // two arrays: with all the others' keys equal no barrier lies between the last read of `ends` and the counts
+    __shared__ uint32_t ends[2][kWarps], counts[2][kWarps];
     pdl_allow_dependents();
     pdl_wait_primary();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, unit = blockIdx.x, b = unit / a.heads, keep = a.keep;
@@ -640,18 +641,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) page_select_kernel(co
         }
         if (turns) __syncthreads();         // the counts before have been read
         if (lane == 0) {
-            ends[0][warp] = n_more;
-            ends[1][warp] = n_same;
+            counts[0][warp] = n_more;
+            counts[1][warp] = n_same;
         }
         __syncthreads();
         uint32_t up = above, eq = equal;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            above += ends[0][w];
-            equal += ends[1][w];
+            above += counts[0][w];
+            equal += counts[1][w];
             if (w < warp) {
-                up += ends[0][w];
-                eq += ends[1][w];
+                up += counts[0][w];
+                eq += counts[1][w];
             }
         }
         const uint32_t before = (1u << lane) - 1u;
