@@ -265,6 +265,7 @@ int moe_attn_pages(const void* q, int q_dtype, int64_t q_batch_stride, int64_t q
                              ws, ws_bytes);
     if (rc || B == 0) return rc;
     if (const int bad = check_tables(who, B, cache->heads)) return bad;
+    if (max_pages > kMostPages) return api_fail(MOE_ERR_UNSUPPORTED, "%s: max_pages=%d exceeds 2^30", who, max_pages);
     a.B = B * cache->heads;
     return launched(moe::launch_attn_pages(a, as_stream(stream)), who);
 }
