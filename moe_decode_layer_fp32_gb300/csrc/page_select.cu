@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
         };
         if (a.q_dt == MOE_DTYPE_BF16) add(std::integral_constant<int, MOE_DTYPE_BF16>());
         else add(std::integral_constant<int, MOE_DTYPE_F32>());
-        float back = a.c.k_scale ? a.c.k_scale[here.g] : 1.0f;
+        float back = a.c.k_scale ? a.c.k_scale[here.g] : 1.0f, turn_back = 1.0f;
         if constexpr (F8) {
             // a power of two brings the greatest between 2^14 and 2^15: f16 holds it, and three terms 2^-38 of it
             float most = 0.0f;
@@ -371,7 +371,10 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
             for (int e = 0; e < V; ++e) most = fmaxf(most, fabsf(q[e]));
             __syncwarp();
             const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23, up = min(268 - e, 253u);
-            back *= __uint_as_float((254 - up) << 23);
+            // on one side of 1 both, they stay two factors: their product may be no normal number, and the score one
+            const float down = __uint_as_float((254 - up) << 23);
+            if ((down < 1.0f) == (back < 1.0f)) turn_back = down;
+            else back *= down;
 #pragma unroll
             for (int v = 0; v < V; ++v) q[v] *= __uint_as_float(up << 23);
         }
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kScoreThreads, (Scores<F8, JC>::kBlocksPerSm))
                 const float first = c0[u % 2 * 2] + c1[u % 2 * 2], second = c0[u % 2 * 2 + 1] + c1[u % 2 * 2 + 1];
                 const float found = first + (second + __shfl_down_sync(0xffffffffu, first, 1));
                 const int at = u * 8 + lane / 4, known = __shfl_sync(0xffffffffu, had, at);
-                if (lane % 4 == 0 && known != INT_MIN) out[here.n * kBatch + at] = known < 0 ? -CUDART_INF_F : found * back;
+                if (lane % 4 == 0 && known != INT_MIN) out[here.n * kBatch + at] = known < 0 ? -CUDART_INF_F : (F8 ? found * turn_back : found) * back;
             }
         }
     } while (next_head(here));
