@@ -134,6 +134,40 @@ def test_attn_pages_and_decode_in_turn(B, group, q, dtype):
         lists.attend(lens[:, :1].expand(-1, 2).contiguous(), dense=True, what=f"mix {i}")
 
 
+@pytest.mark.parametrize("group", [4, 17])
+@pytest.mark.parametrize("q,dtype", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "e4m3"), ("f32", "e4m3")])
+def test_attn_pages_what_lies_behind_a_list(B, group, q, dtype):
+    """NaN in the slots behind a list's last key, and no page behind its last one: neither is read."""
+    g = gen(60)
+    page, hkv, D = 16, 2, 64
+    lens = torch.tensor([[1, 17], [16, 0], [1000, 333], [63, 64]], **INT)
+    width = 70
+    pages = 1 + int(((lens + page - 1) // page).sum())
+    k, v, ks, vs, cache = make_cache(B, g, pages, page, hkv, D, dtype)
+    qt = normal(g, 4, hkv * group, D, dtype=DT[q])
+    tables, at = torch.full((4, hkv, width), -7, **INT), 0
+    for b in range(4):
+        for h in range(hkv):
+            n = int(lens[b, h])
+            need = -(-n // page)
+            tables[b, h, :need] = torch.arange(at, at + need, **INT)
+            at += need
+    ws, runs = B.new_attn_workspace(4, hkv * group, hkv, D), []
+    for spoil in (False, True):
+        if spoil:
+            for b in range(4):
+                for h in range(hkv):
+                    n = int(lens[b, h])
+                    last = int(tables[b, h, (n - 1) // page]) if n else pages - 1
+                    for c in (k, v):
+                        bits(c)[last, (n - 1) % page + 1 if n else 0:] = 0x7F if dtype == "e4m3" else 0x7FC0
+        out = torch.full_like(qt, 9.0)
+        B.moe_attn_pages(qt, cache, tables, lens, 0.125, out, ws)
+        runs.append(out)
+    assert torch.isfinite(runs[0].float()).all() and torch.equal(bits(runs[0]), bits(runs[1]))
+    assert (runs[1][1, group:] == 0).all() and B.moe_read_status(ws)[0] == 0
+
+
 # ------------------------------------------------------------------------ repeats
 
 PARTS = ("q", "out", "tables", "kept", "bounds", "k", "v", "scores")
