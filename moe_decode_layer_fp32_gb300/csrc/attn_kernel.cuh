@@ -60,13 +60,22 @@ constexpr int kJoinGroup = 16;
 // What a tile and the beginning and end of a unit cost.  Unit costs of 1, 3, 5 and 8: 204, 137, 136, 136 us
 // for 128 ragged bf16 requests in order of length, 134, 92, 94, 98 for E4M3 with a cap, 10.2, 10.1, 10.8,
 // 12.0 for one request of 777 keys.
-// HEADS: a unit has a length and a table row of its own; unit costs of 3, 5 and 6: 58, 52 and 51 us for 1024 ragged
-// lists of up to 1000 bf16 keys, 154, 145 and 146 for 1024 of up to 4096 over E4M3, 11, 11 and 12 for 256 of up to 250.
+// HEADS: a unit has a length and a table row of its own; unit costs of 3, 5 and 6, one after another on one GPU: 58, 52 and
+// 50 us for 1024 ragged lists of up to 1000 bf16 keys, 154, 145 and 145 for 1024 of up to 4096 over E4M3 (145 to 150 with 5, from
+// one GPU to another), 10.8, 10.6 and 11.7 for 256 of up to 250.
 constexpr int kTileCost = 2, kUnitCost = 3, kHeadsUnitCost = 5;
 // The least share of a CTA.  Of 3, 5 and 7: one request of 2048 keys takes 13.5, 13.4 and 14.3 us.
 constexpr int kLeastShare = 5;
-// Units of so many tiles go to one CTA (HEADS): 4 heads of 2, 4, 5, 6 and 8 tiles of bf16 keys take 6.7, 8.5, 9.6, 10.5
-// and 12.2 us in one piece, and 13.2, 9.8, 9.8, 10.0 and 10.1 in parts that are joined.
+// Units of so many tiles go to one CTA (HEADS).  4 heads of 2, 3, 4 and 5 tiles in one piece, and in parts that are joined
+// (with a unit cost of 5), in us:
+//   bf16 keys, D 128   6.9, 7.9, 8.8, 9.7     8.4, 7.7, 10.1, 10.1
+//   E4M3, D 128        7.6, 8.9, 9.9, 11.0    9.0, 8.7, 11.1, 11.3
+//   bf16, D 64         6.3, 7.1, 8.1, 9.0     7.2, 7.1, 8.7, 8.7    (over E4M3 within 0.3 of it)
+//   bf16, D 256        9.6, 10.9, 12.4, 13.9  12.3, 10.9, 14.9, 14.9    (over E4M3 within 0.3)
+//   bf16, fp32 q       7.2, 8.4, 9.4, 10.6    8.7, 8.4, 10.6, 10.7    (E4M3 0.7 to 1 more)
+//   bf16, D 256, fp32  14.8, 18.6, 22.7, 27.0 16.1, 18.6, 22.6, 22.4
+// 1024 ragged lists of up to 250 keys of 128: bf16 28 and 29, E4M3 25 and 28; of up to 1000: 52 and 50, 45 and 42.5; of 256
+// with fp32 q over bf16 140 and 135, 297 and 296.  So it gains on short lists, and costs up to 8 % where all are near the limit.
 constexpr int kWholeTiles = 5;
 // The fast tanh is off by 2^-22 of the cap: up to 256, 2^-14 of a weight, where a bf16 output is rounded to
 // 2^-9.  Larger caps take the kernel of fp32 outputs, with tanhf (64 x 2048 keys, bf16 91 and 94 us, E4M3 60

@@ -11,8 +11,8 @@
 // of cos, sin comes from the row of its pair's axis: single words copied into one row, which is read like any other.
 //
 // Measured, 12345 tokens of 56 + 8 + 8 heads of 128, bf16 into E4M3, half of each head rotated by three axes (430 MB):
-// 77 us, 5.6 TB/s (with one axis 76; the append without norms 67). The instructions bound it, at 0.57 a clock and
-// scheduler. One head at a time 86 us, the append's kernel with plain multiplications 104; at 102 registers
+// 77 us, 5.6 TB/s (with one axis 76; the append without norms 67). Latency bounds it: at 16 warps per SM the schedulers issue
+// at 57 % of the clocks and wait for instructions with a fixed latency and for shuffles and shared memory otherwise. One head at a time 86 us, the append's kernel with plain multiplications 104; at 102 registers
 // instead of 117 (5 blocks per SM instead of 4) 89. 12345 tokens of 32 + 8 + 8 heads: of 64 34 us (blocks of 128 threads
 // 46 before, and 43 of 64), of 80 62 (5 of 8 threads have an item; 6 heads of 5 threads to a warp, with sums one
 // thread after another, 64), of 80 with 40 rotated, in vectors of 4, 67 (an element at a time 240).
@@ -399,7 +399,9 @@ cudaError_t launch_as(const QkAppendArgs& a, cudaStream_t s) {
 
 // Blocks of 64 threads where 128 would take all heads of q in one turn, and tokens are more than blocks of 128 at once:
 // half the instructions that every warp spends on a token as such.  12345, 2000, 800 and 600 tokens of 16 + 4 + 4 heads of 64
-// in bf16 28.6, 8.1, 5.5 and 5.5 us with 64 threads, 43.5, 10.2, 6.4 and 4.7 with 128; a token 4.5 and 4.0.
+// in bf16 28.6, 8.1, 5.5 and 5.5 us with 64 threads, 43.5, 10.2, 6.4 and 4.7 with 128; a token 4.5 and 4.0.  2000 tokens, bf16, with 64
+// and 128: 32 heads of 64 9.0 and 10.8, 16 of 80 9.7 and 11.8, of 128 4 heads 8.6 and 11.4, 16 9.7 and 12.1, 8 of 256 11.0 and 12.5; fp32: 16
+// of 64 8.9 and 10.6, 8 of 128 9.8 and 11.8, 16 of 80 12.8 and 13.3, of 128 15.2 and 15.1, 8 of 256 15.6 and 15.5, but 32 of 64 14.4 and 13.2.
 template <bool BF, int VEC>
 cudaError_t launch(const QkAppendArgs& a, cudaStream_t s) {
     const bool narrow = a.T > 4 * device_sm_count() && a.q_heads * span_of(items_of(a.c.head_dim, a.rot, VEC)) <= 128;
